@@ -74,7 +74,7 @@ typedef enum {
     MOE_ERR_HIP = 4
 } moe_status_t;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_MXFP4 = 3, MOE_MXFP8 = 4 } moe_dtype_t;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_MXFP4 = 3, MOE_MXFP8 = 4, MOE_I8 = 5 } moe_dtype_t;
 
 typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score_t;
 
@@ -279,6 +279,88 @@ moe_status_t moe_layer_noalloc(const void* x, int32_t x_dt, int32_t T, int32_t H
                                void* out, int32_t out_dt, int32_t y_dt,
                                int32_t* topk_ids_out, float* topk_w_out, int32_t* counts_out,
                                void* stream);
+
+/* ---- dense gated FFN -------------------------------------------------------
+ * The FFN block of a layer without a router (the first layers of a DeepSeek
+ * model, or the always-on shared expert by itself), with its gradients:
+ *     g = x W_gate, u = x W_up, h = silu(g) * u, y = h W_down
+ * x: [T][H] MOE_BF16; bank: n = 1, dt MOE_BF16, H and I positive multiples of
+ * 8 (the multiple of 128 that routed banks need does not apply here); y: [T][H]
+ * MOE_BF16 or MOE_F32.  h is rounded to bf16 (nearest even) between the two
+ * products; all sums are fp32.  gu: optional (NULL to skip) fp32 [T][2 I], row
+ * t holding g[t][0..I) then u[t][0..I): what the backward pass needs of the
+ * forward pass.  All tensors 16-byte aligned. */
+moe_status_t moe_ffn(const void* x, int32_t x_dt, int32_t T, const moe_experts_t* bank, void* y, int32_t y_dt,
+                     float* gu, void* ws, size_t ws_bytes, void* stream);
+/* 0 for invalid sizes and for T = 0. */
+size_t moe_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
+
+/* Gradients of moe_ffn for the output gradient dy [T][H], with
+ * s = 1 / (1 + exp(-g)):
+ *     dh = dy W_down^T,  dg = dh u s (1 + g (1 - s)),  du = dh g s
+ *     dx = dg W_gate^T + du W_up^T,  dW_gate = x^T dg,  dW_up = x^T du,  dW_down = h^T dy
+ * dy, x, and every output are of type dt (MOE_BF16); the weight gradients are
+ * stored like the weights ([I][H], [I][H], [H][I]) and are written, not added
+ * to.  Each output may be NULL (not computed).  gu: what moe_ffn wrote for the
+ * same x and bank, or NULL to compute it again (the workspace then also holds
+ * it: has_gu = 0 in the size query).  dg, du and h are rounded to bf16 before
+ * the next product.  T = 0 writes zero weight gradients. */
+moe_status_t moe_ffn_backward(const void* dy, const void* x, int32_t dt, int32_t T, const moe_experts_t* bank,
+                              const float* gu, void* dx, void* dw_gate, void* dw_up, void* dw_down, void* ws,
+                              size_t ws_bytes, void* stream);
+size_t moe_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I, int32_t has_gu);
+
+/* ---- norm before and after a block, with gate and residual scale -----------
+ * The step between two blocks of a layer, one kernel:
+ *     n[t] = y[t] * post_w / sqrt(mean(y[t]^2) + eps)      (n = y when post_w is NULL)
+ *     r[t] = res_scale * res[t] + gate[t / gate_div] * n[t] (res NULL: 0; gate NULL: 1)
+ *     x[t] = r[t] * pre_w / sqrt(mean(r[t]^2) + eps)       (pre_w NULL: 1)
+ * y: [T][H] of y_dt (the block's output), res and r_out: [T][H] of r_dt (the
+ * residual stream; r_out may be res itself), x_out: [T][H] of x_dt (the next
+ * block's input), each of MOE_F32 or MOE_BF16; x_dt may also be MOE_I8: codes
+ * quantised per row by the rule of moe_quant_i8 with the scales in x_scale [T].
+ * post_w, pre_w: [H], gate: [ceil(T / gate_div)][H], all of w_dt (MOE_F32 or
+ * MOE_BF16).  gate_div = T gives one gate for all tokens, a sequence length one
+ * per sequence, 1 one per token.  r_out or x_out may be NULL (not written, but
+ * not both).  x is formed from r before r is rounded to r_dt.  fp32
+ * arithmetic; 1 <= H <= 16384, any alignment to the element (16 bytes and H a
+ * multiple of 8 are faster). */
+moe_status_t moe_norm(const void* y, int32_t y_dt, const void* res, int32_t r_dt, int32_t T, int32_t H,
+                      const void* post_w, const void* gate, int32_t gate_div, const void* pre_w, int32_t w_dt,
+                      float res_scale, float eps, void* r_out, void* x_out, int32_t x_dt, float* x_scale,
+                      void* stream);
+
+/* Gradients of moe_norm.  dx: gradient of x (x_dt), dr: gradient of r from
+ * elsewhere (r_dt); either may be NULL (0), not both.  y: as given to moe_norm
+ * (may be NULL when post_w and gate are), r: what it wrote to r_out (may be NULL
+ * when dx is): the gradient of x is taken at this stored r.  Outputs, each
+ * optional (NULL): dy (y_dt), dres (r_dt; may be dr itself), and fp32 sums over
+ * the tokens dpost_w [H], dgate [ceil(T / gate_div)][H], dpre_w [H].  T = 0
+ * writes zero dpost_w and dpre_w.  gate_div in the size query: 0 without a gate. */
+moe_status_t moe_norm_backward(const void* dx, int32_t x_dt, const void* dr, const void* y, int32_t y_dt,
+                               const void* r, int32_t r_dt, int32_t T, int32_t H, const void* post_w,
+                               const void* gate, int32_t gate_div, const void* pre_w, int32_t w_dt, float res_scale,
+                               float eps, void* dy, void* dres, float* dpost_w, float* dgate, float* dpre_w, void* ws,
+                               size_t ws_bytes, void* stream);
+size_t moe_norm_backward_workspace_size(int32_t T, int32_t H, int32_t gate_div);
+
+/* ---- int8 product with a scale per token and per output channel ------------
+ * moe_quant_i8, per row: scale = max|v| / 127 (1 where that is 0), code =
+ * round-to-nearest-even(v / scale), both IEEE fp32 divisions, codes in
+ * [-127, 127].  x: [rows][cols] MOE_F32 or MOE_BF16, cols % 16 == 0. */
+moe_status_t moe_quant_i8(const void* x, int32_t x_dt, int32_t rows, int32_t cols, int8_t* q, float* scale,
+                          void* stream);
+
+/* out[t][n] = (sum_k q[t][k] * w[n][k]) * (q_scale[t] * w_scale[n]) + bias[n]
+ * q: [T][K] codes with q_scale [T] (of moe_quant_i8, or of moe_norm with int8
+ * x); w: [N][K] int8 with one scale per output channel w_scale [N]; bias: fp32
+ * [N] or NULL; out: [T][N] MOE_F32 or MOE_BF16.  The sum is exact (int32); it
+ * is rounded to fp32 once, then scaled.  K % 16 == 0, K <= 131071; any N. */
+moe_status_t moe_linear_i8(const int8_t* q, const float* q_scale, int32_t T, int32_t K, const int8_t* w,
+                           const float* w_scale, const float* bias, int32_t N, void* out, int32_t out_dt, void* ws,
+                           size_t ws_bytes, void* stream);
+/* May be 0 (no workspace needed: ws may be NULL). */
+size_t moe_linear_i8_workspace_size(int32_t T, int32_t K, int32_t N);
 
 /* Name of a status code; text of the calling thread's last error ("" if none). */
 const char* moe_status_string(int32_t status);

@@ -7,7 +7,8 @@ first use and a missing library is an error (there is no fallback path).
 
 Entry points mirror the C ABI: route, permute, quant_e4m3_1x128,
 quant_mxfp8, grouped_ffn, combine, layer, layer_noalloc (plus
-workspace-size queries).
+workspace-size queries), and around the layer: ffn, ffn_backward, norm,
+norm_backward, quant_i8, linear_i8.
 """
 from __future__ import annotations
 
@@ -22,16 +23,19 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MOE_GFX950_LIB") or os.path.join(HERE, "libmoe_gfx950.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
-F32, BF16, E4M3, MXFP4, MXFP8 = 0, 1, 2, 3, 4
+F32, BF16, E4M3, MXFP4, MXFP8, I8 = 0, 1, 2, 3, 4, 5
 SOFTMAX, SIGMOID = 0, 1
 
-DT = {"f32": F32, "bf16": BF16, "e4m3": E4M3, "mxfp4": MXFP4, "mxfp8": MXFP8}
+DT = {"f32": F32, "bf16": BF16, "e4m3": E4M3, "mxfp4": MXFP4, "mxfp8": MXFP8, "i8": I8}
 SCORE = {"softmax": SOFTMAX, "sigmoid": SIGMOID}
 
 EXPORTS = [
     "moe_route", "moe_route_workspace_size", "moe_permute", "moe_permute_workspace_size",
     "moe_quant_e4m3_1x128", "moe_quant_mxfp8", "moe_grouped_ffn", "moe_grouped_ffn_workspace_size",
     "moe_combine", "moe_layer", "moe_layer_workspace_size", "moe_layer_noalloc", "moe_mx_pack_scales",
+    "moe_ffn", "moe_ffn_workspace_size", "moe_ffn_backward", "moe_ffn_backward_workspace_size",
+    "moe_norm", "moe_norm_backward", "moe_norm_backward_workspace_size",
+    "moe_quant_i8", "moe_linear_i8", "moe_linear_i8_workspace_size",
     "moe_status_string", "moe_last_error",
 ]
 
@@ -50,7 +54,7 @@ class ExpertsT(ctypes.Structure):
 
 
 _lib = None
-_P, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_P, _I32, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -78,6 +82,17 @@ def lib() -> ctypes.CDLL:
             "moe_layer_noalloc": ([_P, _I32, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.POINTER(ExpertsT),
                                    ctypes.POINTER(ExpertsT), _P, _I32, _I32, _P, _P, _P, _P], _I32),
             "moe_mx_pack_scales": ([ctypes.POINTER(ExpertsT), _P, _P, _P], _I32),
+            "moe_ffn": ([_P, _I32, _I32, ctypes.POINTER(ExpertsT), _P, _I32, _P, _P, _SZ, _P], _I32),
+            "moe_ffn_workspace_size": ([_I32] * 3, _SZ),
+            "moe_ffn_backward": ([_P, _P, _I32, _I32, ctypes.POINTER(ExpertsT), _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+            "moe_ffn_backward_workspace_size": ([_I32] * 4, _SZ),
+            "moe_norm": ([_P, _I32, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _I32, _F32, _F32, _P, _P, _I32, _P, _P], _I32),
+            "moe_norm_backward": ([_P, _I32, _P, _P, _I32, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _I32, _F32, _F32,
+                                   _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+            "moe_norm_backward_workspace_size": ([_I32] * 3, _SZ),
+            "moe_quant_i8": ([_P, _I32, _I32, _I32, _P, _P, _P], _I32),
+            "moe_linear_i8": ([_P, _P, _I32, _I32, _P, _P, _P, _I32, _P, _I32, _P, _SZ, _P], _I32),
+            "moe_linear_i8_workspace_size": ([_I32] * 3, _SZ),
             "moe_status_string": ([_I32], ctypes.c_char_p),
             "moe_last_error": ([], ctypes.c_char_p),
         }
@@ -358,3 +373,238 @@ def layer_noalloc(x, w_router, bias, k: int, score: str, routed: Experts, shared
                                    ctypes.byref(rs), ctypes.byref(ss) if ss is not None else None,
                                    _ptr(out), _dt_of(out), y_dt, _ptr(ids), _ptr(w), _ptr(counts), _stream(stream)))
     return (out, ids, w, counts) if want_routing else out
+
+
+# ---------------------------------------------------------------- around the layer
+
+class _On:
+    """Runs a call on the tensors' device and on `stream` (default: that
+    device's current stream), so that what the call allocates belongs to the
+    stream that uses it."""
+
+    __slots__ = ("ctx", "handle")
+
+    def __init__(self, device, stream):
+        import torch
+        cur = torch.cuda.current_stream(device)
+        if stream is None:
+            stream = cur
+        elif stream.device != device:
+            raise ValueError(f"stream of {stream.device} with tensors on {device}")
+        here = torch.cuda.current_device() == device.index and stream == cur
+        self.ctx = None if here else torch.cuda.stream(stream)
+        self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            return self.ctx.__exit__(*exc)
+
+
+def _tensors(device, **ts):
+    """Checks (name -> (tensor or None, shape, dtypes)): on the device,
+    contiguous, of the shape and of one of the dtypes."""
+    for name, (t, shape, dtypes) in ts.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+
+
+def _matrix(name, t):
+    """(rows, columns, device) of a 2-d device tensor."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a 2-d tensor on a GPU, got {tuple(t.shape)} on {t.device}")
+    return t.shape[0], t.shape[1], t.device
+
+
+def _scratch(ws, need, device):
+    if ws is None:
+        return _workspace(need, device)
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, expected {device}")
+    return ws
+
+
+def _nbytes(ws) -> int:
+    return ws.numel() * ws.element_size()
+
+
+def _dense_bank(bank: Experts, H: int, device):
+    import torch
+    bf = (torch.bfloat16,)
+    if bank.w_gate.dim() != 3:
+        raise ValueError("bank: weights are [1][I][H] and [1][H][I]")
+    I = bank.w_gate.shape[1]
+    _tensors(device, w_gate=(bank.w_gate, (1, I, H), bf), w_up=(bank.w_up, (1, I, H), bf),
+             w_down=(bank.w_down, (1, H, I), bf))
+    return bank.struct(), I
+
+
+def ffn(x, bank: Experts, *, want_gu: bool = False, y_dtype=None, out=None, gu=None, ws=None, stream=None):
+    """The dense gated FFN block (moe_ffn) with a bf16 bank of n = 1.  Returns
+    y [T][H], or (y, gu) with want_gu: gu fp32 [T][2 I], what ffn_backward needs."""
+    import torch
+    T, H, dev = _matrix("x", x)
+    st, I = _dense_bank(bank, H, dev)
+    y_dtype = out.dtype if out is not None else (y_dtype or torch.bfloat16)
+    f32 = (torch.float32,)
+    _tensors(dev, x=(x, (T, H), (torch.bfloat16,)), out=(out, (T, H), (torch.bfloat16, torch.float32)),
+             gu=(gu, (T, 2 * I), f32))
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty((T, H), dtype=y_dtype, device=dev)
+        if gu is None and want_gu:
+            gu = torch.empty((T, 2 * I), dtype=torch.float32, device=dev)
+        ws = _scratch(ws, lib().moe_ffn_workspace_size(T, H, I), dev)
+        _check(lib().moe_ffn(_ptr(x), BF16, T, ctypes.byref(st), _ptr(out), _dt_of(out), _ptr(gu), _ptr(ws),
+                             _nbytes(ws), s))
+    return (out, gu) if want_gu else out
+
+
+def ffn_backward(dy, x, bank: Experts, gu=None, *, need=("dx", "dw_gate", "dw_up", "dw_down"), ws=None, stream=None):
+    """Gradients of ffn (moe_ffn_backward): (dx [T][H], dw_gate, dw_up [1][I][H],
+    dw_down [1][H][I]), None for those not in `need`.  gu: what ffn returned
+    (None: computed again)."""
+    import torch
+    T, H, dev = _matrix("x", x)
+    st, I = _dense_bank(bank, H, dev)
+    bf = (torch.bfloat16,)
+    _tensors(dev, x=(x, (T, H), bf), dy=(dy, (T, H), bf), gu=(gu, (T, 2 * I), (torch.float32,)))
+    shapes = {"dx": (T, H), "dw_gate": (1, I, H), "dw_up": (1, I, H), "dw_down": (1, H, I)}
+    if not set(need) <= set(shapes):
+        raise ValueError(f"need: {need}")
+    with _On(dev, stream) as s:
+        o = {k: torch.empty(shapes[k], dtype=torch.bfloat16, device=dev) if k in need else None for k in shapes}
+        ws = _scratch(ws, lib().moe_ffn_backward_workspace_size(T, H, I, int(gu is not None)), dev)
+        _check(lib().moe_ffn_backward(_ptr(dy), _ptr(x), BF16, T, ctypes.byref(st), _ptr(gu), _ptr(o["dx"]),
+                                      _ptr(o["dw_gate"]), _ptr(o["dw_up"]), _ptr(o["dw_down"]), _ptr(ws), _nbytes(ws),
+                                      s))
+    return tuple(o.values())
+
+
+def _norm_params(T, H, dev, post_w, gate, gate_div, pre_w):
+    """(rows of the gate, weight dtype code) after the checks."""
+    import torch
+    fl = (torch.float32, torch.bfloat16)
+    dtypes = {t.dtype for t in (post_w, gate, pre_w) if t is not None}
+    if len(dtypes) > 1:
+        raise TypeError(f"post_w, gate and pre_w have different dtypes: {dtypes}")
+    if gate is not None and gate_div < 1:
+        raise ValueError(f"gate_div={gate_div}")
+    G = -(-T // gate_div) if gate is not None else 0
+    _tensors(dev, post_w=(post_w, (H,), fl), gate=(gate, (G, H), fl), pre_w=(pre_w, (H,), fl))
+    return G, BF16 if dtypes == {torch.bfloat16} else F32
+
+
+def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: float = 1.0, pre_w=None,
+         eps: float = 1e-6, r_dtype=None, x_dtype=None, want_r: bool = True, want_x: bool = True, r=None, x=None,
+         stream=None):
+    """The norm step between two blocks (moe_norm).  Returns (r, x); with
+    x_dtype torch.int8 x is the pair (codes [T][H], scales [T]).  r_dtype
+    defaults to res's dtype (y's without res), x_dtype to y's.  r, x: optional
+    output tensors; r may be res itself."""
+    import torch
+    T, H, dev = _matrix("y", y)
+    fl = (torch.float32, torch.bfloat16)
+    _, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
+    r_dtype = res.dtype if res is not None else r.dtype if r is not None else (r_dtype or y.dtype)
+    q, scale = x if isinstance(x, tuple) else (x, None)
+    x_dtype = q.dtype if q is not None else (x_dtype or y.dtype)
+    if r_dtype not in fl or x_dtype not in fl + (torch.int8,):
+        raise TypeError(f"norm: r {r_dtype}, x {x_dtype}")
+    i8 = x_dtype == torch.int8
+    _tensors(dev, y=(y, (T, H), fl), res=(res, (T, H), (r_dtype,)), r=(r, (T, H), (r_dtype,)),
+             x=(q, (T, H), (x_dtype,)), x_scale=(scale, (T,), (torch.float32,)))
+    with _On(dev, stream) as s:
+        if r is None and want_r:
+            r = torch.empty((T, H), dtype=r_dtype, device=dev)
+        if q is None and want_x:
+            q = torch.empty((T, H), dtype=x_dtype, device=dev)
+        if q is not None and i8 and scale is None:
+            scale = torch.empty((T,), dtype=torch.float32, device=dev)
+        _check(lib().moe_norm(_ptr(y), _dt_of(y), _ptr(res), F32 if r_dtype == torch.float32 else BF16, T, H,
+                              _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w), w_dt, res_scale, eps, _ptr(r), _ptr(q),
+                              I8 if i8 else F32 if x_dtype == torch.float32 else BF16, _ptr(scale), s))
+    return r, ((q, scale) if i8 and q is not None else q)
+
+
+def norm_backward(dx, dr, y, r, *, post_w=None, gate=None, gate_div: int = 1, res_scale: float = 1.0, pre_w=None,
+                  eps: float = 1e-6, need=("dy", "dres", "dpost_w", "dgate", "dpre_w"), ws=None, stream=None):
+    """Gradients of norm (moe_norm_backward) as a dict with the keys dy (y's
+    dtype), dres (r's), dpost_w, dgate and dpre_w (fp32); None for those that
+    are not in `need` or have no input.  dx or dr may be None (zero), r with dx
+    None, y without post_w and gate (dy then has dr's dtype, or r's)."""
+    import torch
+    some = next((t for t in (y, r, dx, dr) if t is not None), None)
+    if some is None:
+        raise ValueError("norm_backward: no tensors")
+    T, H, dev = _matrix("y, r, dx or dr", some)
+    fl = (torch.float32, torch.bfloat16)
+    G, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
+    r_dtype = r.dtype if r is not None else dr.dtype if dr is not None else torch.float32
+    y_dtype = y.dtype if y is not None else r_dtype
+    _tensors(dev, dx=(dx, (T, H), fl), dr=(dr, (T, H), (r_dtype,)), y=(y, (T, H), fl), r=(r, (T, H), fl))
+    if r_dtype not in fl:
+        raise TypeError(f"norm_backward: dr has dtype {r_dtype}")
+    what = {"dy": ((T, H), y_dtype, True), "dres": ((T, H), r_dtype, True), "dpost_w": ((H,), torch.float32, post_w is not None),
+            "dgate": ((G, H), torch.float32, gate is not None), "dpre_w": ((H,), torch.float32, pre_w is not None and dx is not None)}
+    if not set(need) <= set(what):
+        raise ValueError(f"need: {need}")
+    with _On(dev, stream) as s:
+        o = {k: torch.empty(shape, dtype=dt, device=dev) if k in need and has else None
+             for k, (shape, dt, has) in what.items()}
+        ws = _scratch(ws, lib().moe_norm_backward_workspace_size(T, H, gate_div if gate is not None else 0), dev)
+        _check(lib().moe_norm_backward(
+            _ptr(dx), F32 if dx is None else _dt_of(dx), _ptr(dr), _ptr(y), F32 if y_dtype == torch.float32 else BF16,
+            _ptr(r), F32 if r_dtype == torch.float32 else BF16, T, H, _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w),
+            w_dt, res_scale, eps, _ptr(o["dy"]), _ptr(o["dres"]), _ptr(o["dpost_w"]), _ptr(o["dgate"]),
+            _ptr(o["dpre_w"]), _ptr(ws), _nbytes(ws), s))
+    return o
+
+
+def quant_i8(x, stream=None, out=None):
+    """int8 codes [rows][cols], scales [rows] fp32 (moe_quant_i8)."""
+    import torch
+    rows, cols, dev = _matrix("x", x)
+    q, scale = out if out is not None else (None, None)
+    _tensors(dev, x=(x, (rows, cols), (torch.float32, torch.bfloat16)), q=(q, (rows, cols), (torch.int8,)),
+             scale=(scale, (rows,), (torch.float32,)))
+    with _On(dev, stream) as s:
+        if out is None:
+            q = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+            scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+        _check(lib().moe_quant_i8(_ptr(x), _dt_of(x), rows, cols, _ptr(q), _ptr(scale), s))
+    return q, scale
+
+
+def linear_i8(q, q_scale, w, w_scale, bias=None, *, out_dtype=None, out=None, ws=None, stream=None):
+    """out [T][N] = (q w^T) * q_scale[:, None] * w_scale + bias (moe_linear_i8):
+    q [T][K] and w [N][K] int8, q_scale [T], w_scale and bias [N] fp32."""
+    import torch
+    T, K, dev = _matrix("q", q)
+    N = _matrix("w", w)[0]
+    f32, i8 = (torch.float32,), (torch.int8,)
+    out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"linear_i8: out {out_dtype}")
+    _tensors(dev, q=(q, (T, K), i8), w=(w, (N, K), i8), q_scale=(q_scale, (T,), f32), w_scale=(w_scale, (N,), f32),
+             bias=(bias, (N,), f32), out=(out, (T, N), (out_dtype,)))
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty((T, N), dtype=out_dtype, device=dev)
+        need = lib().moe_linear_i8_workspace_size(T, K, N)
+        ws = _scratch(ws, need, dev) if need or ws is not None else None
+        _check(lib().moe_linear_i8(_ptr(q), _ptr(q_scale), T, K, _ptr(w), _ptr(w_scale), _ptr(bias), N, _ptr(out),
+                                   _dt_of(out), _ptr(ws), 0 if ws is None else _nbytes(ws), s))
+    return out

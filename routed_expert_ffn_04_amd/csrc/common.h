@@ -63,6 +63,18 @@ __device__ __forceinline__ uint32_t mx_e8m0_for_e4m3(float amax) {
 // this factor are the block's elements before rounding.
 __device__ __forceinline__ float mx_inv_scale(uint32_t E) { return __uint_as_float((254u - E) << 23); }
 
+// ---- int8 with one fp32 scale per row -----------------------------------------
+// scale = amax / 127 (1 where that is 0), code = rne(v / scale), both IEEE fp32
+// divisions.  The clamp only acts where the scale is subnormal and has lost
+// bits.
+__device__ __forceinline__ float i8_scale(float amax) {
+    const float s = amax / 127.0f;
+    return s > 0.0f ? s : 1.0f;
+}
+__device__ __forceinline__ uint32_t i8_code(float v, float scale) {
+    return (uint32_t)(int)fminf(fmaxf(rintf(v / scale), -127.0f), 127.0f) & 0xFFu;
+}
+
 // ---- wave64 helpers ----------------------------------------------------------
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 

@@ -1,0 +1,174 @@
+// Dense gated FFN block and its gradients in bf16 (moe_ffn, moe_ffn_backward).
+//   g = x Wg^T, u = x Wu^T, h = silu(g) u, y = h Wd^T      (weights output-major)
+// One kernel forms both projections of the same columns side by side, applies
+// the activation and the product in its epilogue and writes h once.
+// Backward, with the fp32 g and u that the forward pass saved:
+//   dh = dy Wd        -> epilogue: dg = dh u s (1 + g (1 - s)), du = dh g s, h again   (s = sigmoid(g))
+//   dx = [dg du] [Wg; Wu]       one product over 2 I
+//   [dWg; dWu] = [dg du]^T x    one product with 2 I rows
+//   dWd = dy^T h
+// The matrices are met in the layout they have: products over the contiguous
+// index read rows, the others read columns (gemm_tile.h), nothing is
+// transposed in memory.
+//
+// Roundings: h, dg and du go into the next product as bf16 (nearest even), as
+// the matrix cores take them; g and u are kept in fp32, because rounding them
+// as well would put a second error of the same size on dx and the gate and up
+// gradients.  All sums are fp32.
+#include "gemm_plan.h"
+
+namespace moe {
+using namespace gemm;
+
+namespace {
+
+constexpr int kKE = kStage / 2;
+
+Operand rows(const void* p, long ld, int n, const void* p2 = nullptr) {
+    return Operand{(const uint8_t*)p, (const uint8_t*)p2, (size_t)ld * 2, n, 0};
+}
+Operand cols(const void* p, long ld, int n, const void* p2 = nullptr, int split = 0) {
+    return Operand{(const uint8_t*)p, (const uint8_t*)p2, (size_t)ld * 2, n, split};
+}
+
+Args base(int M, int N, int K) {
+    Args G{};
+    G.M = M; G.N = N; G.K = K; G.vec = 1; G.msplit = M;
+    return G;
+}
+
+struct Plans {
+    Plan gateup, down, dh, dx, dwgu, dw1, dwd;
+};
+Plans plans(int T, int H, int I) {
+    return Plans{plan_tiles(T, 2L * I, H, kKE), plan_tiles(T, H, I, kKE),  plan_tiles(T, I, H, kKE),
+                 plan_tiles(T, H, 2 * I, kKE),  plan_tiles(2L * I, H, T, kKE), plan_tiles(I, H, T, kKE),
+                 plan_tiles(H, I, T, kKE)};
+}
+
+size_t max2(size_t a, size_t b) { return a > b ? a : b; }
+
+struct Ws {
+    size_t gu, dgu, h, part, total;
+};
+Ws forward_ws(int T, int H, int I) {
+    const Plans p = plans(T, H, I);
+    Ws w{};
+    w.h = 0;
+    w.part = align256((size_t)T * I * 2);
+    w.total = w.part + max2(part_bytes(p.gateup, T, 2L * I), part_bytes(p.down, T, H));
+    return w;
+}
+Ws backward_ws(int T, int H, int I, int has_gu) {
+    const Plans p = plans(T, H, I);
+    Ws w{};
+    size_t o = 0;
+    w.gu = o;
+    o += has_gu ? 0 : align256((size_t)T * I * 8);
+    w.dgu = o;
+    o += align256((size_t)T * I * 4);
+    w.h = o;
+    o += align256((size_t)T * I * 2);
+    w.part = o;
+    size_t most = max2(part_bytes(p.dh, T, I), part_bytes(p.dx, T, H));
+    most = max2(most, max2(part_bytes(p.dwgu, 2L * I, H), part_bytes(p.dw1, I, H)));
+    most = max2(most, part_bytes(p.dwd, H, I));
+    if (!has_gu) most = max2(most, part_bytes(p.gateup, T, 2L * I));
+    w.total = o + most;
+    return w;
+}
+
+hipError_t gateup(const FfnProblem& p, void* h, float* gu, float* part, hipStream_t s) {
+    Args G = base(p.T, p.I, p.H);
+    G.A = rows(p.x, p.H, p.T);
+    G.B = rows(p.wg, p.H, p.I, p.wu);
+    G.out = h;
+    G.out2 = gu;
+    return run<kBf16, kRow, kRow, kEpiGateUp>(G, plans(p.T, p.H, p.I).gateup, part, s);
+}
+
+// rows of zeros (the weight gradients of no tokens)
+hipError_t zero_rows(void* out, int M, int N, hipStream_t s) {
+    Args G = base(M, N, 0);
+    G.out = out;
+    return launch_reduce<kEpiOut>(G, nullptr, 0, s);
+}
+
+}  // namespace
+
+size_t ffn_ws_bytes(int T, int H, int I) { return T > 0 ? forward_ws(T, H, I).total : 0; }
+size_t ffn_backward_ws_bytes(int T, int H, int I, int has_gu) { return T > 0 ? backward_ws(T, H, I, has_gu).total : 0; }
+
+hipError_t launch_ffn(const FfnProblem& p, void* ws, hipStream_t s) {
+    const Ws w = forward_ws(p.T, p.H, p.I);
+    uint8_t* b = (uint8_t*)ws;
+    float* part = (float*)(b + w.part);
+    hipError_t e = gateup(p, b + w.h, p.gu, part, s);
+    if (e != hipSuccess) return e;
+    Args G = base(p.T, p.H, p.I);
+    G.A = rows(b + w.h, p.I, p.T);
+    G.B = rows(p.wd, p.I, p.H);
+    G.out = p.y;
+    G.out_f32 = p.y_f32;
+    return run<kBf16, kRow, kRow, kEpiOut>(G, plans(p.T, p.H, p.I).down, part, s);
+}
+
+hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    if (p.T == 0) {
+        if (p.dwg) e = zero_rows(p.dwg, p.I, p.H, s);
+        if (e == hipSuccess && p.dwu) e = zero_rows(p.dwu, p.I, p.H, s);
+        if (e == hipSuccess && p.dwd) e = zero_rows(p.dwd, p.H, p.I, s);
+        return e;
+    }
+    const int T = p.T, H = p.H, I = p.I;
+    const Plans pl = plans(T, H, I);
+    const Ws w = backward_ws(T, H, I, p.gu_in != nullptr);
+    uint8_t* b = (uint8_t*)ws;
+    float* part = (float*)(b + w.part);
+    uint8_t* dgu = b + w.dgu;
+    uint8_t* h = b + w.h;
+    const float* gu = p.gu_in;
+    if (!gu) {
+        gu = (const float*)(b + w.gu);
+        e = gateup(p, h, (float*)(b + w.gu), part, s);
+        if (e != hipSuccess) return e;
+    }
+    {
+        Args G = base(T, I, H);
+        G.A = rows(p.dy, H, T);
+        G.B = cols(p.wd, I, I);
+        G.gu = gu;
+        G.out = dgu;
+        G.out2 = h;
+        e = run<kBf16, kRow, kCol, kEpiGrad>(G, pl.dh, part, s);
+    }
+    if (e == hipSuccess && p.dx) {
+        Args G = base(T, H, 2 * I);
+        G.A = rows(dgu, 2L * I, T);
+        G.B = cols(p.wg, H, H, p.wu, I);
+        G.out = p.dx;
+        e = run<kBf16, kRow, kCol, kEpiOut>(G, pl.dx, part, s);
+    }
+    if (e == hipSuccess && (p.dwg || p.dwu)) {
+        // both at once; one alone: its half of dgu
+        const bool both = p.dwg && p.dwu;
+        Args G = base(both ? 2 * I : I, H, T);
+        G.A = cols(dgu + (p.dwg ? 0 : (size_t)I * 2), 2L * I, both ? 2 * I : I);
+        G.B = cols(p.x, H, H);
+        G.out = p.dwg ? p.dwg : p.dwu;
+        G.out2 = p.dwu;
+        G.msplit = I;
+        e = run<kBf16, kCol, kCol, kEpiOut>(G, both ? pl.dwgu : pl.dw1, part, s);
+    }
+    if (e == hipSuccess && p.dwd) {
+        Args G = base(H, I, T);
+        G.A = cols(p.dy, H, H);
+        G.B = cols(h, I, I);
+        G.out = p.dwd;
+        e = run<kBf16, kCol, kCol, kEpiOut>(G, pl.dwd, part, s);
+    }
+    return e;
+}
+
+}  // namespace moe

@@ -1,0 +1,483 @@
+// Tiled matrix product C[m][n] = sum_k A(m, k) B(n, k) on the matrix cores,
+// with the epilogues of the dense gated FFN (forward and backward) and of the
+// int8 product.  Used by ffn.hip (bf16) and linear_i8.hip (int8).
+//
+// Operands.  Each of A and B is stored either with k contiguous (kRow: row m
+// holds its k values, like an activation or an output-major weight) or with m
+// contiguous (kCol: row k holds the values of all m, which is how the gradient
+// products meet the same matrices).  Neither is ever transposed in memory: a
+// kCol tile goes into LDS as it is and its fragments are read with the
+// transposing LDS read (ds_read_b64_tr_b16: 16 lanes read 4 k-rows x 16
+// columns, each lane gets the 4 k values of one column).
+//
+// Tile.  BM x BN outputs per workgroup, 64 bytes of k per stage (32 bf16 or 64
+// int8), a ring of kRing stages in LDS filled by direct global->LDS 16-byte
+// loads.  256 x 256 tiles: 8 waves (2 x 4) of 128 x 64, 128 KiB of LDS, one
+// workgroup per CU.  128 x 128 tiles: 4 waves (2 x 2) of 64 x 64, 64 KiB, two
+// workgroups per CU.  Each wave's product is formed transposed (the n side is
+// the MFMA row operand), so a lane holds four consecutive n of one row m.
+//
+// One barrier per stage, placed between the stage's two k-steps: before it
+// the wave has read the second step's fragments (so after it nobody reads this
+// stage's buffer any more and stage s + kRing is loaded into it) and waited for
+// its share of stage s + 1 (so after it the first fragments of the next stage
+// are read while the second step multiplies).  kRing - 1 stages stay in flight
+// across every barrier.
+//
+// Bounds.  m and n past the end re-read the last row (last 16-byte chunk) and
+// are never stored; k past the end (the ragged last stage, and the stages that
+// the ring prefetches past it) reads a zero page, so it adds exactly nothing.
+#pragma once
+#include "common.h"
+#include "gffn_common.h"
+
+namespace moe {
+namespace gemm {
+
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(16))) int i32x16;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+enum { kRow = 0, kCol = 1 };
+enum { kBf16 = 0, kI8 = 1 };
+
+// what becomes of the accumulators
+enum Epi {
+    kEpiGateUp = 0,    // B tile: BN/2 gate columns then BN/2 up columns; h = silu(g) u (bf16), optionally g and u (fp32)
+    kEpiOut = 1,       // bf16 or fp32 matrix
+    kEpiGrad = 2,      // acc = dh; with the saved g, u: dg, du (bf16 [M][2 N]) and h (bf16 [M][N])
+    kEpiPart = 3,      // 32-bit accumulators of one k-split, [split][M][N] (gate/up: [split][M][2 I])
+    kEpiI8 = 4,        // acc * x_scale[m] * w_scale[n] + bias[n], bf16 or fp32
+};
+
+constexpr int kStage = 64;   // bytes of k per stage
+constexpr int kRing = 4;
+
+struct Operand {
+    const uint8_t* p;    // element (row 0, k 0)
+    const uint8_t* p2;   // gate/up B: the up matrix; kCol with split < K: rows k >= split, as if they began at row split
+    size_t ld;           // bytes from row to row (kRow: of m; kCol: of k)
+    int n;               // rows m (kRow), columns m (kCol); gate/up B: I
+    int split;           // kCol: first k that p2 holds
+};
+
+struct Args {
+    Operand A, B;
+    int M, N, K;         // N: output columns (gate/up: I)
+    int mt, nt;          // tiles
+    int splits, kspan;   // k-splits; k elements per split (a multiple of the stage)
+    int vec;             // rows of the outputs allow 16-byte accesses
+    void* out;           // kEpiOut / kEpiI8 / kEpiPart: [M][N]; kEpiGateUp: h; kEpiGrad: dgu
+    void* out2;          // kEpiOut: rows m >= msplit, as if they began at row msplit; kEpiGrad: h; kEpiGateUp: gu (or null)
+    int msplit;
+    int out_f32;
+    const float* gu;     // kEpiGrad: saved pre-activations [M][2 N]
+    const float* xs; const float* ws; const float* bias;   // kEpiI8
+};
+
+// k past the end reads this.
+static __device__ __align__(16) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+// Offset of 16-byte chunk c of row r in a kRow tile (64-byte rows).  Four rows
+// span the 64 banks; the key shifts every next four rows by one chunk, so the
+// 16 rows of a quarter-wave read all 16 bank groups.
+__device__ __forceinline__ int row_off(int r, int c) { return r * 64 + ((c ^ ((r >> 2) & 3)) << 4); }
+
+template <int BMN, int LAYOUT>
+struct Tile {
+    static constexpr int kBytes = BMN * kStage;              // bytes per stage in either layout
+    static constexpr int kRowBytes = LAYOUT == kRow ? 64 : BMN * 2;
+};
+
+// One direct load of a lane: its 16 bytes of every stage.
+struct Lane {
+    const uint8_t* p;    // next stage's address
+    int left;            // k elements from this chunk's first k to the end of the split (<= 0: zeros)
+};
+
+template <int N>
+__device__ __forceinline__ void barrier_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (0 << 8) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Orders a wave's LDS accesses for its other lanes (they complete in order in
+// hardware; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_sync() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// MFMA operands of NB 32-row blocks x one k-step (16 bf16 or 32 int8), 16
+// bytes a lane: lane l holds row l % 32, k values [8 (l / 32), +8) (int8: 16).
+// kRow: one 16-byte LDS read.  kCol: two transposing reads of 4 k-rows each;
+// the key (k-row mod 4) << 2 on the chunk index puts the four rows that a
+// half-wave reads into four different 64-byte quarters of the banks.
+template <int LAYOUT, int BMN, int NB>
+struct Frag {
+    int off[2][NB];   // kRow: by k-step; kCol: off[0] only
+    __device__ __forceinline__ Frag(int block0, int block_step, int lane) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int block = block0 + b * block_step;
+            if constexpr (LAYOUT == kRow) {
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) off[ks][b] = row_off(block * 32 + lane % 32, 2 * ks + lane / 32);
+            } else {
+                const int g = lane / 16, j = lane % 16;
+                const int chunk = (4 * block + 2 * (g & 1) + (j % 4) / 2) ^ ((j / 4) << 2);
+                off[0][b] = ((g >> 1) * 8 + j / 4) * (BMN * 2) + chunk * 16 + (j & 1) * 8;
+            }
+        }
+    }
+    __device__ __forceinline__ i32x4 read(const uint8_t* tile, int b, int ks) const {
+        if constexpr (LAYOUT == kRow) {
+            return *(const i32x4*)(tile + off[ks][b]);
+        } else {
+            const uint8_t* q = tile + off[0][b] + ks * 16 * (BMN * 2);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)q);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(q + 4 * (BMN * 2)));
+            return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+};
+
+template <int E> struct Acc;
+template <> struct Acc<kBf16> {
+    typedef f32x16 type;
+    __device__ static type mma(i32x4 a, i32x4 b, type c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    }
+};
+template <> struct Acc<kI8> {
+    typedef i32x16 type;
+    __device__ static type mma(i32x4 a, i32x4 b, type c) { return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0); }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return f32_to_bf16_bits(a) | (f32_to_bf16_bits(b) << 16); }
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+// The gated activation's derivative: with s = sigmoid(g), a = g s, h = a u:
+//   dg = dh u s (1 + g (1 - s)),  du = dh a.
+// 1 - s is formed as e^-g / (1 + e^-g) so that it keeps its digits for large g;
+// for g so negative that e^-g overflows, s = 0 makes every term exactly 0.
+__device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float& dg, float& du, float& h) {
+    const float e = __expf(-g);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    const float a = g * s;
+    const float t = s == 0.0f ? 0.0f : a * (e * s);
+    dg = dh * u * (s + t);
+    du = dh * a;
+    h = a * u;
+}
+
+// Eight consecutive outputs (m, n .. n + 7) of a kEpiOut / kEpiI8 / kEpiPart matrix.
+__device__ __forceinline__ void store8(const Args& G, uint8_t* row, int n, const float (&v)[8], bool f32) {
+    if (G.vec && n + 8 <= G.N) {
+        if (f32) {
+            float4* o = (float4*)((float*)row + n);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *(uint4*)((uint16_t*)row + n) = pack8(v);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (n + e < G.N) {
+                if (f32) ((float*)row)[n + e] = v[e];
+                else ((uint16_t*)row)[n + e] = (uint16_t)f32_to_bf16_bits(v[e]);
+            }
+    }
+}
+
+// Workgroup b of `total` -> tile.  Workgroups go to the eight dies round robin,
+// each die with an L2 of its own: every die takes one contiguous run of tiles,
+// ordered in bands of 8 m-tiles with n outermost, so the 32 tiles that a die
+// works on together form a block of about 8 x 4 and share their operands in L2.
+__device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& tm, int& tn, int& split) {
+    const int x = b % kXcds, j = b / kXcds;
+    const int base = total / kXcds, extra = total % kXcds;
+    int t = x * base + min(x, extra) + j;
+    const int per = mt * nt;
+    split = t / per;
+    t -= split * per;
+    const int band = t / (8 * nt);
+    const int rows = min(8, mt - band * 8);
+    t -= band * 8 * nt;
+    tn = t / rows;
+    tm = band * 8 + t % rows;
+}
+
+template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN>
+__global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(Args G) {
+    constexpr int kThreads = BM * 2;
+    constexpr int EB = E == kI8 ? 1 : 2;
+    constexpr int KE = kStage / EB;                            // k elements per stage
+    constexpr int WN = BN / 64, WM = (kThreads / 64) / WN;     // waves along n and m
+    constexpr int IB = BM / WM / 32, JB = 2;                   // 32 x 32 blocks of a wave
+    constexpr int LDA = BM * 4 / kThreads, LDB = BN * 4 / kThreads;   // direct loads per lane and stage
+    constexpr int kLoads = LDA + LDB;
+    constexpr int kStageBytes = (BM + BN) * kStage;
+    constexpr int kTileN = GU ? BN / 2 : BN;                   // output columns per tile
+    static_assert(E == kBf16 || (LA == kRow && LB == kRow), "the transposing read is for 16-bit elements");
+    static_assert(WM * WN * 64 == kThreads && WM * IB * 32 == BM, "waves cover the tile");
+
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int wm = wave / WN, wn = wave % WN;
+
+    int tm, tn, split;
+    tile_of(blockIdx.x, G.mt, G.nt, gridDim.x, tm, tn, split);
+    const int m0 = tm * BM, n0 = tn * kTileN;
+    const int k0 = split * G.kspan;
+    const int kn = min(G.K - k0, G.kspan);                     // k elements of this split
+    const int nst = (kn + KE - 1) / KE;
+
+    // ---- the lane's share of the direct loads
+    Lane ld[kLoads];
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+        const bool isA = q < LDA;
+        const Operand& O = isA ? G.A : G.B;
+        const int r0 = isA ? m0 : n0;
+        const int qq = isA ? q : q - LDA;
+        const int at = (wave * (isA ? LDA : LDB) + qq) * 64 + lane;    // 16-byte slot in the operand's tile
+        if ((isA ? LA : LB) == kRow) {
+            const int r = at / 4, c = (at % 4) ^ ((r >> 2) & 3);
+            const uint8_t* p = O.p;
+            int row = r0 + r;
+            if (GU && !isA && r >= BN / 2) {
+                p = O.p2;
+                row -= BN / 2;
+            }
+            row = min(row, O.n - 1);
+            ld[q].p = p + (size_t)row * O.ld + (size_t)k0 * EB + c * 16;
+            ld[q].left = kn - c * (16 / EB);
+        } else {
+            constexpr int kA = BM * 2 / 16, kB = BN * 2 / 16;          // slots per k row
+            const int per = isA ? kA : kB;
+            const int r = at / per, c = (at % per) ^ ((r & 3) << 2);
+            const int col = min(r0 + c * 8, O.n - 8);
+            ld[q].p = O.p + (size_t)(k0 + r) * O.ld + (size_t)col * 2;
+            ld[q].left = kn - r;
+        }
+    }
+    // kCol B of two matrices (k < split in p, the rest in p2): the distance
+    // between the second's rows and where the first's would continue
+    const ptrdiff_t second = LB == kCol && G.B.p2 ? G.B.p2 - (G.B.p + (size_t)G.B.split * G.B.ld) : 0;
+    const int second_at = LB == kCol && G.B.p2 ? kn - (G.B.split - k0) : 0;   // `left` at or below this: second matrix
+
+    auto issue = [&](uint8_t* buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const bool isA = q < LDA;
+            const uint8_t* p = ld[q].p;
+            if (LB == kCol && !isA) p += ld[q].left <= second_at ? second : 0;
+            p = ld[q].left > 0 ? p : (const uint8_t*)kZeros;
+            uint8_t* dst = buf + (isA ? 0 : BM * kStage) + (wave * (isA ? LDA : LDB) + (isA ? q : q - LDA)) * 1024;
+            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)dst, 16, 0, 0);
+            ld[q].p += (isA ? LA : LB) == kRow ? (size_t)kStage : (size_t)KE * (isA ? G.A.ld : G.B.ld);
+            ld[q].left -= KE;
+        }
+    };
+
+    typename Acc<E>::type acc[IB][JB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) acc[i][j] = typename Acc<E>::type{};
+
+    const Frag<LA, BM, IB> fa(wm * IB, 1, lane);
+    const Frag<LB, BN, JB> fb(GU ? wn : wn * JB, GU ? BN / 64 : 1, lane);
+    i32x4 a0[IB], a1[IB], b0[JB], b1[JB];
+    auto read = [&](const uint8_t* buf, int ks, i32x4(&a)[IB], i32x4(&b)[JB]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < JB; ++j) b[j] = fb.read(buf + BM * kStage, j, ks);
+#pragma unroll
+        for (int i = 0; i < IB; ++i) a[i] = fa.read(buf, i, ks);
+    };
+    auto mma = [&](const i32x4(&a)[IB], const i32x4(&b)[JB], int i0, int i1) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i)
+#pragma unroll
+            for (int j = 0; j < JB; ++j) acc[i][j] = Acc<E>::mma(b[j], a[i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // One turn of the ring.  wr: the stage that everybody has read to its end;
+    // rd: the next one.  The second k-step's reads go out in the middle of the
+    // first one's products (the compiler waits for every LDS read in flight
+    // before an MFMA that needs one).  The restrict qualifiers state that the
+    // loads into wr do not touch rd; without them the compiler waits for every
+    // direct load before a transposing read.
+    auto turn = [&](uint8_t* __restrict__ wr, const uint8_t* __restrict__ rd) __attribute__((always_inline)) {
+        issue(wr);
+        read(rd, 0, a0, b0);
+        __builtin_amdgcn_sched_barrier(0);
+        mma(a1, b1, 0, IB);
+        mma(a0, b0, 0, IB / 2);
+        read(rd, 1, a1, b1);
+        __builtin_amdgcn_sched_barrier(0);
+        mma(a0, b0, IB / 2, IB);
+    };
+    auto start = [&](uint8_t* __restrict__ wr, const uint8_t* __restrict__ rd) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s + 1 < kRing; ++s) issue(wr + s * kStageBytes);
+        barrier_vm<(kRing - 1) * kLoads>();
+        read(rd, 0, a0, b0);
+        read(rd, 1, a1, b1);
+        mma(a0, b0, 0, IB);
+    };
+
+    issue(smem);
+    start(smem + kStageBytes, smem);
+    for (int s = 0; s + 1 < nst; ++s) {
+        barrier_vm<(kRing - 2) * kLoads>();
+        turn(smem + (s % kRing) * kStageBytes, smem + ((s + 1) % kRing) * kStageBytes);
+    }
+    mma(a1, b1, 0, IB);
+    // the prefetched (zero) stages land before the ring becomes the epilogue's scratch
+    barrier_vm<0>();
+
+    // ---- epilogue.  acc[i][j][v]: m = 32 i + l % 32, n = 32 j + 8 (v / 4) + 4 (l / 32) + v % 4 of the
+    // wave's part.  One 32-row block at a time passes through the wave's own piece of LDS (rows of 64 words
+    // and a 16-byte pad, free of bank conflicts both ways), so that global accesses are whole row pieces.
+    constexpr int RS = 64 * 4 + 16;
+    uint8_t* piece = smem + wave * 32 * RS;
+    const int nw = n0 + wn * (GU ? 32 : 64);
+#pragma unroll
+    for (int i = 0; i < IB; ++i) {
+        const int mb = m0 + wm * IB * 32 + i * 32;
+        if (mb >= G.M) break;
+        wave_sync();
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const auto v = acc[i][j][4 * q + e];   // a value: a bit_cast of the element itself takes element 0
+                    w[e] = __builtin_bit_cast(uint32_t, v);
+                }
+                *(uint4*)(piece + (lane % 32) * RS + (32 * j + 8 * q + 4 * (lane / 32)) * 4) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        wave_sync();
+        auto words = [&](int row, int n, float(&v)[8]) {
+            const float4 lo = *(const float4*)(piece + row * RS + n * 4);
+            const float4 hi = *(const float4*)(piece + row * RS + n * 4 + 16);
+            v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w; v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        };
+        if constexpr (GU) {
+            // 32 gate and 32 up columns: 4 lanes a row, 16 rows a pass
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int row = p * 16 + lane / 4, c = (lane % 4) * 8;
+                const int m = mb + row, n = nw + c;
+                float g[8], u[8], h[8];
+                words(row, c, g);
+                words(row, 32 + c, u);
+                if (m < G.M && n < G.N) {
+                    if constexpr (EPI == kEpiPart) {
+                        float* o = (float*)G.out + ((size_t)split * G.M + m) * (2 * (size_t)G.N) + n;
+                        *(float4*)o = make_float4(g[0], g[1], g[2], g[3]);
+                        *(float4*)(o + 4) = make_float4(g[4], g[5], g[6], g[7]);
+                        o += G.N;
+                        *(float4*)o = make_float4(u[0], u[1], u[2], u[3]);
+                        *(float4*)(o + 4) = make_float4(u[4], u[5], u[6], u[7]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[e] = silu_mul(g[e], u[e]);
+                        *(uint4*)((uint16_t*)G.out + (size_t)m * G.N + n) = pack8(h);
+                        if (G.out2) {
+                            float* o = (float*)G.out2 + (size_t)m * (2 * (size_t)G.N) + n;
+                            *(float4*)o = make_float4(g[0], g[1], g[2], g[3]);
+                            *(float4*)(o + 4) = make_float4(g[4], g[5], g[6], g[7]);
+                            o += G.N;
+                            *(float4*)o = make_float4(u[0], u[1], u[2], u[3]);
+                            *(float4*)(o + 4) = make_float4(u[4], u[5], u[6], u[7]);
+                        }
+                    }
+                }
+            }
+        } else {
+            // 64 columns: 8 lanes a row, 8 rows a pass
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int row = p * 8 + lane / 8, c = (lane % 8) * 8;
+                const int m = mb + row, n = nw + c;
+                float v[8];
+                words(row, c, v);
+                if (m < G.M && n < G.N) {
+                    if constexpr (EPI == kEpiGrad) {
+                        const float4* gp = (const float4*)(G.gu + (size_t)m * (2 * (size_t)G.N) + n);
+                        const float4* up = (const float4*)(G.gu + (size_t)m * (2 * (size_t)G.N) + G.N + n);
+                        const float4 ga = gp[0], gb = gp[1], ua = up[0], ub = up[1];
+                        const float g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
+                        const float u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
+                        float dg[8], du[8], h[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) swiglu_grad(g[e], u[e], v[e], dg[e], du[e], h[e]);
+                        uint16_t* d = (uint16_t*)G.out + (size_t)m * (2 * (size_t)G.N) + n;
+                        *(uint4*)d = pack8(dg);
+                        *(uint4*)(d + G.N) = pack8(du);
+                        *(uint4*)((uint16_t*)G.out2 + (size_t)m * G.N + n) = pack8(h);
+                    } else if constexpr (EPI == kEpiPart) {
+                        store8(G, (uint8_t*)((float*)G.out + ((size_t)split * G.M + m) * G.N), n, v, true);
+                    } else if constexpr (EPI == kEpiI8) {
+                        const float xs = G.xs[m];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int ne = min(n + e, G.N - 1);
+                            const float s = xs * G.ws[ne];
+                            v[e] = (float)__float_as_int(v[e]) * s;
+                            if (G.bias) v[e] += G.bias[ne];
+                        }
+                        store8(G, (uint8_t*)G.out + (size_t)m * G.N * (G.out_f32 ? 4 : 2), n, v, G.out_f32);
+                    } else {
+                        const size_t row_bytes = (size_t)G.N * (G.out_f32 ? 4 : 2);
+                        uint8_t* o = m < G.msplit ? (uint8_t*)G.out + (size_t)m * row_bytes
+                                                  : (uint8_t*)G.out2 + (size_t)(m - G.msplit) * row_bytes;
+                        store8(G, o, n, v, G.out_f32);
+                    }
+                }
+            }
+        }
+    }
+}
+
+constexpr int tile_lds_bytes(int bm, int bn) { return kRing * (bm + bn) * kStage; }
+
+// Launches one tiling; mt, nt and the grid follow from the sizes in G.
+template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN>
+hipError_t launch_tiles(Args G, hipStream_t s) {
+    auto* k = tile_kernel<E, LA, LB, EPI, GU, BM, BN>;
+    constexpr int lds = tile_lds_bytes(BM, BN);
+    static DeviceCache ready;   // the LDS limit is a property of the function on each device
+    const int ok = per_device(ready, [&] {
+        return hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds) == hipSuccess ? 1 : 0;
+    });
+    if (!ok) return hipErrorInvalidValue;
+    G.mt = (G.M + BM - 1) / BM;
+    G.nt = (G.N + (GU ? BN / 2 : BN) - 1) / (GU ? BN / 2 : BN);
+    const long total = (long)G.mt * G.nt * G.splits;
+    if (total <= 0 || total > 0x7fffffffL) return hipErrorInvalidValue;
+    k<<<dim3((unsigned)total), dim3(BM * 2), lds, s>>>(G);
+    return hipGetLastError();
+}
+
+}  // namespace gemm
+}  // namespace moe

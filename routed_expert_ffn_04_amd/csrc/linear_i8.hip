@@ -1,0 +1,85 @@
+// int8 product with a scale per token and per output channel (moe_linear_i8),
+// and the per-token quantisation that feeds it (moe_quant_i8).
+//   q[t][k] = rne(x[t][k] / s_t),  s_t = amax_t / 127 (IEEE divisions; 1 where that is 0)
+//   out[t][n] = (sum_k q[t][k] w[n][k]) * (s_t * w_scale[n]) + bias[n]
+// The sum is exact in int32 (K <= 131071 keeps 128 * 128 * K below 2^31); it is
+// converted to fp32 once (nearest even) and scaled.
+#include "gemm_plan.h"
+
+namespace moe {
+using namespace gemm;
+
+namespace {
+
+// One row per workgroup of 256 threads: the row's maximum, then its codes.
+// The second reading of a row comes from L2.
+template <bool F32>
+__global__ __launch_bounds__(256) void quant_i8_kernel(const void* __restrict__ x, int cols, int8_t* __restrict__ q,
+                                                       float* __restrict__ scale) {
+    const size_t row = blockIdx.x;
+    const int tid = threadIdx.x;
+    __shared__ float part[4];
+    auto load = [&](int c, float(&v)[8]) {
+        if (F32) {
+            const float4* p = (const float4*)((const float*)x + row * cols + c);
+            const float4 a = p[0], b = p[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 u = *(const uint4*)((const uint16_t*)x + row * cols + c);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
+                v[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
+            }
+        }
+    };
+    float amax = 0.0f;
+    for (int c = tid * 8; c < cols; c += 2048) {
+        float v[8];
+        load(c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m, kWave));
+    if (tid % 64 == 0) part[tid / 64] = amax;
+    __syncthreads();
+    amax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    const float s = i8_scale(amax);
+    if (tid == 0) scale[row] = s;
+    for (int c = tid * 8; c < cols; c += 2048) {
+        float v[8];
+        load(c, v);
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e / 4] |= i8_code(v[e], s) << (8 * (e % 4));
+        *(uint2*)(q + row * cols + c) = make_uint2(w[0], w[1]);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_quant_i8(const void* x, int x_f32, int rows, int cols, int8_t* q, float* scale, hipStream_t s) {
+    if (x_f32) quant_i8_kernel<true><<<dim3(rows), dim3(256), 0, s>>>(x, cols, q, scale);
+    else quant_i8_kernel<false><<<dim3(rows), dim3(256), 0, s>>>(x, cols, q, scale);
+    return hipGetLastError();
+}
+
+size_t linear_i8_ws_bytes(int T, int K, int N) {
+    return T > 0 ? part_bytes(plan_tiles(T, N, K, kStage), T, N) : 0;
+}
+
+hipError_t launch_linear_i8(const LinearI8Problem& p, void* ws, hipStream_t s) {
+    Args G{};
+    G.M = p.T; G.N = p.N; G.K = p.K; G.msplit = p.T;
+    G.A = Operand{(const uint8_t*)p.q, nullptr, (size_t)p.K, p.T, 0};
+    G.B = Operand{(const uint8_t*)p.w, nullptr, (size_t)p.K, p.N, 0};
+    G.xs = p.xs; G.ws = p.ws; G.bias = p.bias;
+    G.out = p.out;
+    G.out_f32 = p.out_f32;
+    G.vec = p.N % (p.out_f32 ? 4 : 8) == 0 && ((uintptr_t)p.out & 15u) == 0;
+    return run<kI8, kRow, kRow, kEpiI8>(G, plan_tiles(p.T, p.N, p.K, kStage), (float*)ws, s);
+}
+
+}  // namespace moe
