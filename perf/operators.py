@@ -249,7 +249,7 @@ def run(state):
             bank = _bank(moe, s)
             y, gu = moe.ffn(s["x"], bank, want_gu=True)
             dx, dwg, dwu, dwd = moe.ffn_backward(s["dy"], s["x"], bank, gu)
-            return {"y": y, "dx": dx, "dw_gate": dwg, "dw_up": dwu, "dw_down": dwd}
+            return {"y": y, "dx": dx, "dw_gate": dwg[0], "dw_up": dwu[0], "dw_down": dwd[0]}
         return _plain_ffn_train(s)
     if op == "norm":
         if own:
