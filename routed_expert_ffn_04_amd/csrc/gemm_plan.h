@@ -23,7 +23,7 @@ inline Plan plan_tiles(long M, long mma_cols, int K, int stage_elems) {
         const long tiles = ((M + 127) / 128) * ((mma_cols + 127) / 128);
         if (tiles < 256) {
             const int want = (int)((511 + tiles) / tiles);
-            const int most = stages / 8 > 1 ? stages / 8 : 1;
+            const int most = stages / 4 > 1 ? stages / 4 : 1;
             const int s = want < most ? want : most;
             const int span = (stages + s - 1) / s;
             p.kspan = span * stage_elems;

@@ -10,19 +10,22 @@
 // transposing LDS read (ds_read_b64_tr_b16: 16 lanes read 4 k-rows x 16
 // columns, each lane gets the 4 k values of one column).
 //
-// Tile.  BM x BN outputs per workgroup, 64 bytes of k per stage (32 bf16 or 64
-// int8), a ring of kRing stages in LDS filled by direct global->LDS 16-byte
-// loads.  256 x 256 tiles: 8 waves (2 x 4) of 128 x 64, 128 KiB of LDS, one
-// workgroup per CU.  128 x 128 tiles: 4 waves (2 x 2) of 64 x 64, 64 KiB, two
-// workgroups per CU.  Each wave's product is formed transposed (the n side is
-// the MFMA row operand), so a lane holds four consecutive n of one row m.
+// Tile.  BM x BN outputs per workgroup, 128 bytes of k per stage (64 bf16 or
+// 128 int8).  LDS is a ring of five half-stages (the A part or the B part of a
+// stage) filled by direct global->LDS 16-byte loads.  256 x 256 tiles: 8 waves
+// (2 x 4) of 128 x 64, all 160 KiB of LDS, one workgroup per CU.  128 x 128
+// tiles: 4 waves (2 x 2) of 64 x 64, 80 KiB, two workgroups per CU.  Each wave's
+// product is formed transposed (the n side is the MFMA row operand), so a lane
+// holds four consecutive n of one row m.
 //
-// One barrier per stage, placed between the stage's two k-steps: before it
-// the wave has read the second step's fragments (so after it nobody reads this
-// stage's buffer any more and stage s + kRing is loaded into it) and waited for
-// its share of stage s + 1 (so after it the first fragments of the next stage
-// are read while the second step multiplies).  kRing - 1 stages stay in flight
-// across every barrier.
+// Row pieces of 128 bytes, whole cache lines: a kernel that only loads moves 32
+// KiB per CU into LDS in 0.36 us with 128-byte pieces and in 0.5 to 0.75 us
+// with 64-byte ones, and the loads are what limits a stage first.
+//
+// One barrier per stage, after the last fragments of a stage have been read
+// and before its last k-step multiplies: after it both halves of the stage are
+// free and take the B half one stage and the A half two stages ahead, which
+// leaves at least a whole stage of products for every load to land in.
 //
 // Bounds.  m and n past the end re-read the last row (last 16-byte chunk) and
 // are never stored; k past the end (the ragged last stage, and the stages that
@@ -54,8 +57,8 @@ enum Epi {
     kEpiI8 = 4,        // acc * x_scale[m] * w_scale[n] + bias[n], bf16 or fp32
 };
 
-constexpr int kStage = 64;   // bytes of k per stage
-constexpr int kRing = 4;
+constexpr int kStage = 128;  // bytes of k per stage
+constexpr int kRing = 5;     // half-stages in the ring
 
 struct Operand {
     const uint8_t* p;    // element (row 0, k 0)
@@ -82,22 +85,9 @@ struct Args {
 // k past the end reads this.
 static __device__ __align__(16) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
-// Offset of 16-byte chunk c of row r in a kRow tile (64-byte rows).  Four rows
-// span the 64 banks; the key shifts every next four rows by one chunk, so the
-// 16 rows of a quarter-wave read all 16 bank groups.
-__device__ __forceinline__ int row_off(int r, int c) { return r * 64 + ((c ^ ((r >> 2) & 3)) << 4); }
-
-template <int BMN, int LAYOUT>
-struct Tile {
-    static constexpr int kBytes = BMN * kStage;              // bytes per stage in either layout
-    static constexpr int kRowBytes = LAYOUT == kRow ? 64 : BMN * 2;
-};
-
-// One direct load of a lane: its 16 bytes of every stage.
-struct Lane {
-    const uint8_t* p;    // next stage's address
-    int left;            // k elements from this chunk's first k to the end of the split (<= 0: zeros)
-};
+// Chunk key of row r of a kRow half-stage (128-byte rows): chunk c sits at
+// position c ^ key, which spreads the fragment reads over all banks.
+__device__ __forceinline__ int row_key(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 template <int N>
 __device__ __forceinline__ void barrier_vm() {
@@ -123,26 +113,29 @@ __device__ __forceinline__ void wave_sync() {
 // half-wave reads into four different 64-byte quarters of the banks.
 template <int LAYOUT, int BMN, int NB>
 struct Frag {
-    int off[2][NB];   // kRow: by k-step; kCol: off[0] only
+    int off[LAYOUT == kRow ? 4 : NB];   // kRow: by k-step (block 0); kCol: by block (k-step 0)
+    int step;                           // kRow: bytes from block to block
     __device__ __forceinline__ Frag(int block0, int block_step, int lane) {
+        if constexpr (LAYOUT == kRow) {
+            const int r = block0 * 32 + lane % 32;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int block = block0 + b * block_step;
-            if constexpr (LAYOUT == kRow) {
+            for (int ks = 0; ks < 4; ++ks) off[ks] = r * kStage + (((2 * ks + lane / 32) ^ row_key(r)) << 4);
+            step = block_step * 32 * kStage;
+        } else {
+            step = 0;
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) off[ks][b] = row_off(block * 32 + lane % 32, 2 * ks + lane / 32);
-            } else {
+            for (int b = 0; b < NB; ++b) {
                 const int g = lane / 16, j = lane % 16;
-                const int chunk = (4 * block + 2 * (g & 1) + (j % 4) / 2) ^ ((j / 4) << 2);
-                off[0][b] = ((g >> 1) * 8 + j / 4) * (BMN * 2) + chunk * 16 + (j & 1) * 8;
+                const int chunk = (4 * (block0 + b * block_step) + 2 * (g & 1) + (j % 4) / 2) ^ ((j / 4) << 2);
+                off[b] = ((g >> 1) * 8 + j / 4) * (BMN * 2) + chunk * 16 + (j & 1) * 8;
             }
         }
     }
-    __device__ __forceinline__ i32x4 read(const uint8_t* tile, int b, int ks) const {
+    __device__ __forceinline__ i32x4 read(const uint8_t* half, int b, int ks) const {
         if constexpr (LAYOUT == kRow) {
-            return *(const i32x4*)(tile + off[ks][b]);
+            return *(const i32x4*)(half + off[ks] + b * step);
         } else {
-            const uint8_t* q = tile + off[0][b] + ks * 16 * (BMN * 2);
+            const uint8_t* q = half + off[b] + ks * 16 * (BMN * 2);
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)q);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(q + 4 * (BMN * 2)));
             return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -228,9 +221,9 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     constexpr int KE = kStage / EB;                            // k elements per stage
     constexpr int WN = BN / 64, WM = (kThreads / 64) / WN;     // waves along n and m
     constexpr int IB = BM / WM / 32, JB = 2;                   // 32 x 32 blocks of a wave
-    constexpr int LDA = BM * 4 / kThreads, LDB = BN * 4 / kThreads;   // direct loads per lane and stage
-    constexpr int kLoads = LDA + LDB;
-    constexpr int kStageBytes = (BM + BN) * kStage;
+    constexpr int LDA = BM * 8 / kThreads, LDB = BN * 8 / kThreads;   // direct loads per lane and half-stage
+    constexpr int kHalf = BM * kStage;                                // bytes of a half-stage
+    static_assert(BM == BN && LDA == 4 && LDB == 4, "square tiles");
     constexpr int kTileN = GU ? BN / 2 : BN;                   // output columns per tile
     static_assert(E == kBf16 || (LA == kRow && LB == kRow), "the transposing read is for 16-bit elements");
     static_assert(WM * WN * 64 == kThreads && WM * IB * 32 == BM, "waves cover the tile");
@@ -247,52 +240,58 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     const int kn = min(G.K - k0, G.kspan);                     // k elements of this split
     const int nst = (kn + KE - 1) / KE;
 
-    // ---- the lane's share of the direct loads
-    Lane ld[kLoads];
+    // ---- the lane's share of the direct loads: four 16-byte slots in each half-stage
+    const uint8_t* pa[LDA];
+    const uint8_t* pb[LDB];
+    auto place = [&](int layout, const Operand& O, int r0, bool gu, const uint8_t*(&p)[4]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-        const bool isA = q < LDA;
-        const Operand& O = isA ? G.A : G.B;
-        const int r0 = isA ? m0 : n0;
-        const int qq = isA ? q : q - LDA;
-        const int at = (wave * (isA ? LDA : LDB) + qq) * 64 + lane;    // 16-byte slot in the operand's tile
-        if ((isA ? LA : LB) == kRow) {
-            const int r = at / 4, c = (at % 4) ^ ((r >> 2) & 3);
-            const uint8_t* p = O.p;
-            int row = r0 + r;
-            if (GU && !isA && r >= BN / 2) {
-                p = O.p2;
-                row -= BN / 2;
+        for (int q = 0; q < 4; ++q) {
+            const int at = (wave * 4 + q) * 64 + lane;
+            if (layout == kRow) {
+                const int r = at / 8, c = (at % 8) ^ row_key(r);
+                const bool up = gu && r >= BN / 2;
+                const int row = min(r0 + r - (up ? BN / 2 : 0), O.n - 1);
+                p[q] = (up ? O.p2 : O.p) + (size_t)row * O.ld + (size_t)k0 * EB + c * 16;
+            } else {
+                constexpr int per = BM * 2 / 16;                       // slots per k row
+                const int r = at / per, c = (at % per) ^ ((r & 3) << 2);
+                p[q] = O.p + (size_t)(k0 + r) * O.ld + (size_t)min(r0 + c * 8, O.n - 8) * 2;
             }
-            row = min(row, O.n - 1);
-            ld[q].p = p + (size_t)row * O.ld + (size_t)k0 * EB + c * 16;
-            ld[q].left = kn - c * (16 / EB);
-        } else {
-            constexpr int kA = BM * 2 / 16, kB = BN * 2 / 16;          // slots per k row
-            const int per = isA ? kA : kB;
-            const int r = at / per, c = (at % per) ^ ((r & 3) << 2);
-            const int col = min(r0 + c * 8, O.n - 8);
-            ld[q].p = O.p + (size_t)(k0 + r) * O.ld + (size_t)col * 2;
-            ld[q].left = kn - r;
         }
-    }
+    };
+    place(LA, G.A, m0, false, pa);
+    place(LB, G.B, n0, GU, pb);
+    // k of a slot within its stage: kRow its chunk's first k, kCol its row
+    const int kr = ((lane % 8) ^ (lane / 8)) * (16 / EB);             // q even; q odd: the neighbouring chunk
+    const int kc = wave * 4 * (64 / (BM / 8)) + lane / (BM / 8);      // q = 0
+    auto k_of = [&](int layout, int q) __attribute__((always_inline)) {
+        return layout == kRow ? kr ^ ((q & 1) * (16 / EB)) : kc + q * (64 / (BM / 8));
+    };
     // kCol B of two matrices (k < split in p, the rest in p2): the distance
     // between the second's rows and where the first's would continue
     const ptrdiff_t second = LB == kCol && G.B.p2 ? G.B.p2 - (G.B.p + (size_t)G.B.split * G.B.ld) : 0;
-    const int second_at = LB == kCol && G.B.p2 ? kn - (G.B.split - k0) : 0;   // `left` at or below this: second matrix
+    const int turn_at = LB == kCol && G.B.p2 ? G.B.split - k0 : 0x7fffffff;   // first k of this split in the second
 
-    auto issue = [&](uint8_t* buf) __attribute__((always_inline)) {
+    int ka = 0, kb = 0;   // first k of the next half-stages to load
+    auto issueA = [&](uint8_t* half, int q0, int q1) __attribute__((always_inline)) {
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) {
-            const bool isA = q < LDA;
-            const uint8_t* p = ld[q].p;
-            if (LB == kCol && !isA) p += ld[q].left <= second_at ? second : 0;
-            p = ld[q].left > 0 ? p : (const uint8_t*)kZeros;
-            uint8_t* dst = buf + (isA ? 0 : BM * kStage) + (wave * (isA ? LDA : LDB) + (isA ? q : q - LDA)) * 1024;
-            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)dst, 16, 0, 0);
-            ld[q].p += (isA ? LA : LB) == kRow ? (size_t)kStage : (size_t)KE * (isA ? G.A.ld : G.B.ld);
-            ld[q].left -= KE;
+        for (int q = q0; q < q1; ++q) {
+            const uint8_t* p = k_of(LA, q) < kn - ka ? pa[q] : (const uint8_t*)kZeros;
+            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)(half + (wave * 4 + q) * 1024), 16, 0, 0);
+            pa[q] += LA == kRow ? (size_t)kStage : (size_t)KE * G.A.ld;
         }
+        if (q1 == LDA) ka += KE;
+    };
+    auto issueB = [&](uint8_t* half, int q0, int q1) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = q0; q < q1; ++q) {
+            const uint8_t* p = pb[q];
+            if (LB == kCol) p += k_of(LB, q) >= turn_at - kb ? second : 0;
+            p = k_of(LB, q) < kn - kb ? p : (const uint8_t*)kZeros;
+            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)(half + (wave * 4 + q) * 1024), 16, 0, 0);
+            pb[q] += LB == kRow ? (size_t)kStage : (size_t)KE * G.B.ld;
+        }
+        if (q1 == LDB) kb += KE;
     };
 
     typename Acc<E>::type acc[IB][JB];
@@ -304,11 +303,15 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     const Frag<LA, BM, IB> fa(wm * IB, 1, lane);
     const Frag<LB, BN, JB> fb(GU ? wn : wn * JB, GU ? BN / 64 : 1, lane);
     i32x4 a0[IB], a1[IB], b0[JB], b1[JB];
-    auto read = [&](const uint8_t* buf, int ks, i32x4(&a)[IB], i32x4(&b)[JB]) __attribute__((always_inline)) {
+    // Fragments of one k-step, the A blocks [i0, i1); the B blocks with the first.
+    auto read = [&](const uint8_t* ha, const uint8_t* hb, int ks, i32x4(&a)[IB], i32x4(&b)[JB], int i0, int i1)
+                    __attribute__((always_inline)) {
+        if (i0 == 0)
 #pragma unroll
-        for (int j = 0; j < JB; ++j) b[j] = fb.read(buf + BM * kStage, j, ks);
+            for (int j = 0; j < JB; ++j) b[j] = fb.read(hb, j, ks);
 #pragma unroll
-        for (int i = 0; i < IB; ++i) a[i] = fa.read(buf, i, ks);
+        for (int i = i0; i < i1; ++i) a[i] = fa.read(ha, i, ks);
+        __builtin_amdgcn_sched_barrier(0);
     };
     auto mma = [&](const i32x4(&a)[IB], const i32x4(&b)[JB], int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
@@ -317,36 +320,60 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
             for (int j = 0; j < JB; ++j) acc[i][j] = Acc<E>::mma(b[j], a[i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // One turn of the ring.  wr: the stage that everybody has read to its end;
-    // rd: the next one.  The second k-step's reads go out in the middle of the
-    // first one's products (the compiler waits for every LDS read in flight
-    // before an MFMA that needs one).  The restrict qualifiers state that the
-    // loads into wr do not touch rd; without them the compiler waits for every
-    // direct load before a transposing read.
-    auto turn = [&](uint8_t* __restrict__ wr, const uint8_t* __restrict__ rd) __attribute__((always_inline)) {
-        issue(wr);
-        read(rd, 0, a0, b0);
+    // The products of one k-step in a and b while the next step's fragments go
+    // into an and bn.  LDS reads and direct loads go out a few at a time between
+    // products: together they would fill the memory pipes' queues and hold up
+    // the products behind them.
+    constexpr int H = IB / 2;
+    auto step = [&](i32x4(&a)[IB], i32x4(&b)[JB], const uint8_t* ha, const uint8_t* hb, int ks, i32x4(&an)[IB],
+                    i32x4(&bn)[JB], auto&& load) __attribute__((always_inline)) {
+        mma(a, b, 0, H / 2);
+        read(ha, hb, ks, an, bn, 0, H);
+        mma(a, b, H / 2, H);
+        read(ha, hb, ks, an, bn, H, IB);
+        mma(a, b, H, IB - 1);
+        load();
         __builtin_amdgcn_sched_barrier(0);
-        mma(a1, b1, 0, IB);
-        mma(a0, b0, 0, IB / 2);
-        read(rd, 1, a1, b1);
-        __builtin_amdgcn_sched_barrier(0);
-        mma(a0, b0, IB / 2, IB);
+        mma(a, b, IB - 1, IB);
     };
-    auto start = [&](uint8_t* __restrict__ wr, const uint8_t* __restrict__ rd) __attribute__((always_inline)) {
-#pragma unroll
-        for (int s = 0; s + 1 < kRing; ++s) issue(wr + s * kStageBytes);
-        barrier_vm<(kRing - 1) * kLoads>();
-        read(rd, 0, a0, b0);
-        read(rd, 1, a1, b1);
-        mma(a0, b0, 0, IB);
+    // One stage from its halves rA, rB, beginning with the previous stage's
+    // last k-step; wA and wB are the halves that stage has left.  The restrict
+    // qualifiers state that the loads into wA and wB do not touch rA and rB;
+    // without them the compiler waits for every direct load before a
+    // transposing read.
+    auto turn = [&](uint8_t* __restrict__ wB, uint8_t* __restrict__ wA, const uint8_t* __restrict__ rA,
+                    const uint8_t* __restrict__ rB) __attribute__((always_inline)) {
+        step(a1, b1, rA, rB, 0, a0, b0, [&]() __attribute__((always_inline)) { issueB(wB, 0, 2); });
+        step(a0, b0, rA, rB, 1, a1, b1, [&]() __attribute__((always_inline)) { issueB(wB, 2, 4); });
+        step(a1, b1, rA, rB, 2, a0, b0, [&]() __attribute__((always_inline)) { issueA(wA, 0, 2); });
+        step(a0, b0, rA, rB, 3, a1, b1, [&]() __attribute__((always_inline)) { issueA(wA, 2, 4); });
+    };
+    auto none = []() __attribute__((always_inline)) {};
+    auto start = [&](uint8_t* __restrict__ w, const uint8_t* __restrict__ rA, const uint8_t* __restrict__ rB)
+                     __attribute__((always_inline)) {
+        issueA(w, 0, 4);
+        issueB(w + kHalf, 0, 4);
+        issueA(w + 2 * kHalf, 0, 4);
+        barrier_vm<12>();   // the first two halves
+        read(rA, rB, 0, a0, b0, 0, IB);
+        step(a0, b0, rA, rB, 1, a1, b1, none);
+        step(a1, b1, rA, rB, 2, a0, b0, none);
+        step(a0, b0, rA, rB, 3, a1, b1, none);
     };
 
-    issue(smem);
-    start(smem + kStageBytes, smem);
-    for (int s = 0; s + 1 < nst; ++s) {
-        barrier_vm<(kRing - 2) * kLoads>();
-        turn(smem + (s % kRing) * kStageBytes, smem + ((s + 1) % kRing) * kStageBytes);
+    issueA(smem, 0, 4);
+    issueB(smem + kHalf, 0, 4);
+    start(smem + 2 * kHalf, smem, smem + kHalf);
+    int u = 0;   // slot of the current stage's A half; the ring's order is A B A B A ...
+    auto slot = [&](int i) __attribute__((always_inline)) { return smem + (u + i >= kRing ? u + i - kRing : u + i) * kHalf; };
+    for (int s = 1; s < nst; ++s) {
+        barrier_vm<4>();   // everything but the A half of stage s + 1 has landed
+        uint8_t* wB = slot(0);
+        uint8_t* wA = slot(1);
+        const uint8_t* rA = slot(2);
+        const uint8_t* rB = slot(3);
+        u = u + 2 >= kRing ? u + 2 - kRing : u + 2;
+        turn(wB, wA, rA, rB);
     }
     mma(a1, b1, 0, IB);
     // the prefetched (zero) stages land before the ring becomes the epilogue's scratch
@@ -459,13 +486,13 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     }
 }
 
-constexpr int tile_lds_bytes(int bm, int bn) { return kRing * (bm + bn) * kStage; }
+constexpr int tile_lds_bytes(int bm) { return kRing * bm * kStage; }
 
 // Launches one tiling; mt, nt and the grid follow from the sizes in G.
 template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN>
 hipError_t launch_tiles(Args G, hipStream_t s) {
     auto* k = tile_kernel<E, LA, LB, EPI, GU, BM, BN>;
-    constexpr int lds = tile_lds_bytes(BM, BN);
+    constexpr int lds = tile_lds_bytes(BM);
     static DeviceCache ready;   // the LDS limit is a property of the function on each device
     const int ok = per_device(ready, [&] {
         return hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds) == hipSuccess ? 1 : 0;
