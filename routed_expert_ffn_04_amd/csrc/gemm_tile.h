@@ -23,7 +23,7 @@
 // with 64-byte ones, and the loads are what limits a stage first.
 //
 // One barrier per stage, after the last fragments of a stage have been read
-// and before its last k-step multiplies: after it both halves of the stage are
+// and before its last quarter multiplies: after it both halves of the stage are
 // free and take the B half one stage and the A half two stages ahead, which
 // leaves at least a whole stage of products for every load to land in.
 //
@@ -37,9 +37,6 @@
 namespace moe {
 namespace gemm {
 
-typedef __attribute__((ext_vector_type(16))) float f32x16;
-typedef __attribute__((ext_vector_type(16))) int i32x16;
-typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(8))) short s16x8;
 typedef __attribute__((address_space(3))) void lds_void;
@@ -88,6 +85,8 @@ static __device__ __align__(16) const uint32_t kZeros[4] = {0, 0, 0, 0};
 // Chunk key of row r of a kRow half-stage (128-byte rows): chunk c sits at
 // position c ^ key, which spreads the fragment reads over all banks.
 __device__ __forceinline__ int row_key(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// The same of row k of a kCol half-stage (2 BM-byte rows).
+__device__ __forceinline__ int col_key(int r) { return ((r & 3) << 2) | (((r >> 3) & 1) << 1); }
 
 template <int N>
 __device__ __forceinline__ void barrier_vm() {
@@ -106,36 +105,31 @@ __device__ __forceinline__ void wave_sync() {
     asm volatile("" ::: "memory");
 }
 
-// MFMA operands of NB 32-row blocks x one k-step (16 bf16 or 32 int8), 16
-// bytes a lane: lane l holds row l % 32, k values [8 (l / 32), +8) (int8: 16).
-// kRow: one 16-byte LDS read.  kCol: two transposing reads of 4 k-rows each;
-// the key (k-row mod 4) << 2 on the chunk index puts the four rows that a
-// half-wave reads into four different 64-byte quarters of the banks.
-template <int LAYOUT, int BMN, int NB>
+// MFMA operands of the 16-row blocks of a wave, one k-step (32 bf16 or 64 int8),
+// 16 bytes a lane: lane l holds row l % 16, k values [8 (l / 16), +8) (int8: 16).
+// kRow: one 16-byte LDS read.  kCol: two transposing reads of 4 k-rows each; a
+// half-wave reads 32 bytes of eight k-rows, which col_key puts into eight
+// different parts of the banks.
+template <int LAYOUT, int BMN>
 struct Frag {
-    int off[LAYOUT == kRow ? 4 : NB];   // kRow: by k-step (block 0); kCol: by block (k-step 0)
-    int step;                           // kRow: bytes from block to block
-    __device__ __forceinline__ Frag(int block0, int block_step, int lane) {
+    int off[LAYOUT == kRow ? 2 : 1];   // kRow: by k-step
+    __device__ __forceinline__ Frag(int block0, int lane) {
+        const int g = lane / 16, j = lane % 16;
         if constexpr (LAYOUT == kRow) {
-            const int r = block0 * 32 + lane % 32;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) off[ks] = r * kStage + (((2 * ks + lane / 32) ^ row_key(r)) << 4);
-            step = block_step * 32 * kStage;
+            for (int ks = 0; ks < 2; ++ks) off[ks] = (block0 * 16 + j) * kStage + (((4 * ks + g) ^ row_key(j)) << 4);
         } else {
-            step = 0;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int g = lane / 16, j = lane % 16;
-                const int chunk = (4 * (block0 + b * block_step) + 2 * (g & 1) + (j % 4) / 2) ^ ((j / 4) << 2);
-                off[b] = ((g >> 1) * 8 + j / 4) * (BMN * 2) + chunk * 16 + (j & 1) * 8;
-            }
+            const int row = 8 * g + j / 4;
+            off[0] = row * (BMN * 2) + (block0 >> 3) * 256 + ((2 * (block0 & 7) + (j % 4) / 2) ^ col_key(row)) * 16 + (j & 1) * 8;
         }
     }
+    // b: block within the wave's part (kCol: block0 is a multiple of the part's blocks, so
+    // the block's offset is an exclusive or on the chunk bits)
     __device__ __forceinline__ i32x4 read(const uint8_t* half, int b, int ks) const {
         if constexpr (LAYOUT == kRow) {
-            return *(const i32x4*)(half + off[ks] + b * step);
+            return *(const i32x4*)(half + off[ks] + b * 16 * kStage);
         } else {
-            const uint8_t* q = half + off[b] + ks * 16 * (BMN * 2);
+            const uint8_t* q = half + (off[0] ^ (b * 32)) + ks * 32 * (BMN * 2);
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)q);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(q + 4 * (BMN * 2)));
             return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -143,17 +137,20 @@ struct Frag {
     }
 };
 
+// The 16 x 16 forms: on random operands the chip's power limit lets a
+// register-only loop of 16x16x32 bf16 products run at 2.21 PFLOP/s and one of
+// 32x32x16 at 1.89 (2.45 and 2.50 on zeros).
 template <int E> struct Acc;
 template <> struct Acc<kBf16> {
-    typedef f32x16 type;
+    typedef f32x4 type;
     __device__ static type mma(i32x4 a, i32x4 b, type c) {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                        0, 0, 0);
     }
 };
 template <> struct Acc<kI8> {
-    typedef i32x16 type;
-    __device__ static type mma(i32x4 a, i32x4 b, type c) { return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0); }
+    typedef i32x4 type;
+    __device__ static type mma(i32x4 a, i32x4 b, type c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0); }
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return f32_to_bf16_bits(a) | (f32_to_bf16_bits(b) << 16); }
@@ -220,13 +217,13 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     constexpr int EB = E == kI8 ? 1 : 2;
     constexpr int KE = kStage / EB;                            // k elements per stage
     constexpr int WN = BN / 64, WM = (kThreads / 64) / WN;     // waves along n and m
-    constexpr int IB = BM / WM / 32, JB = 2;                   // 32 x 32 blocks of a wave
+    constexpr int IB = BM / WM / 16, JB = 4;                   // 16 x 16 blocks of a wave
     constexpr int LDA = BM * 8 / kThreads, LDB = BN * 8 / kThreads;   // direct loads per lane and half-stage
     constexpr int kHalf = BM * kStage;                                // bytes of a half-stage
     static_assert(BM == BN && LDA == 4 && LDB == 4, "square tiles");
     constexpr int kTileN = GU ? BN / 2 : BN;                   // output columns per tile
     static_assert(E == kBf16 || (LA == kRow && LB == kRow), "the transposing read is for 16-bit elements");
-    static_assert(WM * WN * 64 == kThreads && WM * IB * 32 == BM, "waves cover the tile");
+    static_assert(WM * WN * 64 == kThreads && WM * IB * 16 == BM, "waves cover the tile");
 
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid % 64;
@@ -254,7 +251,7 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
                 p[q] = (up ? O.p2 : O.p) + (size_t)row * O.ld + (size_t)k0 * EB + c * 16;
             } else {
                 constexpr int per = BM * 2 / 16;                       // slots per k row
-                const int r = at / per, c = (at % per) ^ ((r & 3) << 2);
+                const int r = at / per, c = (at % per) ^ col_key(r);
                 p[q] = O.p + (size_t)(k0 + r) * O.ld + (size_t)min(r0 + c * 8, O.n - 8) * 2;
             }
         }
@@ -300,53 +297,59 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 #pragma unroll
         for (int j = 0; j < JB; ++j) acc[i][j] = typename Acc<E>::type{};
 
-    const Frag<LA, BM, IB> fa(wm * IB, 1, lane);
-    const Frag<LB, BN, JB> fb(GU ? wn : wn * JB, GU ? BN / 64 : 1, lane);
-    i32x4 a0[IB], a1[IB], b0[JB], b1[JB];
-    // Fragments of one k-step, the A blocks [i0, i1); the B blocks with the first.
-    auto read = [&](const uint8_t* ha, const uint8_t* hb, int ks, i32x4(&a)[IB], i32x4(&b)[JB], int i0, int i1)
-                    __attribute__((always_inline)) {
-        if (i0 == 0)
+    const Frag<LA, BM> fa(wm * IB, lane);
+    const Frag<LB, BN> fb(wn * (GU ? 2 : 4), lane);
+    // A stage is four parts: k-step (0, 1) x half of the wave's rows.  a: the
+    // rows' fragments of one part, b: the columns' of one k-step, both twice:
+    // one set multiplies while the next is read.
+    constexpr int AH = IB / 2;
+    i32x4 a[2][AH], b[2][JB];
+    auto read_a = [&](const uint8_t* half, int part, int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < JB; ++j) b[j] = fb.read(hb, j, ks);
-#pragma unroll
-        for (int i = i0; i < i1; ++i) a[i] = fa.read(ha, i, ks);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = i0; i < i1; ++i) a[part & 1][i] = fa.read(half, (part & 1) * AH + i, part >> 1);
     };
-    auto mma = [&](const i32x4(&a)[IB], const i32x4(&b)[JB], int i0, int i1) __attribute__((always_inline)) {
+    auto read_b = [&](const uint8_t* half, int ks) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < JB; ++j)   // gate/up: two blocks of gate columns, two of up columns
+            b[ks][j] = fb.read(half + (GU && j >= 2 ? BN / 2 * kStage : 0), GU ? j & 1 : j, ks);
+    };
+    auto mma = [&](int part, int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = i0; i < i1; ++i)
 #pragma unroll
-            for (int j = 0; j < JB; ++j) acc[i][j] = Acc<E>::mma(b[j], a[i], acc[i][j]);
+            for (int j = 0; j < JB; ++j)
+                acc[(part & 1) * AH + i][j] = Acc<E>::mma(b[part >> 1][j], a[part & 1][i], acc[(part & 1) * AH + i][j]);
         __builtin_amdgcn_sched_barrier(0);
     };
-    // The products of one k-step in a and b while the next step's fragments go
-    // into an and bn.  LDS reads and direct loads go out a few at a time between
-    // products: together they would fill the memory pipes' queues and hold up
-    // the products behind them.
-    constexpr int H = IB / 2;
-    auto step = [&](i32x4(&a)[IB], i32x4(&b)[JB], const uint8_t* ha, const uint8_t* hb, int ks, i32x4(&an)[IB],
-                    i32x4(&bn)[JB], auto&& load) __attribute__((always_inline)) {
-        mma(a, b, 0, H / 2);
-        read(ha, hb, ks, an, bn, 0, H);
-        mma(a, b, H / 2, H);
-        read(ha, hb, ks, an, bn, H, IB);
-        mma(a, b, H, IB - 1);
+    // The products of `part` while the next part's fragments are read.  LDS
+    // reads and direct loads go out a few at a time between products: together
+    // they would fill the memory pipes' queues and hold up the products behind
+    // them.
+    auto step = [&](int part, const uint8_t* ha, const uint8_t* hb, auto&& load) __attribute__((always_inline)) {
+        const int next = (part + 1) & 3;
+        mma(part, 0, AH / 4);
+        if ((next & 1) == 0) read_b(hb, next >> 1);
+        read_a(ha, next, 0, AH / 2);
+        __builtin_amdgcn_sched_barrier(0);
+        mma(part, AH / 4, AH / 2);
+        read_a(ha, next, AH / 2, AH);
+        __builtin_amdgcn_sched_barrier(0);
+        mma(part, AH / 2, AH - 1);
         load();
         __builtin_amdgcn_sched_barrier(0);
-        mma(a, b, IB - 1, IB);
+        mma(part, AH - 1, AH);
     };
     // One stage from its halves rA, rB, beginning with the previous stage's
-    // last k-step; wA and wB are the halves that stage has left.  The restrict
+    // last part; wA and wB are the halves that stage has left.  The restrict
     // qualifiers state that the loads into wA and wB do not touch rA and rB;
     // without them the compiler waits for every direct load before a
     // transposing read.
     auto turn = [&](uint8_t* __restrict__ wB, uint8_t* __restrict__ wA, const uint8_t* __restrict__ rA,
                     const uint8_t* __restrict__ rB) __attribute__((always_inline)) {
-        step(a1, b1, rA, rB, 0, a0, b0, [&]() __attribute__((always_inline)) { issueB(wB, 0, 2); });
-        step(a0, b0, rA, rB, 1, a1, b1, [&]() __attribute__((always_inline)) { issueB(wB, 2, 4); });
-        step(a1, b1, rA, rB, 2, a0, b0, [&]() __attribute__((always_inline)) { issueA(wA, 0, 2); });
-        step(a0, b0, rA, rB, 3, a1, b1, [&]() __attribute__((always_inline)) { issueA(wA, 2, 4); });
+        step(3, rA, rB, [&]() __attribute__((always_inline)) { issueB(wB, 0, 2); });
+        step(0, rA, rB, [&]() __attribute__((always_inline)) { issueB(wB, 2, 4); });
+        step(1, rA, rB, [&]() __attribute__((always_inline)) { issueA(wA, 0, 2); });
+        step(2, rA, rB, [&]() __attribute__((always_inline)) { issueA(wA, 2, 4); });
     };
     auto none = []() __attribute__((always_inline)) {};
     auto start = [&](uint8_t* __restrict__ w, const uint8_t* __restrict__ rA, const uint8_t* __restrict__ rB)
@@ -355,10 +358,11 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
         issueB(w + kHalf, 0, 4);
         issueA(w + 2 * kHalf, 0, 4);
         barrier_vm<12>();   // the first two halves
-        read(rA, rB, 0, a0, b0, 0, IB);
-        step(a0, b0, rA, rB, 1, a1, b1, none);
-        step(a1, b1, rA, rB, 2, a0, b0, none);
-        step(a0, b0, rA, rB, 3, a1, b1, none);
+        read_b(rB, 0);
+        read_a(rA, 0, 0, AH);
+        step(0, rA, rB, none);
+        step(1, rA, rB, none);
+        step(2, rA, rB, none);
     };
 
     issueA(smem, 0, 4);
@@ -375,33 +379,25 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
         u = u + 2 >= kRing ? u + 2 - kRing : u + 2;
         turn(wB, wA, rA, rB);
     }
-    mma(a1, b1, 0, IB);
+    mma(3, 0, AH);
     // the prefetched (zero) stages land before the ring becomes the epilogue's scratch
     barrier_vm<0>();
 
-    // ---- epilogue.  acc[i][j][v]: m = 32 i + l % 32, n = 32 j + 8 (v / 4) + 4 (l / 32) + v % 4 of the
-    // wave's part.  One 32-row block at a time passes through the wave's own piece of LDS (rows of 64 words
+    // ---- epilogue.  acc[i][j][v]: m = 16 i + l % 16, n = 16 j + 4 (l / 16) + v of the wave's part.  One 32-row block at a time passes through the wave's own piece of LDS (rows of 64 words
     // and a 16-byte pad, free of bank conflicts both ways), so that global accesses are whole row pieces.
     constexpr int RS = 64 * 4 + 16;
     uint8_t* piece = smem + wave * 32 * RS;
     const int nw = n0 + wn * (GU ? 32 : 64);
 #pragma unroll
-    for (int i = 0; i < IB; ++i) {
-        const int mb = m0 + wm * IB * 32 + i * 32;
+    for (int ib = 0; ib < IB / 2; ++ib) {
+        const int mb = m0 + wm * IB * 16 + ib * 32;
         if (mb >= G.M) break;
         wave_sync();
 #pragma unroll
-        for (int j = 0; j < JB; ++j)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const auto v = acc[i][j][4 * q + e];   // a value: a bit_cast of the element itself takes element 0
-                    w[e] = __builtin_bit_cast(uint32_t, v);
-                }
-                *(uint4*)(piece + (lane % 32) * RS + (32 * j + 8 * q + 4 * (lane / 32)) * 4) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int j = 0; j < JB; ++j)
+                *(typename Acc<E>::type*)(piece + (i * 16 + lane % 16) * RS + (16 * j + 4 * (lane / 16)) * 4) = acc[ib * 2 + i][j];
         wave_sync();
         auto words = [&](int row, int n, float(&v)[8]) {
             const float4 lo = *(const float4*)(piece + row * RS + n * 4);
