@@ -41,9 +41,10 @@ struct Plans {
     Plan gateup, down, dh, dx, dwgu, dw1, dwd;
 };
 Plans plans(int T, int H, int I) {
-    return Plans{plan_tiles(T, 2L * I, H, kKE), plan_tiles(T, H, I, kKE),  plan_tiles(T, I, H, kKE),
-                 plan_tiles(T, H, 2 * I, kKE),  plan_tiles(2L * I, H, T, kKE), plan_tiles(I, H, T, kKE),
-                 plan_tiles(H, I, T, kKE)};
+    return Plans{plan_tiles(T, 2L * I, H, kKE, true),  plan_tiles(T, H, I, kKE, true),
+                 plan_tiles(T, I, H, kKE, false),      plan_tiles(T, H, 2 * I, kKE, false),
+                 plan_tiles(2L * I, H, T, kKE, false), plan_tiles(I, H, T, kKE, false),
+                 plan_tiles(H, I, T, kKE, false)};
 }
 
 size_t max2(size_t a, size_t b) { return a > b ? a : b; }

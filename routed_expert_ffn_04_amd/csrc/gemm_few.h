@@ -1,0 +1,137 @@
+// The products for a few rows of A (decode: one to 32 tokens), both operands
+// with k contiguous: their time is reading B once, so nothing is tiled and
+// nothing passes through LDS.
+//
+// A workgroup takes 16 weight rows (gate/up: 8 gate rows and the 8 up rows of
+// the same columns) for all tokens, its waves share out k in blocks of 128
+// bytes (whole cache lines), and every wave loads its MFMA operands straight
+// into registers, U blocks ahead.  Lane l holds weight row l % 16 and bytes [32
+// (l / 16), +32) of the block, the two 16-byte pieces for two MFMAs; tokens are
+// laid out the same way, so both sides agree on which k a piece holds.  The
+// waves' sums meet in LDS in a fixed order and the epilogue follows, with no
+// second launch: k is split eight ways, and 16 rows a workgroup give enough
+// workgroups for every CU.
+#pragma once
+#include "gemm_tile.h"
+
+namespace moe {
+namespace gemm {
+
+// Four consecutive outputs n .. n + 3 of a row.
+__device__ __forceinline__ void store4(const Args& G, uint8_t* row, int n, const float (&v)[4], bool f32) {
+    if (G.vec && n + 4 <= G.N) {
+        if (f32) *(float4*)((float*)row + n) = make_float4(v[0], v[1], v[2], v[3]);
+        else *(uint2*)((uint16_t*)row + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < G.N) {
+                if (f32) ((float*)row)[n + e] = v[e];
+                else ((uint16_t*)row)[n + e] = (uint16_t)f32_to_bf16_bits(v[e]);
+            }
+    }
+}
+
+template <int E, int EPI, int NB, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void few_kernel(Args G) {
+    constexpr bool GU = EPI == kEpiGateUp;
+    constexpr int EB = E == kI8 ? 1 : 2;
+    constexpr int U = NB == 1 ? 4 : 2;   // blocks in flight per wave
+    static_assert(NB <= WAVES, "one wave for each token block in the epilogue");
+    __shared__ __attribute__((aligned(16))) uint8_t sums[WAVES * NB * 1024];
+    const int lane = threadIdx.x % 64, r = lane % 16, c = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int n0 = blockIdx.x * (GU ? 8 : 16);
+    const int kbytes = G.K * EB;
+    const int blocks = (kbytes + 127) / 128;
+
+    const bool up = GU && r >= 8;
+    const int wrow = min(n0 + (GU ? r % 8 : r), G.B.n - 1);
+    const uint8_t* wp = (up ? G.B.p2 : G.B.p) + (size_t)wrow * G.B.ld + c * 32;
+    const uint8_t* xp[NB];
+#pragma unroll
+    for (int t = 0; t < NB; ++t) xp[t] = G.A.p + (size_t)min(t * 16 + r, G.A.n - 1) * G.A.ld + c * 32;
+    const int left = kbytes - c * 32;   // bytes of the row from the lane's first piece on
+
+    typename Acc<E>::type acc[NB];
+#pragma unroll
+    for (int t = 0; t < NB; ++t) acc[t] = typename Acc<E>::type{};
+    for (int b = wave; b < blocks; b += WAVES * U) {
+        i32x4 w[U][2], x[U][NB][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int off = (b + u * WAVES) * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = off + h * 16 < left;
+                w[u][h] = *(const i32x4*)(in ? wp + off + h * 16 : (const uint8_t*)kZeros);
+#pragma unroll
+                for (int t = 0; t < NB; ++t) x[u][t][h] = *(const i32x4*)(in ? xp[t] + off + h * 16 : (const uint8_t*)kZeros);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // every load of the turn is out before the first product waits
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < NB; ++t) acc[t] = Acc<E>::mma(w[u][h], x[u][t][h], acc[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < NB; ++t) *(typename Acc<E>::type*)(sums + ((wave * NB + t) * 64 + lane) * 16) = acc[t];
+    __syncthreads();
+    if (wave >= NB) return;
+
+    // token block `wave`: lane l has n = 4 (l / 16) + v of token l % 16
+    typename Acc<E>::type total = *(const typename Acc<E>::type*)(sums + (wave * 64 + lane) * 16);
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) total += *(const typename Acc<E>::type*)(sums + ((i * NB + wave) * 64 + lane) * 16);
+    const int m = wave * 16 + r;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)total[e];
+    if constexpr (GU) {
+        // rows 0..7 (lanes 0..31) gate, rows 8..15 (lanes 32..63) up
+        float u[4], h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = __shfl(v[e], lane % 32 + 32, kWave);
+        const int n = n0 + 4 * (c % 2);
+        if (m >= G.M || n >= G.N) return;
+        if (G.out2) {   // g and u, each from the lanes that hold it
+            float* o = (float*)G.out2 + (size_t)m * (2 * (size_t)G.N) + (lane < 32 ? 0 : G.N) + n;
+            *(float4*)o = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (lane >= 32) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = silu_mul(v[e], u[e]);
+        *(uint2*)((uint16_t*)G.out + (size_t)m * G.N + n) = make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
+    } else {
+        const int n = n0 + 4 * c;
+        if (m >= G.M || n >= G.N) return;
+        if constexpr (EPI == kEpiI8) {
+            const float xs = G.xs[m];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int ne = min(n + e, G.N - 1);
+                v[e] *= xs * G.ws[ne];
+                if (G.bias) v[e] += G.bias[ne];
+            }
+        }
+        store4(G, (uint8_t*)G.out + (size_t)m * G.N * (G.out_f32 ? 4 : 2), n, v, G.out_f32);
+    }
+}
+
+constexpr int kFewRows = 32;
+
+// G.M <= kFewRows.
+template <int E, int EPI>
+hipError_t launch_few(const Args& G, hipStream_t s) {
+    constexpr int cols = EPI == kEpiGateUp ? 8 : 16;
+    const dim3 grid((G.N + cols - 1) / cols);
+    if (G.M <= 16) few_kernel<E, EPI, 1, 8><<<grid, dim3(512), 0, s>>>(G);
+    else few_kernel<E, EPI, 2, 8><<<grid, dim3(512), 0, s>>>(G);
+    return hipGetLastError();
+}
+
+}  // namespace gemm
+}  // namespace moe

@@ -1,36 +1,56 @@
 // Tile size and k-splits of a product, and the kernel that sums the splits.
 #pragma once
 #include "dense.h"
+#include "gemm_few.h"
 #include "gemm_tile.h"
 
 namespace moe {
 namespace gemm {
 
 struct Plan {
+    int few;             // the kernel for a few rows
     int big;             // 256 x 256 tiles, else 128 x 128
     int splits, kspan;
+    int workgroups;
 };
 
+// The tiling with the least estimated time.  In us, from whole products of 4096
+// columns and 14336 bytes of k on 256 CUs: a stage takes 1.6 in the 256-row tiles
+// (one workgroup per CU) and 0.7 in the 128-row tiles with one workgroup per
+// CU, 1.3 with two; a round of tiles costs 10 (3) besides its stages for filling
+// the ring and writing the outputs; splitting k costs a launch, 4, and the
+// partial sums written and read at 4 TB/s.  1024 x 4096 (gate/up of 2048): one
+// round of 128-row tiles 77 us, of 256-row tiles on a quarter of the CUs 190.
 // mma_cols: MFMA columns of the product (gate/up: both matrices' columns).
-inline Plan plan_tiles(long M, long mma_cols, int K, int stage_elems) {
-    Plan p;
-    const long big = ((M + 255) / 256) * ((mma_cols + 255) / 256);
-    p.big = big >= 192;
+// rows: both operands have k contiguous.
+inline Plan plan_tiles(long M, long mma_cols, int K, int stage_elems, bool rows) {
+    Plan best{};
     const int stages = (K + stage_elems - 1) / stage_elems;
-    p.splits = 1;
-    p.kspan = stages * stage_elems;
-    if (!p.big) {
-        const long tiles = ((M + 127) / 128) * ((mma_cols + 127) / 128);
-        if (tiles < 256) {
-            const int want = (int)((511 + tiles) / tiles);
-            const int most = stages / 4 > 1 ? stages / 4 : 1;
-            const int s = want < most ? want : most;
-            const int span = (stages + s - 1) / s;
-            p.kspan = span * stage_elems;
-            p.splits = (stages + span - 1) / span;
+    if (rows && M <= kFewRows) {
+        best.few = best.splits = 1;
+        best.kspan = stages * stage_elems;
+        return best;
+    }
+    double least = 0;
+    for (int big = 0; big < 2; ++big) {
+        const long edge = big ? 256 : 128;
+        const long tiles = ((M + edge - 1) / edge) * ((mma_cols + edge - 1) / edge);
+        for (int s = 1; s <= 16 && (s == 1 || (stages / s >= 2 && tiles * s <= 512)); ++s) {
+            const int span = (stages + s - 1) / s, n = (stages + span - 1) / span;
+            const long wg = tiles * n;
+            double us = big ? (double)((wg + 255) / 256) * (span * 1.6 + 10)
+                            : wg <= 256 ? span * 0.7 + 3 : (double)((wg + 511) / 512) * (span * 1.3 + 3);
+            if (n > 1) us += 4 + (double)n * M * mma_cols * 8 / 4e6;
+            if (least == 0 || us < least) {
+                least = us;
+                best.big = big;
+                best.splits = n;
+                best.kspan = span * stage_elems;
+                best.workgroups = (int)(wg < 0x7fffffff ? wg : 0x7fffffff);
+            }
         }
     }
-    return p;
+    return best;
 }
 
 // bytes of the partial sums
@@ -63,14 +83,18 @@ __global__ __launch_bounds__(256) void reduce_kernel(Args G, const float* __rest
         int acc[8] = {};
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-        for (int s = 0; s < splits; ++s) {
-            float v[8];
-            load(q + s * plane, v);
+        for (int s0 = 0; s0 < splits; s0 += 4) {   // four splits' loads in flight
+            float v[4][8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (EPI == kEpiI8) acc[e] += __float_as_int(v[e]);   // the splits of an int8 product are int32
-                else sum[e] += v[e];
-            }
+            for (int s = 0; s < 4; ++s) load(q + min(s0 + s, splits - 1) * plane, v[s]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (s0 + s < splits)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (EPI == kEpiI8) acc[e] += __float_as_int(v[s][e]);   // the splits of an int8 product are int32
+                        else sum[e] += v[s][e];
+                    }
         }
         if (EPI == kEpiI8)
 #pragma unroll
@@ -130,6 +154,16 @@ hipError_t launch_reduce(const Args& G, const float* part, int splits, hipStream
     return hipGetLastError();
 }
 
+// 128-row tiles: with one workgroup per CU a ring of ten half-stages (1024 x 4096
+// gate/up: 77 us against 108 with five), with more two per CU and five each
+// (4096 x 2048 dh: 146 us against 193 with ten).
+template <int E, int LA, int LB, int EPI, bool GU>
+hipError_t launch_tiling(const Args& G, const Plan& p, hipStream_t s) {
+    if (p.big) return launch_tiles<E, LA, LB, EPI, GU, 256, 256, 5>(G, s);
+    if (p.workgroups <= 256) return launch_tiles<E, LA, LB, EPI, GU, 128, 128, 10>(G, s);
+    return launch_tiles<E, LA, LB, EPI, GU, 128, 128, 5>(G, s);
+}
+
 // The product with its epilogue: one launch, or the k-splits' partial sums
 // into `part` and a second launch that joins them.
 template <int E, int LA, int LB, int EPI>
@@ -137,13 +171,16 @@ hipError_t run(Args G, const Plan& p, float* part, hipStream_t s) {
     constexpr bool GU = EPI == kEpiGateUp;
     G.splits = p.splits;
     G.kspan = p.kspan;
-    if (p.big) return launch_tiles<E, LA, LB, EPI, GU, 256, 256>(G, s);
-    if (p.splits == 1) return launch_tiles<E, LA, LB, EPI, GU, 128, 128>(G, s);
+    if constexpr (LA == kRow && LB == kRow) {
+        if (p.few) return launch_few<E, EPI>(G, s);
+    }
     Args P = G;
-    P.out = part;
-    P.vec = (G.N & 3) == 0;
-    const hipError_t e = launch_tiles<E, LA, LB, kEpiPart, GU, 128, 128>(P, s);
-    return e != hipSuccess ? e : launch_reduce<EPI>(G, part, p.splits, s);
+    if (p.splits > 1) {
+        P.out = part;
+        P.vec = (G.N & 3) == 0;
+    }
+    const hipError_t e = p.splits > 1 ? launch_tiling<E, LA, LB, kEpiPart, GU>(P, p, s) : launch_tiling<E, LA, LB, EPI, GU>(G, p, s);
+    return e != hipSuccess || p.splits == 1 ? e : launch_reduce<EPI>(G, part, p.splits, s);
 }
 
 }  // namespace gemm

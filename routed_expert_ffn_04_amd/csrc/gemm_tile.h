@@ -16,7 +16,9 @@
 // (2 x 4) of 128 x 64, all 160 KiB of LDS, one workgroup per CU.  128 x 128
 // tiles: 4 waves (2 x 2) of 64 x 64, 80 KiB, two workgroups per CU.  Each wave's
 // product is formed transposed (the n side is the MFMA row operand), so a lane
-// holds four consecutive n of one row m.
+// holds four consecutive n of one row m.  Four waves of 128 x 128 instead read a
+// third less from LDS but have nothing to run while they wait: T = 16384 FFN
+// 1187 us against 1179, T = 4096 gradients 729 against 664.
 //
 // Row pieces of 128 bytes, whole cache lines: a kernel that only loads moves 32
 // KiB per CU into LDS in 0.36 us with 128-byte pieces and in 0.5 to 0.75 us
@@ -55,7 +57,6 @@ enum Epi {
 };
 
 constexpr int kStage = 128;  // bytes of k per stage
-constexpr int kRing = 5;     // half-stages in the ring
 
 struct Operand {
     const uint8_t* p;    // element (row 0, k 0)
@@ -211,8 +212,8 @@ __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& t
     tm = band * 8 + t % rows;
 }
 
-template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN>
-__global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(Args G) {
+template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
+__global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM * kStage > 81920 && BM == 128 ? 1 : 2, 2))) void tile_kernel(Args G) {
     constexpr int kThreads = BM * 2;
     constexpr int EB = E == kI8 ? 1 : 2;
     constexpr int KE = kStage / EB;                            // k elements per stage
@@ -299,14 +300,15 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 
     const Frag<LA, BM> fa(wm * IB, lane);
     const Frag<LB, BN> fb(wn * (GU ? 2 : 4), lane);
-    // A stage is four parts: k-step (0, 1) x half of the wave's rows.  a: the
-    // rows' fragments of one part, b: the columns' of one k-step, both twice:
-    // one set multiplies while the next is read.
-    constexpr int AH = IB / 2;
+    // A stage is two k-steps, each one part (128-row tiles) or two (256-row
+    // tiles: the halves of the wave's rows).  a: the rows' fragments of one
+    // part, b: the columns' of one k-step, both twice: one set multiplies while
+    // the next is read.
+    constexpr int PK = IB / 4, AH = 4, kParts = 2 * PK;
     i32x4 a[2][AH], b[2][JB];
     auto read_a = [&](const uint8_t* half, int part, int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = i0; i < i1; ++i) a[part & 1][i] = fa.read(half, (part & 1) * AH + i, part >> 1);
+        for (int i = i0; i < i1; ++i) a[part & 1][i] = fa.read(half, part % PK * AH + i, part / PK);
     };
     auto read_b = [&](const uint8_t* half, int ks) __attribute__((always_inline)) {
 #pragma unroll
@@ -317,8 +319,10 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 #pragma unroll
         for (int i = i0; i < i1; ++i)
 #pragma unroll
-            for (int j = 0; j < JB; ++j)
-                acc[(part & 1) * AH + i][j] = Acc<E>::mma(b[part >> 1][j], a[part & 1][i], acc[(part & 1) * AH + i][j]);
+            for (int j = 0; j < JB; ++j) {
+                auto& c = acc[part % PK * AH + i][j];
+                c = Acc<E>::mma(b[part / PK][j], a[part & 1][i], c);
+            }
         __builtin_amdgcn_sched_barrier(0);
     };
     // The products of `part` while the next part's fragments are read.  LDS
@@ -326,72 +330,110 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     // they would fill the memory pipes' queues and hold up the products behind
     // them.
     auto step = [&](int part, const uint8_t* ha, const uint8_t* hb, auto&& load) __attribute__((always_inline)) {
-        const int next = (part + 1) & 3;
-        mma(part, 0, AH / 4);
-        if ((next & 1) == 0) read_b(hb, next >> 1);
+        const int next = (part + 1) % kParts;
+        mma(part, 0, 1);
+        if (next % PK == 0) read_b(hb, next / PK);
         read_a(ha, next, 0, AH / 2);
         __builtin_amdgcn_sched_barrier(0);
-        mma(part, AH / 4, AH / 2);
+        mma(part, 1, 2);
         read_a(ha, next, AH / 2, AH);
         __builtin_amdgcn_sched_barrier(0);
-        mma(part, AH / 2, AH - 1);
+        mma(part, 2, 3);
         load();
         __builtin_amdgcn_sched_barrier(0);
-        mma(part, AH - 1, AH);
+        mma(part, 3, 4);
     };
     // One stage from its halves rA, rB, beginning with the previous stage's
-    // last part; wA and wB are the halves that stage has left.  The restrict
-    // qualifiers state that the loads into wA and wB do not touch rA and rB;
+    // last part; w0 and w1 are the halves that stage has left.  The restrict
+    // qualifiers state that the loads into w0 and w1 do not touch rA and rB;
     // without them the compiler waits for every direct load before a
     // transposing read.
-    auto turn = [&](uint8_t* __restrict__ wB, uint8_t* __restrict__ wA, const uint8_t* __restrict__ rA,
+    auto turn = [&](uint8_t* __restrict__ w0, uint8_t* __restrict__ w1, const uint8_t* __restrict__ rA,
                     const uint8_t* __restrict__ rB) __attribute__((always_inline)) {
-        step(3, rA, rB, [&]() __attribute__((always_inline)) { issueB(wB, 0, 2); });
-        step(0, rA, rB, [&]() __attribute__((always_inline)) { issueB(wB, 2, 4); });
-        step(1, rA, rB, [&]() __attribute__((always_inline)) { issueA(wA, 0, 2); });
-        step(2, rA, rB, [&]() __attribute__((always_inline)) { issueA(wA, 2, 4); });
+        // the halves' four loads a lane each, in the order of the ring
+        auto fill = [&](int q0, int q1) __attribute__((always_inline)) {
+#pragma unroll
+            for (int q = q0; q < q1; q += 2)
+                if ((q < 4) == (R % 2 == 1)) issueB(q < 4 ? w0 : w1, q % 4, q % 4 + 2);
+                else issueA(q < 4 ? w0 : w1, q % 4, q % 4 + 2);
+        };
+        constexpr int L = 8 / kParts;
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+            step((p + kParts - 1) % kParts, rA, rB, [&]() __attribute__((always_inline)) { fill(p * L, p * L + L); });
     };
     auto none = []() __attribute__((always_inline)) {};
     auto start = [&](uint8_t* __restrict__ w, const uint8_t* __restrict__ rA, const uint8_t* __restrict__ rB)
                      __attribute__((always_inline)) {
-        issueA(w, 0, 4);
-        issueB(w + kHalf, 0, 4);
-        issueA(w + 2 * kHalf, 0, 4);
-        barrier_vm<12>();   // the first two halves
+#pragma unroll
+        for (int h = 2; h < R; ++h)
+            if (h % 2) issueB(w + (h - 2) * kHalf, 0, 4);
+            else issueA(w + (h - 2) * kHalf, 0, 4);
+        barrier_vm<(R - 2) * 4>();   // the first two halves
         read_b(rB, 0);
         read_a(rA, 0, 0, AH);
-        step(0, rA, rB, none);
-        step(1, rA, rB, none);
-        step(2, rA, rB, none);
+#pragma unroll
+        for (int p = 0; p + 1 < kParts; ++p) step(p, rA, rB, none);
     };
 
     issueA(smem, 0, 4);
     issueB(smem + kHalf, 0, 4);
     start(smem + 2 * kHalf, smem, smem + kHalf);
-    int u = 0;   // slot of the current stage's A half; the ring's order is A B A B A ...
-    auto slot = [&](int i) __attribute__((always_inline)) { return smem + (u + i >= kRing ? u + i - kRing : u + i) * kHalf; };
+    int u = 0;   // slot of the previous stage's A half; the ring's order is A B A B A ...
+    auto slot = [&](int i) __attribute__((always_inline)) { return smem + (u + i >= R ? u + i - R : u + i) * kHalf; };
     for (int s = 1; s < nst; ++s) {
-        barrier_vm<4>();   // everything but the A half of stage s + 1 has landed
-        uint8_t* wB = slot(0);
-        uint8_t* wA = slot(1);
+        barrier_vm<(R - 4) * 4>();   // stage s has landed
+        uint8_t* w0 = slot(0);
+        uint8_t* w1 = slot(1);
         const uint8_t* rA = slot(2);
         const uint8_t* rB = slot(3);
-        u = u + 2 >= kRing ? u + 2 - kRing : u + 2;
-        turn(wB, wA, rA, rB);
+        u = u + 2 >= R ? u + 2 - R : u + 2;
+        turn(w0, w1, rA, rB);
     }
-    mma(3, 0, AH);
+    mma(kParts - 1, 0, AH);
     // the prefetched (zero) stages land before the ring becomes the epilogue's scratch
     barrier_vm<0>();
 
-    // ---- epilogue.  acc[i][j][v]: m = 16 i + l % 16, n = 16 j + 4 (l / 16) + v of the wave's part.  One 32-row block at a time passes through the wave's own piece of LDS (rows of 64 words
-    // and a 16-byte pad, free of bank conflicts both ways), so that global accesses are whole row pieces.
+    // ---- epilogue.  acc[i][j][v]: m = 16 i + l % 16, n = 16 j + 4 (l / 16) + v of
+    // the wave's part.  32 rows at a time pass through the wave's own piece of LDS
+    // (rows of 64 words and a 16-byte pad, free of bank conflicts both ways), so
+    // that global accesses are whole row pieces.
     constexpr int RS = 64 * 4 + 16;
     uint8_t* piece = smem + wave * 32 * RS;
     const int nw = n0 + wn * (GU ? 32 : 64);
+    // A lane's eight columns are the same in every pass: their scales are read once.
+    const int nl = nw + (lane % 8) * 8;
+    float wsv[8], bv[8], xsv[IB / 2][4];
+    if constexpr (EPI == kEpiI8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int ne = min(nl + e, G.N - 1);
+            wsv[e] = G.ws[ne];
+            bv[e] = G.bias ? G.bias[ne] : 0.0f;
+        }
+#pragma unroll
+        for (int ib = 0; ib < IB / 2; ++ib)
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                xsv[ib][p] = G.xs[min(m0 + wm * IB * 16 + ib * 32 + p * 8 + lane / 8, G.M - 1)];
+    }
 #pragma unroll
     for (int ib = 0; ib < IB / 2; ++ib) {
         const int mb = m0 + wm * IB * 16 + ib * 32;
         if (mb >= G.M) break;
+        // the saved pre-activations of the 32 rows, read while the accumulators pass through LDS
+        float4 gv[4][2], uv[4][2];
+        if constexpr (EPI == kEpiGrad) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const size_t at = (size_t)min(mb + p * 8 + lane / 8, G.M - 1) * (2 * (size_t)G.N) + min(nl, G.N - 8);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    gv[p][e] = *(const float4*)(G.gu + at + 4 * e);
+                    uv[p][e] = *(const float4*)(G.gu + at + G.N + 4 * e);
+                }
+            }
+        }
         wave_sync();
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -446,9 +488,7 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
                 words(row, c, v);
                 if (m < G.M && n < G.N) {
                     if constexpr (EPI == kEpiGrad) {
-                        const float4* gp = (const float4*)(G.gu + (size_t)m * (2 * (size_t)G.N) + n);
-                        const float4* up = (const float4*)(G.gu + (size_t)m * (2 * (size_t)G.N) + G.N + n);
-                        const float4 ga = gp[0], gb = gp[1], ua = up[0], ub = up[1];
+                        const float4 ga = gv[p][0], gb = gv[p][1], ua = uv[p][0], ub = uv[p][1];
                         const float g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
                         const float u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
                         float dg[8], du[8], h[8];
@@ -461,13 +501,10 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
                     } else if constexpr (EPI == kEpiPart) {
                         store8(G, (uint8_t*)((float*)G.out + ((size_t)split * G.M + m) * G.N), n, v, true);
                     } else if constexpr (EPI == kEpiI8) {
-                        const float xs = G.xs[m];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const int ne = min(n + e, G.N - 1);
-                            const float s = xs * G.ws[ne];
-                            v[e] = (float)__float_as_int(v[e]) * s;
-                            if (G.bias) v[e] += G.bias[ne];
+                            v[e] = (float)__float_as_int(v[e]) * (xsv[ib][p] * wsv[e]);
+                            if (G.bias) v[e] += bv[e];
                         }
                         store8(G, (uint8_t*)G.out + (size_t)m * G.N * (G.out_f32 ? 4 : 2), n, v, G.out_f32);
                     } else {
@@ -482,13 +519,11 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     }
 }
 
-constexpr int tile_lds_bytes(int bm) { return kRing * bm * kStage; }
-
 // Launches one tiling; mt, nt and the grid follow from the sizes in G.
-template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN>
+template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
 hipError_t launch_tiles(Args G, hipStream_t s) {
-    auto* k = tile_kernel<E, LA, LB, EPI, GU, BM, BN>;
-    constexpr int lds = tile_lds_bytes(BM);
+    auto* k = tile_kernel<E, LA, LB, EPI, GU, BM, BN, R>;
+    constexpr int lds = R * BM * kStage;
     static DeviceCache ready;   // the LDS limit is a property of the function on each device
     const int ok = per_device(ready, [&] {
         return hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds) == hipSuccess ? 1 : 0;

@@ -67,7 +67,7 @@ hipError_t launch_quant_i8(const void* x, int x_f32, int rows, int cols, int8_t*
 }
 
 size_t linear_i8_ws_bytes(int T, int K, int N) {
-    return T > 0 ? part_bytes(plan_tiles(T, N, K, kStage), T, N) : 0;
+    return T > 0 ? part_bytes(plan_tiles(T, N, K, kStage, true), T, N) : 0;
 }
 
 hipError_t launch_linear_i8(const LinearI8Problem& p, void* ws, hipStream_t s) {
@@ -79,7 +79,7 @@ hipError_t launch_linear_i8(const LinearI8Problem& p, void* ws, hipStream_t s) {
     G.out = p.out;
     G.out_f32 = p.out_f32;
     G.vec = p.N % (p.out_f32 ? 4 : 8) == 0 && ((uintptr_t)p.out & 15u) == 0;
-    return run<kI8, kRow, kRow, kEpiI8>(G, plan_tiles(p.T, p.N, p.K, kStage), (float*)ws, s);
+    return run<kI8, kRow, kRow, kEpiI8>(G, plan_tiles(p.T, p.N, p.K, kStage, true), (float*)ws, s);
 }
 
 }  // namespace moe
