@@ -377,48 +377,47 @@ def layer_noalloc(x, w_router, bias, k: int, score: str, routed: Experts, shared
 
 # ---------------------------------------------------------------- around the layer
 
-class _On:
-    """Runs a call on the tensors' device and on `stream` (default: that
-    device's current stream), so that what the call allocates belongs to the
-    stream that uses it."""
-
-    __slots__ = ("ctx", "handle")
-
-    def __init__(self, device, stream):
-        import torch
-        cur = torch.cuda.current_stream(device)
-        if stream is None:
-            stream = cur
-        elif stream.device != device:
-            raise ValueError(f"stream of {stream.device} with tensors on {device}")
-        here = torch.cuda.current_device() == device.index and stream == cur
-        self.ctx = None if here else torch.cuda.stream(stream)
-        self.handle = stream.cuda_stream
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            return self.ctx.__exit__(*exc)
+def _elsewhere(device, stream):
+    """None if a call with tensors on `device` can go to the current stream as
+    it is, else the context in which it can: the device and `stream` (default:
+    the device's current stream) made current, so that what the call allocates
+    belongs to the stream that uses it."""
+    import torch
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return None
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream of {stream.device} with tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _tensors(device, **ts):
-    """Checks (name -> (tensor or None, shape, dtypes)): on the device,
-    contiguous, of the shape and of one of the dtypes."""
-    for name, (t, shape, dtypes) in ts.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} is not contiguous")
+def _current(device) -> int:
+    """Handle of the device's current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _tensor(device, name, t, shape, dtypes):
+    """Checks an argument (None passes): on the device, contiguous, of the
+    shape and of one of the dtypes."""
+    if t is None or (t.shape == shape and t.dtype in dtypes and t.device == device and t.is_contiguous()):
+        return
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    raise ValueError(f"{name} is not contiguous")
+
+
+def _empty(like, shape, dtype):
+    """An output; `like`: a checked tensor on its device, often of its very shape and dtype (which is quicker)."""
+    import torch
+    if like.dtype is dtype and like.shape == shape:
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _matrix(name, t):
@@ -446,8 +445,9 @@ def _dense_bank(bank: Experts, H: int, device):
     if bank.w_gate.dim() != 3:
         raise ValueError("bank: weights are [1][I][H] and [1][H][I]")
     I = bank.w_gate.shape[1]
-    _tensors(device, w_gate=(bank.w_gate, (1, I, H), bf), w_up=(bank.w_up, (1, I, H), bf),
-             w_down=(bank.w_down, (1, H, I), bf))
+    _tensor(device, "w_gate", bank.w_gate, (1, I, H), bf)
+    _tensor(device, "w_up", bank.w_up, (1, I, H), bf)
+    _tensor(device, "w_down", bank.w_down, (1, H, I), bf)
     return bank.struct(), I
 
 
@@ -456,19 +456,24 @@ def ffn(x, bank: Experts, *, want_gu: bool = False, y_dtype=None, out=None, gu=N
     y [T][H], or (y, gu) with want_gu: gu fp32 [T][2 I], what ffn_backward needs."""
     import torch
     T, H, dev = _matrix("x", x)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return ffn(x, bank, want_gu=want_gu, y_dtype=y_dtype, out=out, gu=gu, ws=ws)
     st, I = _dense_bank(bank, H, dev)
     y_dtype = out.dtype if out is not None else (y_dtype or torch.bfloat16)
     f32 = (torch.float32,)
-    _tensors(dev, x=(x, (T, H), (torch.bfloat16,)), out=(out, (T, H), (torch.bfloat16, torch.float32)),
-             gu=(gu, (T, 2 * I), f32))
-    with _On(dev, stream) as s:
-        if out is None:
-            out = torch.empty((T, H), dtype=y_dtype, device=dev)
-        if gu is None and want_gu:
-            gu = torch.empty((T, 2 * I), dtype=torch.float32, device=dev)
-        ws = _scratch(ws, lib().moe_ffn_workspace_size(T, H, I), dev)
-        _check(lib().moe_ffn(_ptr(x), BF16, T, ctypes.byref(st), _ptr(out), _dt_of(out), _ptr(gu), _ptr(ws),
-                             _nbytes(ws), s))
+    _tensor(dev, "x", x, (T, H), (torch.bfloat16,))
+    _tensor(dev, "out", out, (T, H), (torch.bfloat16, torch.float32))
+    _tensor(dev, "gu", gu, (T, 2 * I), f32)
+    if out is None:
+        out = _empty(x, (T, H), y_dtype)
+    if gu is None and want_gu:
+        gu = torch.empty((T, 2 * I), dtype=torch.float32, device=dev)
+    L = lib()
+    ws = _scratch(ws, L.moe_ffn_workspace_size(T, H, I), dev)
+    _check(L.moe_ffn(x.data_ptr(), BF16, T, ctypes.byref(st), out.data_ptr(), _dt_of(out), _ptr(gu), ws.data_ptr(),
+                     _nbytes(ws), _current(dev)))
     return (out, gu) if want_gu else out
 
 
@@ -478,33 +483,48 @@ def ffn_backward(dy, x, bank: Experts, gu=None, *, need=("dx", "dw_gate", "dw_up
     (None: computed again)."""
     import torch
     T, H, dev = _matrix("x", x)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return ffn_backward(dy, x, bank, gu, need=need, ws=ws)
     st, I = _dense_bank(bank, H, dev)
     bf = (torch.bfloat16,)
-    _tensors(dev, x=(x, (T, H), bf), dy=(dy, (T, H), bf), gu=(gu, (T, 2 * I), (torch.float32,)))
-    shapes = {"dx": (T, H), "dw_gate": (1, I, H), "dw_up": (1, I, H), "dw_down": (1, H, I)}
-    if not set(need) <= set(shapes):
+    _tensor(dev, "x", x, (T, H), bf)
+    _tensor(dev, "dy", dy, (T, H), bf)
+    _tensor(dev, "gu", gu, (T, 2 * I), (torch.float32,))
+    names = ("dx", "dw_gate", "dw_up", "dw_down")
+    if not set(need) <= set(names):
         raise ValueError(f"need: {need}")
-    with _On(dev, stream) as s:
-        o = {k: torch.empty(shapes[k], dtype=torch.bfloat16, device=dev) if k in need else None for k in shapes}
-        ws = _scratch(ws, lib().moe_ffn_backward_workspace_size(T, H, I, int(gu is not None)), dev)
-        _check(lib().moe_ffn_backward(_ptr(dy), _ptr(x), BF16, T, ctypes.byref(st), _ptr(gu), _ptr(o["dx"]),
-                                      _ptr(o["dw_gate"]), _ptr(o["dw_up"]), _ptr(o["dw_down"]), _ptr(ws), _nbytes(ws),
-                                      s))
-    return tuple(o.values())
+    likes = (x, bank.w_gate, bank.w_up, bank.w_down)
+    o = tuple(torch.empty_like(t) if k in need else None for k, t in zip(names, likes))
+    L = lib()
+    ws = _scratch(ws, L.moe_ffn_backward_workspace_size(T, H, I, int(gu is not None)), dev)
+    _check(L.moe_ffn_backward(dy.data_ptr(), x.data_ptr(), BF16, T, ctypes.byref(st), _ptr(gu), *map(_ptr, o),
+                              ws.data_ptr(), _nbytes(ws), _current(dev)))
+    return o
 
 
 def _norm_params(T, H, dev, post_w, gate, gate_div, pre_w):
     """(rows of the gate, weight dtype code) after the checks."""
     import torch
+    dtype = None
+    for t in (post_w, gate, pre_w):
+        if t is not None:
+            if dtype is not None and t.dtype is not dtype:
+                raise TypeError(f"post_w, gate and pre_w have different dtypes: {dtype}, {t.dtype}")
+            dtype = t.dtype
+    if dtype is None:
+        return 0, F32
     fl = (torch.float32, torch.bfloat16)
-    dtypes = {t.dtype for t in (post_w, gate, pre_w) if t is not None}
-    if len(dtypes) > 1:
-        raise TypeError(f"post_w, gate and pre_w have different dtypes: {dtypes}")
-    if gate is not None and gate_div < 1:
-        raise ValueError(f"gate_div={gate_div}")
-    G = -(-T // gate_div) if gate is not None else 0
-    _tensors(dev, post_w=(post_w, (H,), fl), gate=(gate, (G, H), fl), pre_w=(pre_w, (H,), fl))
-    return G, BF16 if dtypes == {torch.bfloat16} else F32
+    G = 0
+    if gate is not None:
+        if gate_div < 1:
+            raise ValueError(f"gate_div={gate_div}")
+        G = -(-T // gate_div)
+        _tensor(dev, "gate", gate, (G, H), fl)
+    _tensor(dev, "post_w", post_w, (H,), fl)
+    _tensor(dev, "pre_w", pre_w, (H,), fl)
+    return G, F32 if dtype is torch.float32 else BF16
 
 
 def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: float = 1.0, pre_w=None,
@@ -516,6 +536,11 @@ def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: f
     output tensors; r may be res itself."""
     import torch
     T, H, dev = _matrix("y", y)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return norm(y, res, post_w=post_w, gate=gate, gate_div=gate_div, res_scale=res_scale, pre_w=pre_w, eps=eps,
+                        r_dtype=r_dtype, x_dtype=x_dtype, want_r=want_r, want_x=want_x, r=r, x=x)
     fl = (torch.float32, torch.bfloat16)
     _, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
     r_dtype = res.dtype if res is not None else r.dtype if r is not None else (r_dtype or y.dtype)
@@ -524,18 +549,20 @@ def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: f
     if r_dtype not in fl or x_dtype not in fl + (torch.int8,):
         raise TypeError(f"norm: r {r_dtype}, x {x_dtype}")
     i8 = x_dtype == torch.int8
-    _tensors(dev, y=(y, (T, H), fl), res=(res, (T, H), (r_dtype,)), r=(r, (T, H), (r_dtype,)),
-             x=(q, (T, H), (x_dtype,)), x_scale=(scale, (T,), (torch.float32,)))
-    with _On(dev, stream) as s:
-        if r is None and want_r:
-            r = torch.empty((T, H), dtype=r_dtype, device=dev)
-        if q is None and want_x:
-            q = torch.empty((T, H), dtype=x_dtype, device=dev)
-        if q is not None and i8 and scale is None:
-            scale = torch.empty((T,), dtype=torch.float32, device=dev)
-        _check(lib().moe_norm(_ptr(y), _dt_of(y), _ptr(res), F32 if r_dtype == torch.float32 else BF16, T, H,
-                              _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w), w_dt, res_scale, eps, _ptr(r), _ptr(q),
-                              I8 if i8 else F32 if x_dtype == torch.float32 else BF16, _ptr(scale), s))
+    _tensor(dev, "y", y, (T, H), fl)
+    _tensor(dev, "res", res, (T, H), (r_dtype,))
+    _tensor(dev, "r", r, (T, H), (r_dtype,))
+    _tensor(dev, "x", q, (T, H), (x_dtype,))
+    _tensor(dev, "x_scale", scale, (T,), (torch.float32,))
+    if r is None and want_r:
+        r = _empty(y if res is None else res, (T, H), r_dtype)
+    if q is None and want_x:
+        q = _empty(y, (T, H), x_dtype)
+    if q is not None and i8 and scale is None:
+        scale = torch.empty((T,), dtype=torch.float32, device=dev)
+    _check(lib().moe_norm(y.data_ptr(), _dt_of(y), _ptr(res), F32 if r_dtype == torch.float32 else BF16, T, H,
+                          _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w), w_dt, res_scale, eps, _ptr(r), _ptr(q),
+                          I8 if i8 else F32 if x_dtype == torch.float32 else BF16, _ptr(scale), _current(dev)))
     return r, ((q, scale) if i8 and q is not None else q)
 
 
@@ -550,26 +577,33 @@ def norm_backward(dx, dr, y, r, *, post_w=None, gate=None, gate_div: int = 1, re
     if some is None:
         raise ValueError("norm_backward: no tensors")
     T, H, dev = _matrix("y, r, dx or dr", some)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return norm_backward(dx, dr, y, r, post_w=post_w, gate=gate, gate_div=gate_div, res_scale=res_scale,
+                                 pre_w=pre_w, eps=eps, need=need, ws=ws)
     fl = (torch.float32, torch.bfloat16)
     G, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
     r_dtype = r.dtype if r is not None else dr.dtype if dr is not None else torch.float32
     y_dtype = y.dtype if y is not None else r_dtype
-    _tensors(dev, dx=(dx, (T, H), fl), dr=(dr, (T, H), (r_dtype,)), y=(y, (T, H), fl), r=(r, (T, H), fl))
+    _tensor(dev, "dx", dx, (T, H), fl)
+    _tensor(dev, "dr", dr, (T, H), (r_dtype,))
+    _tensor(dev, "y", y, (T, H), fl)
+    _tensor(dev, "r", r, (T, H), fl)
     if r_dtype not in fl:
         raise TypeError(f"norm_backward: dr has dtype {r_dtype}")
-    what = {"dy": ((T, H), y_dtype, True), "dres": ((T, H), r_dtype, True), "dpost_w": ((H,), torch.float32, post_w is not None),
-            "dgate": ((G, H), torch.float32, gate is not None), "dpre_w": ((H,), torch.float32, pre_w is not None and dx is not None)}
+    f32 = torch.float32
+    what = {"dy": (some if y is None else y, (T, H), y_dtype), "dres": (some if r is None else r, (T, H), r_dtype),
+            "dpost_w": (post_w, (H,), f32), "dgate": (gate, (G, H), f32), "dpre_w": (None if dx is None else pre_w, (H,), f32)}
     if not set(need) <= set(what):
         raise ValueError(f"need: {need}")
-    with _On(dev, stream) as s:
-        o = {k: torch.empty(shape, dtype=dt, device=dev) if k in need and has else None
-             for k, (shape, dt, has) in what.items()}
-        ws = _scratch(ws, lib().moe_norm_backward_workspace_size(T, H, gate_div if gate is not None else 0), dev)
-        _check(lib().moe_norm_backward(
-            _ptr(dx), F32 if dx is None else _dt_of(dx), _ptr(dr), _ptr(y), F32 if y_dtype == torch.float32 else BF16,
-            _ptr(r), F32 if r_dtype == torch.float32 else BF16, T, H, _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w),
-            w_dt, res_scale, eps, _ptr(o["dy"]), _ptr(o["dres"]), _ptr(o["dpost_w"]), _ptr(o["dgate"]),
-            _ptr(o["dpre_w"]), _ptr(ws), _nbytes(ws), s))
+    o = {k: _empty(*v) if k in need and v[0] is not None else None for k, v in what.items()}
+    L = lib()
+    ws = _scratch(ws, L.moe_norm_backward_workspace_size(T, H, gate_div if gate is not None else 0), dev)
+    _check(L.moe_norm_backward(
+        _ptr(dx), F32 if dx is None else _dt_of(dx), _ptr(dr), _ptr(y), F32 if y_dtype == torch.float32 else BF16,
+        _ptr(r), F32 if r_dtype == torch.float32 else BF16, T, H, _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w), w_dt,
+        res_scale, eps, *map(_ptr, o.values()), ws.data_ptr(), _nbytes(ws), _current(dev)))
     return o
 
 
@@ -577,14 +611,18 @@ def quant_i8(x, stream=None, out=None):
     """int8 codes [rows][cols], scales [rows] fp32 (moe_quant_i8)."""
     import torch
     rows, cols, dev = _matrix("x", x)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return quant_i8(x, out=out)
     q, scale = out if out is not None else (None, None)
-    _tensors(dev, x=(x, (rows, cols), (torch.float32, torch.bfloat16)), q=(q, (rows, cols), (torch.int8,)),
-             scale=(scale, (rows,), (torch.float32,)))
-    with _On(dev, stream) as s:
-        if out is None:
-            q = torch.empty((rows, cols), dtype=torch.int8, device=dev)
-            scale = torch.empty((rows,), dtype=torch.float32, device=dev)
-        _check(lib().moe_quant_i8(_ptr(x), _dt_of(x), rows, cols, _ptr(q), _ptr(scale), s))
+    _tensor(dev, "x", x, (rows, cols), (torch.float32, torch.bfloat16))
+    _tensor(dev, "q", q, (rows, cols), (torch.int8,))
+    _tensor(dev, "scale", scale, (rows,), (torch.float32,))
+    if out is None:
+        q = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+        scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+    _check(lib().moe_quant_i8(x.data_ptr(), _dt_of(x), rows, cols, q.data_ptr(), scale.data_ptr(), _current(dev)))
     return q, scale
 
 
@@ -593,18 +631,26 @@ def linear_i8(q, q_scale, w, w_scale, bias=None, *, out_dtype=None, out=None, ws
     q [T][K] and w [N][K] int8, q_scale [T], w_scale and bias [N] fp32."""
     import torch
     T, K, dev = _matrix("q", q)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return linear_i8(q, q_scale, w, w_scale, bias, out_dtype=out_dtype, out=out, ws=ws)
     N = _matrix("w", w)[0]
     f32, i8 = (torch.float32,), (torch.int8,)
     out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"linear_i8: out {out_dtype}")
-    _tensors(dev, q=(q, (T, K), i8), w=(w, (N, K), i8), q_scale=(q_scale, (T,), f32), w_scale=(w_scale, (N,), f32),
-             bias=(bias, (N,), f32), out=(out, (T, N), (out_dtype,)))
-    with _On(dev, stream) as s:
-        if out is None:
-            out = torch.empty((T, N), dtype=out_dtype, device=dev)
-        need = lib().moe_linear_i8_workspace_size(T, K, N)
-        ws = _scratch(ws, need, dev) if need or ws is not None else None
-        _check(lib().moe_linear_i8(_ptr(q), _ptr(q_scale), T, K, _ptr(w), _ptr(w_scale), _ptr(bias), N, _ptr(out),
-                                   _dt_of(out), _ptr(ws), 0 if ws is None else _nbytes(ws), s))
+    _tensor(dev, "q", q, (T, K), i8)
+    _tensor(dev, "w", w, (N, K), i8)
+    _tensor(dev, "q_scale", q_scale, (T,), f32)
+    _tensor(dev, "w_scale", w_scale, (N,), f32)
+    _tensor(dev, "bias", bias, (N,), f32)
+    _tensor(dev, "out", out, (T, N), (out_dtype,))
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype, device=dev)
+    L = lib()
+    need = L.moe_linear_i8_workspace_size(T, K, N)
+    ws = _scratch(ws, need, dev) if need or ws is not None else None
+    _check(L.moe_linear_i8(q.data_ptr(), q_scale.data_ptr(), T, K, w.data_ptr(), w_scale.data_ptr(), _ptr(bias), N,
+                           out.data_ptr(), _dt_of(out), _ptr(ws), 0 if ws is None else _nbytes(ws), _current(dev)))
     return out

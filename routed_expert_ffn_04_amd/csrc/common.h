@@ -23,6 +23,14 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
     return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
+// The same of two values, a in the low half, by the hardware conversion
+// (v_cvt_pk_bf16_f32: nearest even).
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float a, float b) {
+    typedef __attribute__((ext_vector_type(2))) float f32x2;
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
 // ---- OCP FP8 E4M3FN encode -------------------------------------------------
 // Round to nearest even, saturate the magnitude at 448 (code 0x7E), keep the
 // sign bit of the input.  Normal results (|v| >= 2^-6) round the fp32

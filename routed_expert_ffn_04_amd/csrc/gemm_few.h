@@ -21,7 +21,7 @@ namespace gemm {
 __device__ __forceinline__ void store4(const Args& G, uint8_t* row, int n, const float (&v)[4], bool f32) {
     if (G.vec && n + 4 <= G.N) {
         if (f32) *(float4*)((float*)row + n) = make_float4(v[0], v[1], v[2], v[3]);
-        else *(uint2*)((uint16_t*)row + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else *(uint2*)((uint16_t*)row + n) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args G) {
         if (lane >= 32) return;
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = silu_mul(v[e], u[e]);
-        *(uint2*)((uint16_t*)G.out + (size_t)m * G.N + n) = make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
+        *(uint2*)((uint16_t*)G.out + (size_t)m * G.N + n) = make_uint2(f32x2_to_bf16x2(h[0], h[1]), f32x2_to_bf16x2(h[2], h[3]));
     } else {
         const int n = n0 + 4 * c;
         if (m >= G.M || n >= G.N) return;

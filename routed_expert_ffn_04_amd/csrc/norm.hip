@@ -5,97 +5,112 @@
 // Memory-bound: y and res are read once, r and x written once.  A row stays in
 // the registers of its threads between the two norms (both means are sums
 // over the whole row), in fp32; r enters the second norm before it is rounded to
-// its stored type.
+// its stored type.  A worker (the threads that share a row) takes a run of
+// consecutive rows: the weights are read once a run (at 7168 columns of fp32 they
+// are as many bytes as a row's own), and the next row's y and res are on their way
+// while a row is reduced.
 #include "norm_row.h"
 
 namespace moe {
 namespace norm {
 
-template <int TPR, int NV, int VEC>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem P) {
-    constexpr int kThreads = TPR < 256 ? 256 : TPR, kRows = kThreads / TPR;
-    __shared__ float slot[kThreads / 64 * 4];
+template <int TPR, int NV, int VEC, bool WIDE>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem P, int rows_per_worker) {
+    constexpr int kThreads = TPR < 256 ? 256 : TPR, kWorkers = kThreads / TPR;
+    typedef Raw<VEC, WIDE> Row;
+    __shared__ __attribute__((aligned(16))) float slot[kThreads / 16 * 4];
     int turn = 0;
     const int t = threadIdx.x % TPR;
-    const long row = (long)blockIdx.x * kRows + threadIdx.x / TPR;
-    const bool live = row < P.T;   // rows past the end take part in the barriers only
     const int H = P.H;
-    const size_t at0 = (size_t)(live ? row : 0) * H;
+    const long first = ((long)blockIdx.x * kWorkers + threadIdx.x / TPR) * rows_per_worker;
     auto col = [&](int v) { return (v * TPR + t) * VEC; };
-
-    Raw<VEC> yr[NV], rr[NV], pw[NV], gw[NV], xw[NV];
-    const size_t gate0 = P.gate ? (size_t)((live ? row : 0) / P.gate_div) * H : 0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const bool in = live && col(v) < H;
-        yr[v] = load<VEC>(P.y, P.y_f32, at0 + col(v), in);
-        rr[v] = load<VEC>(P.res, P.r_f32, at0 + col(v), in && P.res);
-        pw[v] = load<VEC>(P.post_w, P.w_f32, col(v), in && P.post_w);
-        gw[v] = load<VEC>(P.gate, P.w_f32, gate0 + col(v), in && P.gate);
-        xw[v] = load<VEC>(P.pre_w, P.w_f32, col(v), in && P.pre_w);
-    }
-    float n[NV][VEC];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) unpack<VEC>(yr[v], P.y_f32, n[v]);
-    if (P.post_w) {
-        float ss[1] = {0.0f};
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) ss[0] = __builtin_fmaf(n[v][e], n[v][e], ss[0]);
-        row_reduce<TPR, 1>(ss, slot, turn);
-        const float q = 1.0f / sqrtf(ss[0] / (float)H + P.eps);
+    auto fetch = [&](long row, Row(&y)[NV], Row(&r)[NV]) __attribute__((always_inline)) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float w[VEC];
-            unpack<VEC>(pw[v], P.w_f32, w);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) n[v][e] = n[v][e] * q * w[e];
+            const bool in = row < P.T && col(v) < H;
+            const size_t at = (size_t)(in ? row : 0) * H + col(v);
+            y[v] = load<VEC, WIDE>(P.y, P.y_f32, at, in);
+            r[v] = load<VEC, WIDE>(P.res, P.r_f32, at, in && P.res);
         }
-    }
-    float ss[1] = {0.0f};
+    };
+
+    Row yr[NV], rr[NV];
+    float pw[NV][VEC], gw[NV][VEC], xw[NV][VEC];
+    fetch(first, yr, rr);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        float r[VEC], g[VEC];
-        unpack<VEC>(rr[v], P.r_f32, r);
-        unpack<VEC>(gw[v], P.w_f32, g);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            n[v][e] = __builtin_fmaf(P.res_scale, r[e], P.gate ? g[e] * n[v][e] : n[v][e]);
-            ss[0] = __builtin_fmaf(n[v][e], n[v][e], ss[0]);
-        }
-        if (P.r_out && live && col(v) < H) store<VEC>(P.r_out, P.r_f32, at0 + col(v), n[v]);
+        const bool in = col(v) < H;
+        weights<VEC>(P.post_w, P.w_f32, col(v), in, pw[v]);
+        weights<VEC>(P.pre_w, P.w_f32, col(v), in, xw[v]);
+        weights<VEC>(nullptr, 0, 0, false, gw[v]);
     }
-    if (!P.x_out) return;
-    row_reduce<TPR, 1>(ss, slot, turn);
-    const float q = 1.0f / sqrtf(ss[0] / (float)H + P.eps);
-    float amax[1] = {0.0f};
+    // every worker of the workgroup makes the same number of turns (barriers)
+    for (int i = 0; i < rows_per_worker; ++i) {
+        const long row = first + i;
+        const bool live = row < P.T;
+        if (TPR == 64 && !live) return;   // a wave alone: no barriers
+        const size_t at0 = (size_t)(live ? row : 0) * H;
+        if (P.gate && live && (i == 0 || row % P.gate_div == 0)) {
+            const size_t g0 = (size_t)(row / P.gate_div) * H;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        float w[VEC];
-        unpack<VEC>(xw[v], P.w_f32, w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            n[v][e] = n[v][e] * q * (P.pre_w ? w[e] : 1.0f);
-            amax[0] = fmaxf(amax[0], fabsf(n[v][e]));
+            for (int v = 0; v < NV; ++v) weights<VEC>(P.gate, P.w_f32, g0 + col(v), col(v) < H, gw[v]);
         }
-        if (!P.x_scale && live && col(v) < H) store<VEC>(P.x_out, P.x_f32, at0 + col(v), n[v]);
-    }
-    if (!P.x_scale) return;
-    row_reduce<TPR, 1, true>(amax, slot, turn);
-    const float s = i8_scale(amax[0]);
-    if (live && t == 0) P.x_scale[row] = s;
+        float n[NV][VEC], r[NV][VEC];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        if (!live || col(v) >= H) continue;
-        int8_t* o = (int8_t*)P.x_out + at0 + col(v);
-        if constexpr (VEC == 8) {
-            uint32_t w[2] = {0, 0};
+        for (int v = 0; v < NV; ++v) {
+            unpack(yr[v], P.y_f32, n[v]);
+            unpack(rr[v], P.r_f32, r[v]);
+        }
+        if (i + 1 < rows_per_worker) fetch(row + 1, yr, rr);
+        float p = 1.0f;
+        if (P.post_w) {
+            float ss[1] = {0.0f};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e / 4] |= i8_code(n[v][e], s) << (8 * (e % 4));
-            *(uint2*)o = make_uint2(w[0], w[1]);
-        } else {
-            *o = (int8_t)i8_code(n[v][0], s);
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) ss[0] = __builtin_fmaf(n[v][e], n[v][e], ss[0]);
+            row_reduce<TPR, 1>(ss, slot, turn);
+            p = 1.0f / sqrtf(ss[0] / (float)H + P.eps);
+        }
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                n[v][e] = __builtin_fmaf(P.res_scale, r[v][e], n[v][e] * p * pw[v][e] * gw[v][e]);
+                ss[0] = __builtin_fmaf(n[v][e], n[v][e], ss[0]);
+            }
+            if (P.r_out && live && col(v) < H) store<VEC>(P.r_out, P.r_f32, at0 + col(v), n[v]);
+        }
+        if (!P.x_out) continue;
+        row_reduce<TPR, 1>(ss, slot, turn);
+        const float q = 1.0f / sqrtf(ss[0] / (float)H + P.eps);
+        float amax[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                n[v][e] = n[v][e] * q * xw[v][e];
+                if (P.x_scale) amax[0] = fmaxf(amax[0], fabsf(n[v][e]));
+            }
+            if (!P.x_scale && live && col(v) < H) store<VEC>(P.x_out, P.x_f32, at0 + col(v), n[v]);
+        }
+        if (!P.x_scale) continue;
+        row_reduce<TPR, 1, true>(amax, slot, turn);
+        const float s = i8_scale(amax[0]);
+        if (live && t == 0) P.x_scale[row] = s;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (!live || col(v) >= H) continue;
+            int8_t* o = (int8_t*)P.x_out + at0 + col(v);
+            if constexpr (VEC == 8) {
+                uint32_t w[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e / 4] |= i8_code(n[v][e], s) << (8 * (e % 4));
+                *(uint2*)o = make_uint2(w[0], w[1]);
+            } else {
+                *o = (int8_t)i8_code(n[v][0], s);
+            }
         }
     }
 }
@@ -106,17 +121,21 @@ hipError_t launch_norm(const NormProblem& p, hipStream_t s) {
     using namespace norm;
     const bool vec = p.H % 8 == 0 && rows16(p.y) && rows16(p.res) && rows16(p.post_w) && rows16(p.gate) &&
                      rows16(p.pre_w) && rows16(p.r_out) && ((uintptr_t)p.x_out & (p.x_scale ? 7u : 15u)) == 0;
+    const bool wide = p.y_f32 || (p.res && p.r_f32);
     const int units = vec ? p.H / 8 : p.H;
-    // the narrowest shape that holds a row
-#define X(TPR, NV, VEC)                                                                                    \
-    if (vec == (VEC == 8) && units <= TPR * NV) {                                                          \
-        constexpr int threads = TPR < 256 ? 256 : TPR, rows = threads / TPR;                               \
-        const unsigned grid = (unsigned)(((long)p.T + rows - 1) / rows);                                   \
-        norm_kernel<TPR, NV, VEC><<<dim3(grid), dim3(threads), 0, s>>>(p);                                 \
-        return hipGetLastError();                                                                          \
+    // The narrowest shape that holds a row; runs that give every CU PERCU workgroups, or one row each.
+#define X(TPR, NV, VEC, WIDE, PERCU)                                                                            \
+    if (vec == (VEC == 8) && (VEC == 1 || wide == WIDE) && units <= TPR * NV) {                                 \
+        constexpr int threads = TPR < 256 ? 256 : TPR, workers = threads / TPR;                                 \
+        const long most = (long)PERCU * 256 * workers;                                                          \
+        const int run = (int)((p.T + most - 1) / most);                                                         \
+        const unsigned grid = (unsigned)(((long)p.T + (long)run * workers - 1) / ((long)run * workers));        \
+        norm_kernel<TPR, NV, VEC, WIDE><<<dim3(grid), dim3(threads), 0, s>>>(p, run);                           \
+        return hipGetLastError();                                                                               \
     }
-    X(64, 1, 8) X(256, 1, 8) X(256, 2, 8) X(256, 4, 8) X(1024, 2, 8)
-    X(64, 1, 1) X(256, 1, 1) X(256, 4, 1) X(1024, 4, 1) X(1024, 16, 1)
+    X(64, 1, 8, false, 8) X(64, 1, 8, true, 8) X(256, 1, 8, false, 8) X(256, 1, 8, true, 8)
+    X(512, 2, 8, false, 2) X(512, 2, 8, true, 2) X(1024, 2, 8, false, 1) X(1024, 2, 8, true, 1)
+    X(64, 1, 1, true, 8) X(256, 1, 1, true, 8) X(256, 4, 1, true, 4) X(1024, 4, 1, true, 2) X(1024, 16, 1, true, 1)
 #undef X
     return hipErrorInvalidValue;
 }

@@ -21,13 +21,9 @@ struct Runs {
     int workers;
 };
 
-// At least `least` rows a run keep the workspace's traffic (three fp32 values
-// per column and run, written and read) below that of the rows themselves.
 inline Runs runs_of(int T, int gate_div, int want_workers) {
     Runs r;
-    const int least = 4;
-    int c = (int)(((long)T + want_workers - 1) / want_workers);
-    if (c < least) c = least;
+    const int c = (int)(((long)T + want_workers - 1) / want_workers);
     if (gate_div >= c) {
         r.per_gate = (int)(((long)gate_div + c - 1) / c);
         r.rows = (int)(((long)gate_div + r.per_gate - 1) / r.per_gate);
@@ -43,12 +39,12 @@ inline Runs runs_of(int T, int gate_div, int want_workers) {
     return r;
 }
 
-template <int TPR, int NV, int VEC>
+template <int TPR, int NV, int VEC, bool WIDE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormProblem P, Runs R, float* __restrict__ part_pre,
                                                                           float* __restrict__ part_post,
                                                                           float* __restrict__ part_gate) {
     constexpr int kThreads = TPR < 256 ? 256 : TPR, kWorkers = kThreads / TPR;
-    __shared__ float slot[kThreads / 64 * 4];
+    __shared__ __attribute__((aligned(16))) float slot[kThreads / 16 * 4];
     int turn = 0;
     const int t = threadIdx.x % TPR;
     const long wk = (long)blockIdx.x * kWorkers + threadIdx.x / TPR;
@@ -66,73 +62,85 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
             end = min(first + R.rows, (long)P.T);
         }
     }
-    float pre[NV][VEC], post[NV][VEC], gate[NV][VEC];
+    // sums over the rows: dx xh; and d yh of the rows since the gate last changed,
+    // from which both dgate (times post_w) and dpost_w (times the gate) follow
+    float pre[NV][VEC], post[NV][VEC], dyh[NV][VEC];
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) pre[v][e] = post[v][e] = gate[v][e] = 0.0f;
+        for (int e = 0; e < VEC; ++e) pre[v][e] = post[v][e] = dyh[v][e] = 0.0f;
 
-    Raw<VEC> pw[NV], xw[NV], gw[NV];
+    // the next row's loads go out once this row's registers are free, where the
+    // registers suffice
+    constexpr bool kAhead = !(WIDE && NV * VEC > 8);
+    typedef Raw<VEC, WIDE> Row;
+    float pw[NV][VEC], gw[NV][VEC], xw[NV][VEC];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const bool in = col(v) < H;
-        pw[v] = load<VEC>(P.post_w, P.w_f32, col(v), in && P.post_w);
-        xw[v] = load<VEC>(P.pre_w, P.w_f32, col(v), in && P.pre_w);
+        weights<VEC>(P.post_w, P.w_f32, col(v), in, pw[v]);
+        weights<VEC>(P.pre_w, P.w_f32, col(v), in, xw[v]);
+        weights<VEC>(nullptr, 0, 0, false, gw[v]);
     }
     const float inv_h = 1.0f / (float)H;
-
+    Row dxr[NV], rr[NV], drr[NV], yr[NV];
+    auto fetch = [&](long row) __attribute__((always_inline)) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const bool in = row < end && col(v) < H;
+            const size_t at = (size_t)(in ? row : 0) * H + col(v);
+            dxr[v] = load<VEC, WIDE>(P.dx, P.x_f32, at, in && P.dx);
+            rr[v] = load<VEC, WIDE>(P.r, P.r_f32, at, in && P.dx);
+            drr[v] = load<VEC, WIDE>(P.dr, P.r_f32, at, in && P.dr);
+            yr[v] = load<VEC, WIDE>(P.y, P.y_f32, at, in && P.y);
+        }
+    };
+    if (kAhead) fetch(first);
     // every worker of the workgroup makes the same number of turns (barriers)
     for (int i = 0; i < R.rows; ++i) {
         const long row = first + i;
         const bool live = row < end;
+        if (!kAhead) fetch(row);
         const size_t at0 = (size_t)(live ? row : 0) * H;
         if (P.gate && live && (i == 0 || row % P.gate_div == 0)) {
             const size_t g0 = (size_t)(row / P.gate_div) * H;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) gw[v] = load<VEC>(P.gate, P.w_f32, g0 + col(v), col(v) < H);
+            for (int v = 0; v < NV; ++v) weights<VEC>(P.gate, P.w_f32, g0 + col(v), col(v) < H, gw[v]);
         }
-        Raw<VEC> dxr[NV], drr[NV], yr[NV], rr[NV];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const bool in = live && col(v) < H;
-            dxr[v] = load<VEC>(P.dx, P.x_f32, at0 + col(v), in && P.dx);
-            rr[v] = load<VEC>(P.r, P.r_f32, at0 + col(v), in && P.dx);
-            drr[v] = load<VEC>(P.dr, P.r_f32, at0 + col(v), in && P.dr);
-            yr[v] = load<VEC>(P.y, P.y_f32, at0 + col(v), in && P.y);
-        }
+        // absent weights are ones, absent gradients and rows zeros: one formula for all
         float d[NV][VEC], y[NV][VEC];
-        float sum[2] = {0.0f, 0.0f};   // r r, dx pre_w r
+        float q = 0.0f, c = 0.0f;   // 1 / rms(r), mean(dx pre_w r) / rms(r)^3
         if (P.dx) {
+            float sum[2] = {0.0f, 0.0f};   // r r, dx pre_w r
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                float dx[VEC], r[VEC], w[VEC];
-                unpack<VEC>(dxr[v], P.x_f32, dx);
-                unpack<VEC>(rr[v], P.r_f32, r);
-                unpack<VEC>(xw[v], P.w_f32, w);
+                float dx[VEC], r[VEC];
+                unpack(dxr[v], P.x_f32, dx);
+                unpack(rr[v], P.r_f32, r);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     sum[0] = __builtin_fmaf(r[e], r[e], sum[0]);
-                    sum[1] = __builtin_fmaf(dx[e] * (P.pre_w ? w[e] : 1.0f), r[e], sum[1]);
+                    sum[1] = __builtin_fmaf(dx[e] * xw[v][e], r[e], sum[1]);
                 }
             }
             row_reduce<TPR, 2>(sum, slot, turn);
+            q = 1.0f / sqrtf(sum[0] * inv_h + P.eps);
+            c = sum[1] * inv_h * q * q * q;
         }
-        const float q = 1.0f / sqrtf(sum[0] * inv_h + P.eps);
-        const float c = sum[1] * inv_h * q * q * q;
         float sy[2] = {0.0f, 0.0f};   // y y, dn post_w y
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            unpack<VEC>(drr[v], P.r_f32, d[v]);
-            if (P.dx) {
-                float dx[VEC], r[VEC], w[VEC];
-                unpack<VEC>(dxr[v], P.x_f32, dx);
-                unpack<VEC>(rr[v], P.r_f32, r);
-                unpack<VEC>(xw[v], P.w_f32, w);
+            float dx[VEC], r[VEC];
+            unpack(dxr[v], P.x_f32, dx);
+            unpack(rr[v], P.r_f32, r);
+            unpack(drr[v], P.r_f32, d[v]);
+            unpack(yr[v], P.y_f32, y[v]);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    pre[v][e] = __builtin_fmaf(dx[e], r[e] * q, pre[v][e]);
-                    d[v][e] += q * (dx[e] * (P.pre_w ? w[e] : 1.0f)) - c * r[e];
-                }
+            for (int e = 0; e < VEC; ++e) {
+                pre[v][e] = __builtin_fmaf(dx[e] * q, r[e], pre[v][e]);
+                d[v][e] = __builtin_fmaf(q, dx[e] * xw[v][e], __builtin_fmaf(-c, r[e], d[v][e]));
+                sy[0] = __builtin_fmaf(y[v][e], y[v][e], sy[0]);
+                sy[1] = __builtin_fmaf(gw[v][e] * d[v][e] * pw[v][e], y[v][e], sy[1]);
             }
             if (P.dres && live && col(v) < H) {
                 float o[VEC];
@@ -140,22 +148,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
                 for (int e = 0; e < VEC; ++e) o[e] = P.res_scale * d[v][e];
                 store<VEC>(P.dres, P.r_f32, at0 + col(v), o);
             }
-            float g[VEC], w[VEC];
-            unpack<VEC>(yr[v], P.y_f32, y[v]);
-            unpack<VEC>(gw[v], P.w_f32, g);
-            unpack<VEC>(pw[v], P.w_f32, w);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                // d n without the row's 1 / rms(y): joined below
-                if (P.gate && !P.post_w) gate[v][e] = __builtin_fmaf(d[v][e], y[v][e], gate[v][e]);
-                if (P.post_w) {
-                    const float dn = P.gate ? g[e] * d[v][e] : d[v][e];
-                    sy[0] = __builtin_fmaf(y[v][e], y[v][e], sy[0]);
-                    sy[1] = __builtin_fmaf(dn * w[e], y[v][e], sy[1]);
-                }
-            }
         }
-        float p = 1.0f, b = 0.0f;
+        if (kAhead && i + 1 < R.rows) fetch(row + 1);
+        float p = 1.0f, b = 0.0f;   // 1 / rms(y), mean(dn post_w y) / rms(y)^3
         if (P.post_w) {
             row_reduce<TPR, 2>(sy, slot, turn);
             p = 1.0f / sqrtf(sy[0] * inv_h + P.eps);
@@ -163,27 +158,27 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float g[VEC], w[VEC], o[VEC];
-            unpack<VEC>(gw[v], P.w_f32, g);
-            unpack<VEC>(pw[v], P.w_f32, w);
+            float o[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float dn = P.gate ? g[e] * d[v][e] : d[v][e];
-                if (P.post_w) {
-                    const float yh = y[v][e] * p;
-                    if (P.gate) gate[v][e] = __builtin_fmaf(d[v][e], yh * w[e], gate[v][e]);
-                    post[v][e] = __builtin_fmaf(dn, yh, post[v][e]);
-                    o[e] = p * (dn * w[e]) - b * y[v][e];
-                } else {
-                    o[e] = dn;
-                }
+                dyh[v][e] = __builtin_fmaf(d[v][e], y[v][e] * p, dyh[v][e]);
+                o[e] = __builtin_fmaf(p, gw[v][e] * d[v][e] * pw[v][e], -b * y[v][e]);
             }
             if (P.dy && live && col(v) < H) store<VEC>(P.dy, P.y_f32, at0 + col(v), o);
-            // the last row of a gate that lies within the run
-            if (P.dgate && !R.per_gate && live && ((row + 1) % P.gate_div == 0 || row + 1 == P.T)) {
-                if (col(v) < H) store<VEC>(P.dgate, 1, (size_t)(row / P.gate_div) * H + col(v), gate[v]);
+        }
+        if (live && (row + 1 == end || (P.gate && (row + 1) % P.gate_div == 0))) {
+            // the gate's last row here: its gradient, or this run's share of it
+            float* to = !P.dgate ? nullptr : R.per_gate ? part_gate + (size_t)wk * H : P.dgate + (size_t)(row / P.gate_div) * H;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) gate[v][e] = 0.0f;
+            for (int v = 0; v < NV; ++v) {
+                float o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    o[e] = pw[v][e] * dyh[v][e];
+                    post[v][e] = __builtin_fmaf(gw[v][e], dyh[v][e], post[v][e]);
+                    dyh[v][e] = 0.0f;
+                }
+                if (to && col(v) < H) store<VEC>(to, 1, (size_t)col(v), o);
             }
         }
     }
@@ -194,7 +189,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
                 const size_t at = (size_t)wk * H + col(v);
                 if (part_pre) store<VEC>(part_pre, 1, at, pre[v]);
                 if (part_post) store<VEC>(part_post, 1, at, post[v]);
-                if (part_gate) store<VEC>(part_gate, 1, at, gate[v]);
+                if (part_gate && first >= end) store<VEC>(part_gate, 1, at, post[v]);   // no rows: zeros
             }
 }
 
@@ -215,6 +210,7 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(int H, Runs R, const floa
     const int w1 = what < 2 ? R.workers : min(w0 + R.per_gate, R.workers);
     float s = 0.0f;
     if (col < H)
+#pragma unroll 8
         for (int w = w0 + sl; w < w1; w += 8) s += part[(size_t)w * H + col];
     sums[sl][c] = s;
     __syncthreads();
@@ -225,23 +221,23 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(int H, Runs R, const floa
     }
 }
 
-// Runs to aim for: one for each of the 256 CUs where a row takes 1024 threads,
+// Runs to aim for: one for each of the 256 CUs where a row takes 512 threads or more,
 // else two.
-inline int want_workers(int threads_per_row) { return threads_per_row >= 1024 ? 256 : 512; }
+inline int want_workers(int threads_per_row) { return threads_per_row >= 512 ? 256 : 512; }
 
 // Threads per row, chunks per thread and elements per chunk: the row, the
 // weights and the gradients of its columns all stay in registers.
 struct Shape {
     int tpr, nv;
-    bool vec;
+    bool vec, wide;
 };
-inline Shape shape_of(int H, bool vec) {
+inline Shape shape_of(int H, bool vec, bool wide) {
     const int units = vec ? H / 8 : H;
-    if (units <= 64) return {64, 1, vec};
-    if (units <= 256) return {256, 1, vec};
-    if (units <= 1024) return {1024, 1, vec};
-    if (vec) return {1024, 2, vec};
-    return {1024, units <= 4096 ? 4 : 16, vec};
+    if (units <= 64) return {64, 1, vec, wide};
+    if (units <= 256) return {256, 1, vec, wide};
+    if (vec) return {units <= 1024 ? 512 : 1024, 2, vec, wide};
+    if (units <= 1024) return {1024, 1, vec, wide};
+    return {1024, units <= 4096 ? 4 : 16, vec, wide};
 }
 
 inline int gate_rows(const NormProblem& p) { return p.gate ? (p.gate_div < p.T ? p.gate_div : p.T) : (p.T > 0 ? p.T : 1); }
@@ -251,8 +247,10 @@ inline long most_workers(int T, int H, int gate_div) {
     long most = 0;
     for (int vec = 0; vec < 2; ++vec) {
         if (vec && H % 8) continue;
-        const Runs r = runs_of(T, gate_div, want_workers(shape_of(H, vec).tpr));
-        most = r.workers > most ? r.workers : most;
+        for (int wide = 0; wide < 2; ++wide) {
+            const Runs r = runs_of(T, gate_div, want_workers(shape_of(H, vec, wide).tpr));
+            most = r.workers > most ? r.workers : most;
+        }
     }
     return most;
 }
@@ -272,7 +270,8 @@ hipError_t launch_norm_backward(const NormProblem& p0, void* ws, hipStream_t s) 
     p.gate_div = gd;
     const bool vec = p.H % 8 == 0 && rows16(p.dx) && rows16(p.dr) && rows16(p.y) && rows16(p.r) && rows16(p.post_w) &&
                      rows16(p.gate) && rows16(p.pre_w) && rows16(p.dy) && rows16(p.dres) && rows16(p.dgate);
-    const Shape sh = shape_of(p.H, vec);
+    const bool wide = !vec || p.y_f32 || p.r_f32 || p.x_f32;
+    const Shape sh = shape_of(p.H, vec, wide);
     Runs R{0, 1, 0};
     float *pre = nullptr, *post = nullptr, *gate = nullptr;
     if (p.T > 0) {
@@ -283,11 +282,12 @@ hipError_t launch_norm_backward(const NormProblem& p0, void* ws, hipStream_t s) 
         if (p.dgate && R.per_gate) gate = (float*)((uint8_t*)ws + 2 * step);
         const int threads = sh.tpr < 256 ? 256 : sh.tpr, per = threads / sh.tpr;
         const unsigned grid = (unsigned)((R.workers + per - 1) / per);
-#define X(TPR, NV, VEC)                                                                                \
-    if (sh.tpr == TPR && sh.nv == NV && (sh.vec ? 8 : 1) == VEC)                                       \
-        norm_grad_kernel<TPR, NV, VEC><<<dim3(grid), dim3(threads), 0, s>>>(p, R, pre, post, gate);
-        X(64, 1, 8) X(256, 1, 8) X(1024, 1, 8) X(1024, 2, 8)
-        X(64, 1, 1) X(256, 1, 1) X(1024, 1, 1) X(1024, 4, 1) X(1024, 16, 1)
+#define X(TPR, NV, VEC, WIDE)                                                                          \
+    if (sh.tpr == TPR && sh.nv == NV && (sh.vec ? 8 : 1) == VEC && sh.wide == WIDE)                    \
+        norm_grad_kernel<TPR, NV, VEC, WIDE><<<dim3(grid), dim3(threads), 0, s>>>(p, R, pre, post, gate);
+        X(64, 1, 8, false) X(64, 1, 8, true) X(256, 1, 8, false) X(256, 1, 8, true)
+        X(512, 2, 8, false) X(512, 2, 8, true) X(1024, 2, 8, false) X(1024, 2, 8, true)
+        X(64, 1, 1, true) X(256, 1, 1, true) X(1024, 1, 1, true) X(1024, 4, 1, true) X(1024, 16, 1, true)
 #undef X
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
