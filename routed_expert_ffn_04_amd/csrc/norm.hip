@@ -14,35 +14,34 @@
 namespace moe {
 namespace norm {
 
-template <int TPR, int NV, int VEC, bool WIDE>
+template <int TPR, int NV, bool WIDE, bool RAGGED>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem P, int rows_per_worker) {
     constexpr int kThreads = TPR < 256 ? 256 : TPR, kWorkers = kThreads / TPR;
-    typedef Raw<VEC, WIDE> Row;
+    typedef Raw<WIDE> Row;
     __shared__ __attribute__((aligned(16))) float slot[kThreads / 16 * 4];
     int turn = 0;
     const int t = threadIdx.x % TPR;
     const int H = P.H;
     const long first = ((long)blockIdx.x * kWorkers + threadIdx.x / TPR) * rows_per_worker;
-    auto col = [&](int v) { return (v * TPR + t) * VEC; };
+    auto col = [&](int v) { return (v * TPR + t) * kVec; };
     auto fetch = [&](long row, Row(&y)[NV], Row(&r)[NV]) __attribute__((always_inline)) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const bool in = row < P.T && col(v) < H;
-            const size_t at = (size_t)(in ? row : 0) * H + col(v);
-            y[v] = load<VEC, WIDE>(P.y, P.y_f32, at, in);
-            r[v] = load<VEC, WIDE>(P.res, P.r_f32, at, in && P.res);
+            const int in = row < P.T ? H - col(v) : 0;
+            const size_t at = (size_t)(row < P.T ? row : 0) * H + col(v);
+            y[v] = load<WIDE, RAGGED>(P.y, P.y_f32, at, in);
+            r[v] = load<WIDE, RAGGED>(P.res, P.r_f32, at, P.res ? in : 0);
         }
     };
 
     Row yr[NV], rr[NV];
-    float pw[NV][VEC], gw[NV][VEC], xw[NV][VEC];
+    float pw[NV][kVec], gw[NV][kVec], xw[NV][kVec];
     fetch(first, yr, rr);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const bool in = col(v) < H;
-        weights<VEC>(P.post_w, P.w_f32, col(v), in, pw[v]);
-        weights<VEC>(P.pre_w, P.w_f32, col(v), in, xw[v]);
-        weights<VEC>(nullptr, 0, 0, false, gw[v]);
+        weights<RAGGED>(P.post_w, P.w_f32, col(v), H - col(v), pw[v]);
+        weights<RAGGED>(P.pre_w, P.w_f32, col(v), H - col(v), xw[v]);
+        weights<RAGGED>(nullptr, 0, 0, 0, gw[v]);
     }
     // every worker of the workgroup makes the same number of turns (barriers)
     for (int i = 0; i < rows_per_worker; ++i) {
@@ -53,9 +52,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem
         if (P.gate && live && (i == 0 || row % P.gate_div == 0)) {
             const size_t g0 = (size_t)(row / P.gate_div) * H;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) weights<VEC>(P.gate, P.w_f32, g0 + col(v), col(v) < H, gw[v]);
+            for (int v = 0; v < NV; ++v) weights<RAGGED>(P.gate, P.w_f32, g0 + col(v), H - col(v), gw[v]);
         }
-        float n[NV][VEC], r[NV][VEC];
+        float n[NV][kVec], r[NV][kVec];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             unpack(yr[v], P.y_f32, n[v]);
@@ -68,7 +67,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) ss[0] = __builtin_fmaf(n[v][e], n[v][e], ss[0]);
+                for (int e = 0; e < kVec; ++e) ss[0] = __builtin_fmaf(n[v][e], n[v][e], ss[0]);
             row_reduce<TPR, 1>(ss, slot, turn);
             p = 1.0f / sqrtf(ss[0] / (float)H + P.eps);
         }
@@ -76,11 +75,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+            for (int e = 0; e < kVec; ++e) {
                 n[v][e] = __builtin_fmaf(P.res_scale, r[v][e], n[v][e] * p * pw[v][e] * gw[v][e]);
                 ss[0] = __builtin_fmaf(n[v][e], n[v][e], ss[0]);
             }
-            if (P.r_out && live && col(v) < H) store<VEC>(P.r_out, P.r_f32, at0 + col(v), n[v]);
+            if (P.r_out && live && col(v) < H) store<RAGGED>(P.r_out, P.r_f32, at0 + col(v), n[v], H - col(v));
         }
         if (!P.x_out) continue;
         row_reduce<TPR, 1>(ss, slot, turn);
@@ -89,11 +88,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+            for (int e = 0; e < kVec; ++e) {
                 n[v][e] = n[v][e] * q * xw[v][e];
                 if (P.x_scale) amax[0] = fmaxf(amax[0], fabsf(n[v][e]));
             }
-            if (!P.x_scale && live && col(v) < H) store<VEC>(P.x_out, P.x_f32, at0 + col(v), n[v]);
+            if (!P.x_scale && live && col(v) < H) store<RAGGED>(P.x_out, P.x_f32, at0 + col(v), n[v], H - col(v));
         }
         if (!P.x_scale) continue;
         row_reduce<TPR, 1, true>(amax, slot, turn);
@@ -103,13 +102,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem
         for (int v = 0; v < NV; ++v) {
             if (!live || col(v) >= H) continue;
             int8_t* o = (int8_t*)P.x_out + at0 + col(v);
-            if constexpr (VEC == 8) {
+            if (!RAGGED) {
                 uint32_t w[2] = {0, 0};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e / 4] |= i8_code(n[v][e], s) << (8 * (e % 4));
+                for (int e = 0; e < kVec; ++e) w[e / 4] |= i8_code(n[v][e], s) << (8 * (e % 4));
                 *(uint2*)o = make_uint2(w[0], w[1]);
             } else {
-                *o = (int8_t)i8_code(n[v][0], s);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (col(v) + e < H) o[e] = (int8_t)i8_code(n[v][e], s);
             }
         }
     }
@@ -119,24 +120,25 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem
 
 hipError_t launch_norm(const NormProblem& p, hipStream_t s) {
     using namespace norm;
-    const bool vec = p.H % 8 == 0 && rows16(p.y) && rows16(p.res) && rows16(p.post_w) && rows16(p.gate) &&
-                     rows16(p.pre_w) && rows16(p.r_out) && ((uintptr_t)p.x_out & (p.x_scale ? 7u : 15u)) == 0;
+    const bool ragged = p.H % kVec || !rows16(p.y) || !rows16(p.res) || !rows16(p.post_w) || !rows16(p.gate) ||
+                        !rows16(p.pre_w) || !rows16(p.r_out) || ((uintptr_t)p.x_out & (p.x_scale ? 7u : 15u));
     const bool wide = p.y_f32 || (p.res && p.r_f32);
-    const int units = vec ? p.H / 8 : p.H;
+    const int units = (p.H + kVec - 1) / kVec;
     // The narrowest shape that holds a row; runs that give every CU PERCU workgroups, or one row each.
-#define X(TPR, NV, VEC, WIDE, PERCU)                                                                            \
-    if (vec == (VEC == 8) && (VEC == 1 || wide == WIDE) && units <= TPR * NV) {                                 \
-        constexpr int threads = TPR < 256 ? 256 : TPR, workers = threads / TPR;                                 \
-        const long most = (long)PERCU * 256 * workers;                                                          \
-        const int run = (int)((p.T + most - 1) / most);                                                         \
-        const unsigned grid = (unsigned)(((long)p.T + (long)run * workers - 1) / ((long)run * workers));        \
-        norm_kernel<TPR, NV, VEC, WIDE><<<dim3(grid), dim3(threads), 0, s>>>(p, run);                           \
-        return hipGetLastError();                                                                               \
+#define Y(TPR, NV, WIDE, RAGGED, PERCU)                                                                  \
+    if (ragged == RAGGED && wide == WIDE && units <= TPR * NV) {                                         \
+        constexpr int threads = TPR < 256 ? 256 : TPR, workers = threads / TPR;                          \
+        const long most = (long)PERCU * 256 * workers;                                                   \
+        const int run = (int)((p.T + most - 1) / most);                                                  \
+        const unsigned grid = (unsigned)(((long)p.T + (long)run * workers - 1) / ((long)run * workers)); \
+        norm_kernel<TPR, NV, WIDE, RAGGED><<<dim3(grid), dim3(threads), 0, s>>>(p, run);                 \
+        return hipGetLastError();                                                                        \
     }
-    X(64, 1, 8, false, 8) X(64, 1, 8, true, 8) X(256, 1, 8, false, 8) X(256, 1, 8, true, 8)
-    X(512, 2, 8, false, 2) X(512, 2, 8, true, 2) X(1024, 2, 8, false, 1) X(1024, 2, 8, true, 1)
-    X(64, 1, 1, true, 8) X(256, 1, 1, true, 8) X(256, 4, 1, true, 4) X(1024, 4, 1, true, 2) X(1024, 16, 1, true, 1)
+#define X(TPR, NV, PERCU) \
+    Y(TPR, NV, false, false, PERCU) Y(TPR, NV, true, false, PERCU) Y(TPR, NV, false, true, PERCU) Y(TPR, NV, true, true, PERCU)
+    X(64, 1, 8) X(256, 1, 8) X(512, 2, 2) X(1024, 2, 1)
 #undef X
+#undef Y
     return hipErrorInvalidValue;
 }
 

@@ -1,5 +1,5 @@
 // What the norm kernels share: a row held in registers by TPR consecutive
-// threads, eight (or one) neighbouring elements at a time, and sums over a row.
+// threads, eight neighbouring elements at a time, and sums over a row.
 #pragma once
 #include <type_traits>
 
@@ -9,82 +9,122 @@
 namespace moe {
 namespace norm {
 
-// VEC consecutive elements of an fp32 or bf16 array as loaded: 16 or 32 bytes
-// (WIDE: either, else bf16 only, in half the registers).  Loading and unpacking
-// are apart so that many loads can be in flight.
-template <int VEC, bool WIDE>
+// A thread's chunk: eight neighbouring elements of an fp32 or bf16 row.  RAGGED:
+// rows that do not begin on 16 bytes (the vector accesses then carry their
+// elements' alignment only, which global memory allows) and whose last chunk is
+// shorter (element by element).
+constexpr int kVec = 8;
+
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;
+
+// The chunk as loaded: 16 or 32 bytes (WIDE: either, else bf16 only, in half the
+// registers).  Loading and unpacking are apart so that many loads can be in flight.
+template <bool WIDE>
 struct Raw {
-    static constexpr int kWords = VEC == 8 ? (WIDE ? 8 : 4) : 1;
+    static constexpr int kWords = WIDE ? 8 : 4;
     uint32_t w[kWords];
 };
 
-template <int VEC, bool WIDE>
-__device__ __forceinline__ Raw<VEC, WIDE> load(const void* p, int f32, size_t at, bool in) {
-    Raw<VEC, WIDE> r;
+template <bool RAGGED>
+__device__ __forceinline__ u32x4 get16(const void* p) {
+    if constexpr (RAGGED) return *(const u32x4_any*)p;
+    else return *(const u32x4*)p;
+}
+template <bool RAGGED>
+__device__ __forceinline__ void put16(void* p, u32x4 v) {
+    if constexpr (RAGGED) *(u32x4_any*)p = v;
+    else *(u32x4*)p = v;
+}
+
+// n: elements from `at` to the end of the row (zero or less: none, the rest of the chunk is zero).
+template <bool WIDE, bool RAGGED>
+__device__ __forceinline__ Raw<WIDE> load(const void* p, int f32, size_t at, int n) {
+    Raw<WIDE> r;
 #pragma unroll
     for (int e = 0; e < r.kWords; ++e) r.w[e] = 0;
-    if (!in) return r;
-    if constexpr (VEC == 8) {
-        if (WIDE && f32) {
-            const uint4* q = (const uint4*)((const float*)p + at);
-            const uint4 a = q[0], b = q[1];
-            r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
-            if constexpr (WIDE) { r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w; }
-        } else {
-            const uint4 a = *(const uint4*)((const uint16_t*)p + at);
-            r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    if (n <= 0) return r;
+    if (WIDE && f32) {
+        const float* q = (const float*)p + at;
+        if (!RAGGED || n >= kVec) {
+            const u32x4 a = get16<RAGGED>(q), b = get16<RAGGED>(q + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                r.w[e] = a[e];
+                if constexpr (WIDE) r.w[4 + e] = b[e];
+            }
+        } else if constexpr (WIDE) {
+#pragma unroll
+            for (int e = 0; e < kVec - 1; ++e)
+                if (e < n) r.w[e] = __float_as_uint(q[e]);
         }
     } else {
-        r.w[0] = f32 ? ((const uint32_t*)p)[at] : (uint32_t)((const uint16_t*)p)[at];
+        const uint16_t* q = (const uint16_t*)p + at;
+        if (!RAGGED || n >= kVec) {
+            const u32x4 a = get16<RAGGED>(q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r.w[e] = a[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec - 1; ++e)
+                if (e < n) r.w[e / 2] |= (uint32_t)q[e] << (16 * (e % 2));
+        }
     }
     return r;
 }
 
-template <int VEC, bool WIDE>
-__device__ __forceinline__ void unpack(const Raw<VEC, WIDE>& r, int f32, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        if constexpr (WIDE) {
-            if (f32) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) v[e] = __uint_as_float(r.w[e]);
-                return;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = bf16_bits_to_f32(r.w[e] & 0xFFFFu);
-            v[2 * e + 1] = __uint_as_float(r.w[e] & 0xFFFF0000u);
-        }
-    } else {
-        v[0] = f32 ? __uint_as_float(r.w[0]) : bf16_bits_to_f32(r.w[0]);
-    }
-}
-
-template <int VEC>
-__device__ __forceinline__ void store(void* p, int f32, size_t at, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
+template <bool WIDE>
+__device__ __forceinline__ void unpack(const Raw<WIDE>& r, int f32, float (&v)[kVec]) {
+    if constexpr (WIDE) {
         if (f32) {
-            float4* q = (float4*)((float*)p + at);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
-            *(uint4*)((uint16_t*)p + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < kVec; ++e) v[e] = __uint_as_float(r.w[e]);
+            return;
         }
-    } else {
-        if (f32) ((float*)p)[at] = v[0];
-        else ((uint16_t*)p)[at] = (uint16_t)f32_to_bf16_bits(v[0]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = bf16_bits_to_f32(r.w[e] & 0xFFFFu);
+        v[2 * e + 1] = __uint_as_float(r.w[e] & 0xFFFF0000u);
     }
 }
 
-// VEC weights as floats; ones where there are none.
-template <int VEC>
-__device__ __forceinline__ void weights(const void* p, int f32, size_t at, bool in, float (&w)[VEC]) {
+// n as in load, above zero.
+template <bool RAGGED>
+__device__ __forceinline__ void store(void* p, int f32, size_t at, const float (&v)[kVec], int n) {
+    if (f32) {
+        float* q = (float*)p + at;
+        if (!RAGGED || n >= kVec) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) w[e] = 1.0f;
-    if (p && in) unpack(load<VEC, true>(p, f32, at, true), f32, w);
+            for (int h = 0; h < 2; ++h)
+                put16<RAGGED>(q + 4 * h, u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                                               __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])});
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec - 1; ++e)
+                if (e < n) q[e] = v[e];
+        }
+    } else {
+        uint16_t* q = (uint16_t*)p + at;
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+        if (!RAGGED || n >= kVec) {
+            put16<RAGGED>(q, w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec - 1; ++e)
+                if (e < n) q[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+        }
+    }
+}
+
+// Weights as floats; ones where there are none.
+template <bool RAGGED>
+__device__ __forceinline__ void weights(const void* p, int f32, size_t at, int n, float (&w)[kVec]) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) w[e] = 1.0f;
+    if (p && n > 0) unpack(load<true, RAGGED>(p, f32, at, n), f32, w);
 }
 
 template <bool MAX>
