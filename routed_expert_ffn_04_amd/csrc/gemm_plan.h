@@ -9,18 +9,20 @@ namespace gemm {
 
 struct Plan {
     int few;             // the kernel for a few rows
-    int big;             // 256 x 256 tiles, else 128 x 128
+    int edge;            // 256 x 256, 128 x 128 or 64 x 64 tiles
     int splits, kspan;
     int workgroups;
 };
 
-// The tiling with the least estimated time.  In us, from whole products of 4096
-// columns and 14336 bytes of k on 256 CUs: a stage takes 1.6 in the 256-row tiles
-// (one workgroup per CU) and 0.7 in the 128-row tiles with one workgroup per
-// CU, 1.3 with two; a round of tiles costs 10 (3) besides its stages for filling
-// the ring and writing the outputs; splitting k costs a launch, 4, and the
-// partial sums written and read at 4 TB/s.  1024 x 4096 (gate/up of 2048): one
-// round of 128-row tiles 77 us, of 256-row tiles on a quarter of the CUs 190.
+// Estimated time of wg workgroups of `span` stages each, in us.
+inline double tiling_us(int edge, long wg, int span) {
+    auto rounds = [&](long at_once) { return (double)((wg + at_once - 1) / at_once); };
+    if (edge == 256) return rounds(256) * (span * 1.6 + 10);
+    if (edge == 128) return wg <= 256 ? span * 0.7 + 3 : rounds(512) * (span * 1.3 + 3);
+    return wg <= 256 ? span * 0.4 + 3 : wg <= 512 ? span * 0.5 + 3 : rounds(1024) * (span * 0.9 + 3);
+}
+
+// The tiling with the least estimated time.
 // mma_cols: MFMA columns of the product (gate/up: both matrices' columns).
 // rows: both operands have k contiguous.
 inline Plan plan_tiles(long M, long mma_cols, int K, int stage_elems, bool rows) {
@@ -32,18 +34,16 @@ inline Plan plan_tiles(long M, long mma_cols, int K, int stage_elems, bool rows)
         return best;
     }
     double least = 0;
-    for (int big = 0; big < 2; ++big) {
-        const long edge = big ? 256 : 128;
+    for (int edge = 64; edge <= 256; edge *= 2) {
         const long tiles = ((M + edge - 1) / edge) * ((mma_cols + edge - 1) / edge);
         for (int s = 1; s <= 16 && (s == 1 || (stages / s >= 2 && tiles * s <= 512)); ++s) {
             const int span = (stages + s - 1) / s, n = (stages + span - 1) / span;
             const long wg = tiles * n;
-            double us = big ? (double)((wg + 255) / 256) * (span * 1.6 + 10)
-                            : wg <= 256 ? span * 0.7 + 3 : (double)((wg + 511) / 512) * (span * 1.3 + 3);
+            double us = tiling_us(edge, wg, span);
             if (n > 1) us += 4 + (double)n * M * mma_cols * 8 / 4e6;
             if (least == 0 || us < least) {
                 least = us;
-                best.big = big;
+                best.edge = edge;
                 best.splits = n;
                 best.kspan = span * stage_elems;
                 best.workgroups = (int)(wg < 0x7fffffff ? wg : 0x7fffffff);
@@ -159,7 +159,11 @@ hipError_t launch_reduce(const Args& G, const float* part, int splits, hipStream
 // (4096 x 2048 dh: 146 us against 193 with ten).
 template <int E, int LA, int LB, int EPI, bool GU>
 hipError_t launch_tiling(const Args& G, const Plan& p, hipStream_t s) {
-    if (p.big) return launch_tiles<E, LA, LB, EPI, GU, 256, 256, 5>(G, s);
+    if (p.edge == 256) return launch_tiles<E, LA, LB, EPI, GU, 256, 256, 5>(G, s);
+    if (p.edge == 64) {
+        if (p.workgroups <= 512) return launch_tiles<E, LA, LB, EPI, GU, 64, 64, 10>(G, s);
+        return launch_tiles<E, LA, LB, EPI, GU, 64, 64, 5>(G, s);
+    }
     if (p.workgroups <= 256) return launch_tiles<E, LA, LB, EPI, GU, 128, 128, 10>(G, s);
     return launch_tiles<E, LA, LB, EPI, GU, 128, 128, 5>(G, s);
 }

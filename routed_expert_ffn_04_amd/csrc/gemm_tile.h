@@ -86,8 +86,12 @@ static __device__ __align__(16) const uint32_t kZeros[4] = {0, 0, 0, 0};
 // Chunk key of row r of a kRow half-stage (128-byte rows): chunk c sits at
 // position c ^ key, which spreads the fragment reads over all banks.
 __device__ __forceinline__ int row_key(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-// The same of row k of a kCol half-stage (2 BM-byte rows).
-__device__ __forceinline__ int col_key(int r) { return ((r & 3) << 2) | (((r >> 3) & 1) << 1); }
+// The same of row k of a kCol half-stage (2 BM-byte rows): the 32 bytes that a
+// half-wave reads of rows 8 g + 0 .. 3, g = 0, 1, fall into different banks.
+template <int BM>
+__device__ __forceinline__ int col_key(int r) {
+    return (BM == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2) | (((r >> 3) & 1) << 1);
+}
 
 template <int N>
 __device__ __forceinline__ void barrier_vm() {
@@ -121,7 +125,7 @@ struct Frag {
             for (int ks = 0; ks < 2; ++ks) off[ks] = (block0 * 16 + j) * kStage + (((4 * ks + g) ^ row_key(j)) << 4);
         } else {
             const int row = 8 * g + j / 4;
-            off[0] = row * (BMN * 2) + (block0 >> 3) * 256 + ((2 * (block0 & 7) + (j % 4) / 2) ^ col_key(row)) * 16 + (j & 1) * 8;
+            off[0] = row * (BMN * 2) + (block0 >> 3) * 256 + ((2 * (block0 & 7) + (j % 4) / 2) ^ col_key<BMN>(row)) * 16 + (j & 1) * 8;
         }
     }
     // b: block within the wave's part (kCol: block0 is a multiple of the part's blocks, so
@@ -212,18 +216,19 @@ __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& t
 }
 
 template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
-__global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM * kStage > 81920 && BM == 128 ? 1 : 2, 2))) void tile_kernel(Args G) {
-    constexpr int kThreads = BM * 2;
+__global__ __launch_bounds__(BM == 256 ? 512 : 256)
+    __attribute__((amdgpu_waves_per_eu(BM == 256 ? 2 : 163840 / (R * BM * kStage)))) void tile_kernel(Args G) {
+    constexpr int kThreads = BM == 256 ? 512 : 256;
     constexpr int EB = E == kI8 ? 1 : 2;
     constexpr int KE = kStage / EB;                            // k elements per stage
-    constexpr int WN = BN / 64, WM = (kThreads / 64) / WN;     // waves along n and m
-    constexpr int IB = BM / WM / 16, JB = 4;                   // 16 x 16 blocks of a wave
-    constexpr int LDA = BM * 8 / kThreads, LDB = BN * 8 / kThreads;   // direct loads per lane and half-stage
-    constexpr int kHalf = BM * kStage;                                // bytes of a half-stage
-    static_assert(BM == BN && LDA == 4 && LDB == 4, "square tiles");
+    constexpr int WN = BM == 256 ? 4 : 2, WM = 2;              // waves along n and m
+    constexpr int IB = BM / WM / 16, JB = BN / WN / 16;        // 16 x 16 blocks of a wave
+    constexpr int LD = BM * 8 / kThreads;                      // direct loads per lane and half-stage
+    constexpr int kHalf = BM * kStage;                         // bytes of a half-stage
+    static_assert(BM == BN && LD % 2 == 0, "square tiles");
     constexpr int kTileN = GU ? BN / 2 : BN;                   // output columns per tile
     static_assert(E == kBf16 || (LA == kRow && LB == kRow), "the transposing read is for 16-bit elements");
-    static_assert(WM * WN * 64 == kThreads && WM * IB * 16 == BM, "waves cover the tile");
+    static_assert(WM * WN * 64 == kThreads, "waves cover the tile");
 
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid % 64;
@@ -237,13 +242,13 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
     const int kn = min(G.K - k0, G.kspan);                     // k elements of this split
     const int nst = (kn + KE - 1) / KE;
 
-    // ---- the lane's share of the direct loads: four 16-byte slots in each half-stage
-    const uint8_t* pa[LDA];
-    const uint8_t* pb[LDB];
-    auto place = [&](int layout, const Operand& O, int r0, bool gu, const uint8_t*(&p)[4]) __attribute__((always_inline)) {
+    // ---- the lane's share of the direct loads: LD 16-byte slots in each half-stage
+    const uint8_t* pa[LD];
+    const uint8_t* pb[LD];
+    auto place = [&](int layout, const Operand& O, int r0, bool gu, const uint8_t*(&p)[LD]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int at = (wave * 4 + q) * 64 + lane;
+        for (int q = 0; q < LD; ++q) {
+            const int at = (wave * LD + q) * 64 + lane;
             if (layout == kRow) {
                 const int r = at / 8, c = (at % 8) ^ row_key(r);
                 const bool up = gu && r >= BN / 2;
@@ -251,7 +256,7 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
                 p[q] = (up ? O.p2 : O.p) + (size_t)row * O.ld + (size_t)k0 * EB + c * 16;
             } else {
                 constexpr int per = BM * 2 / 16;                       // slots per k row
-                const int r = at / per, c = (at % per) ^ col_key(r);
+                const int r = at / per, c = (at % per) ^ col_key<BM>(r);
                 p[q] = O.p + (size_t)(k0 + r) * O.ld + (size_t)min(r0 + c * 8, O.n - 8) * 2;
             }
         }
@@ -260,7 +265,7 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
     place(LB, G.B, n0, GU, pb);
     // k of a slot within its stage: kRow its chunk's first k, kCol its row
     const int kr = ((lane % 8) ^ (lane / 8)) * (16 / EB);             // q even; q odd: the neighbouring chunk
-    const int kc = wave * 4 * (64 / (BM / 8)) + lane / (BM / 8);      // q = 0
+    const int kc = wave * LD * (64 / (BM / 8)) + lane / (BM / 8);      // q = 0
     auto k_of = [&](int layout, int q) __attribute__((always_inline)) {
         return layout == kRow ? kr ^ ((q & 1) * (16 / EB)) : kc + q * (64 / (BM / 8));
     };
@@ -274,10 +279,10 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
 #pragma unroll
         for (int q = q0; q < q1; ++q) {
             const uint8_t* p = k_of(LA, q) < kn - ka ? pa[q] : (const uint8_t*)kZeros;
-            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)(half + (wave * 4 + q) * 1024), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)(half + (wave * LD + q) * 1024), 16, 0, 0);
             pa[q] += LA == kRow ? (size_t)kStage : (size_t)KE * G.A.ld;
         }
-        if (q1 == LDA) ka += KE;
+        if (q1 == LD) ka += KE;
     };
     auto issueB = [&](uint8_t* half, int q0, int q1) __attribute__((always_inline)) {
 #pragma unroll
@@ -285,10 +290,10 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
             const uint8_t* p = pb[q];
             if (LB == kCol) p += k_of(LB, q) >= turn_at - kb ? second : 0;
             p = k_of(LB, q) < kn - kb ? p : (const uint8_t*)kZeros;
-            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)(half + (wave * 4 + q) * 1024), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)(half + (wave * LD + q) * 1024), 16, 0, 0);
             pb[q] += LB == kRow ? (size_t)kStage : (size_t)KE * G.B.ld;
         }
-        if (q1 == LDB) kb += KE;
+        if (q1 == LD) kb += KE;
     };
 
     typename Acc<E>::type acc[IB][JB];
@@ -298,12 +303,11 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
         for (int j = 0; j < JB; ++j) acc[i][j] = typename Acc<E>::type{};
 
     const Frag<LA, BM> fa(wm * IB, lane);
-    const Frag<LB, BN> fb(wn * (GU ? 2 : 4), lane);
-    // A stage is two k-steps, each one part (128-row tiles) or two (256-row
-    // tiles: the halves of the wave's rows).  a: the rows' fragments of one
-    // part, b: the columns' of one k-step, both twice: one set multiplies while
-    // the next is read.
-    constexpr int PK = IB / 4, AH = 4, kParts = 2 * PK;
+    const Frag<LB, BN> fb(wn * (GU ? JB / 2 : JB), lane);
+    // A stage is two k-steps, each one part, or two in 256-row tiles (the halves
+    // of the wave's rows).  a: the rows' fragments of one part, b: the columns'
+    // of one k-step, both twice: one set multiplies while the next is read.
+    constexpr int AH = IB < 4 ? IB : 4, PK = IB / AH, kParts = 2 * PK;
     i32x4 a[2][AH], b[2][JB];
     auto read_a = [&](const uint8_t* half, int part, int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
@@ -311,8 +315,8 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
     };
     auto read_b = [&](const uint8_t* half, int ks) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < JB; ++j)   // gate/up: two blocks of gate columns, two of up columns
-            b[ks][j] = fb.read(half + (GU && j >= 2 ? BN / 2 * kStage : 0), GU ? j & 1 : j, ks);
+        for (int j = 0; j < JB; ++j)   // gate/up: half of the blocks gate columns, half up columns
+            b[ks][j] = fb.read(half + (GU && j >= JB / 2 ? BN / 2 * kStage : 0), GU ? j % (JB / 2) : j, ks);
     };
     auto mma = [&](int part, int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
@@ -330,17 +334,17 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
     // them.
     auto step = [&](int part, const uint8_t* ha, const uint8_t* hb, auto&& load) __attribute__((always_inline)) {
         const int next = (part + 1) % kParts;
-        mma(part, 0, 1);
+        mma(part, 0, AH / 4);
         if (next % PK == 0) read_b(hb, next / PK);
         read_a(ha, next, 0, AH / 2);
         __builtin_amdgcn_sched_barrier(0);
-        mma(part, 1, 2);
+        mma(part, AH / 4, AH / 2);
         read_a(ha, next, AH / 2, AH);
         __builtin_amdgcn_sched_barrier(0);
-        mma(part, 2, 3);
+        mma(part, AH / 2, AH - 1);
         load();
         __builtin_amdgcn_sched_barrier(0);
-        mma(part, 3, 4);
+        mma(part, AH - 1, AH);
     };
     // One stage from its halves rA, rB, beginning with the previous stage's
     // last part; w0 and w1 are the halves that stage has left.  The restrict
@@ -349,14 +353,14 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
     // transposing read.
     auto turn = [&](uint8_t* __restrict__ w0, uint8_t* __restrict__ w1, const uint8_t* __restrict__ rA,
                     const uint8_t* __restrict__ rB) __attribute__((always_inline)) {
-        // the halves' four loads a lane each, in the order of the ring
+        // the halves' loads, in the order of the ring
         auto fill = [&](int q0, int q1) __attribute__((always_inline)) {
 #pragma unroll
             for (int q = q0; q < q1; q += 2)
-                if ((q < 4) == (R % 2 == 1)) issueB(q < 4 ? w0 : w1, q % 4, q % 4 + 2);
-                else issueA(q < 4 ? w0 : w1, q % 4, q % 4 + 2);
+                if ((q < LD) == (R % 2 == 1)) issueB(q < LD ? w0 : w1, q % LD, q % LD + 2);
+                else issueA(q < LD ? w0 : w1, q % LD, q % LD + 2);
         };
-        constexpr int L = 8 / kParts;
+        constexpr int L = 2 * LD / kParts;
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
             step((p + kParts - 1) % kParts, rA, rB, [&]() __attribute__((always_inline)) { fill(p * L, p * L + L); });
@@ -366,22 +370,22 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
                      __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 2; h < R; ++h)
-            if (h % 2) issueB(w + (h - 2) * kHalf, 0, 4);
-            else issueA(w + (h - 2) * kHalf, 0, 4);
-        barrier_vm<(R - 2) * 4>();   // the first two halves
+            if (h % 2) issueB(w + (h - 2) * kHalf, 0, LD);
+            else issueA(w + (h - 2) * kHalf, 0, LD);
+        barrier_vm<(R - 2) * LD>();   // the first two halves
         read_b(rB, 0);
         read_a(rA, 0, 0, AH);
 #pragma unroll
         for (int p = 0; p + 1 < kParts; ++p) step(p, rA, rB, none);
     };
 
-    issueA(smem, 0, 4);
-    issueB(smem + kHalf, 0, 4);
+    issueA(smem, 0, LD);
+    issueB(smem + kHalf, 0, LD);
     start(smem + 2 * kHalf, smem, smem + kHalf);
     int u = 0;   // slot of the previous stage's A half; the ring's order is A B A B A ...
     auto slot = [&](int i) __attribute__((always_inline)) { return smem + (u + i >= R ? u + i - R : u + i) * kHalf; };
     for (int s = 1; s < nst; ++s) {
-        barrier_vm<(R - 4) * 4>();   // stage s has landed
+        barrier_vm<(R - 4) * LD>();   // stage s has landed
         uint8_t* w0 = slot(0);
         uint8_t* w1 = slot(1);
         const uint8_t* rA = slot(2);
@@ -395,14 +399,17 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
 
     // ---- epilogue.  acc[i][j][v]: m = 16 i + l % 16, n = 16 j + 4 (l / 16) + v of
     // the wave's part.  32 rows at a time pass through the wave's own piece of LDS
-    // (rows of 64 words and a 16-byte pad, free of bank conflicts both ways), so
-    // that global accesses are whole row pieces.
-    constexpr int RS = 64 * 4 + 16;
+    // (rows padded by 16 bytes, free of bank conflicts both ways), so that global
+    // accesses are whole row pieces.
+    constexpr int WC = JB * 16;                          // MFMA columns of a wave
+    constexpr int RS = WC * 4 + 16;
+    constexpr int RL = (GU ? WC / 2 : WC) / 8;           // lanes a row, eight outputs each
+    constexpr int RP = 64 / RL, kPass = 32 / RP;         // rows a pass
     uint8_t* piece = smem + wave * 32 * RS;
-    const int nw = n0 + wn * (GU ? 32 : 64);
+    const int nw = n0 + wn * (GU ? WC / 2 : WC);
     // A lane's eight columns are the same in every pass: their scales are read once.
-    const int nl = nw + (lane % 8) * 8;
-    float wsv[8], bv[8], xsv[IB / 2][4];
+    const int nl = nw + (lane % RL) * 8;
+    float wsv[8], bv[8], xsv[IB / 2][kPass];
     if constexpr (EPI == kEpiI8) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -413,19 +420,19 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
 #pragma unroll
         for (int ib = 0; ib < IB / 2; ++ib)
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-                xsv[ib][p] = G.xs[min(m0 + wm * IB * 16 + ib * 32 + p * 8 + lane / 8, G.M - 1)];
+            for (int p = 0; p < kPass; ++p)
+                xsv[ib][p] = G.xs[min(m0 + wm * IB * 16 + ib * 32 + p * RP + lane / RL, G.M - 1)];
     }
 #pragma unroll
     for (int ib = 0; ib < IB / 2; ++ib) {
         const int mb = m0 + wm * IB * 16 + ib * 32;
         if (mb >= G.M) break;
         // the saved pre-activations of the 32 rows, read while the accumulators pass through LDS
-        float4 gv[4][2], uv[4][2];
+        float4 gv[kPass][2], uv[kPass][2];
         if constexpr (EPI == kEpiGrad) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const size_t at = (size_t)min(mb + p * 8 + lane / 8, G.M - 1) * (2 * (size_t)G.N) + min(nl, G.N - 8);
+            for (int p = 0; p < kPass; ++p) {
+                const size_t at = (size_t)min(mb + p * RP + lane / RL, G.M - 1) * (2 * (size_t)G.N) + min(nl, G.N - 8);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     gv[p][e] = *(const float4*)(G.gu + at + 4 * e);
@@ -446,14 +453,14 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
             v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w; v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
         };
         if constexpr (GU) {
-            // 32 gate and 32 up columns: 4 lanes a row, 16 rows a pass
+            // WC / 2 gate columns, then as many up columns
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int row = p * 16 + lane / 4, c = (lane % 4) * 8;
+            for (int p = 0; p < kPass; ++p) {
+                const int row = p * RP + lane / RL, c = (lane % RL) * 8;
                 const int m = mb + row, n = nw + c;
                 float g[8], u[8], h[8];
                 words(row, c, g);
-                words(row, 32 + c, u);
+                words(row, WC / 2 + c, u);
                 if (m < G.M && n < G.N) {
                     if constexpr (EPI == kEpiPart) {
                         float* o = (float*)G.out + ((size_t)split * G.M + m) * (2 * (size_t)G.N) + n;
@@ -478,10 +485,9 @@ __global__ __launch_bounds__(BM * 2) __attribute__((amdgpu_waves_per_eu(R * BM *
                 }
             }
         } else {
-            // 64 columns: 8 lanes a row, 8 rows a pass
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int row = p * 8 + lane / 8, c = (lane % 8) * 8;
+            for (int p = 0; p < kPass; ++p) {
+                const int row = p * RP + lane / RL, c = (lane % RL) * 8;
                 const int m = mb + row, n = nw + c;
                 float v[8];
                 words(row, c, v);
@@ -532,7 +538,7 @@ hipError_t launch_tiles(Args G, hipStream_t s) {
     G.nt = (G.N + (GU ? BN / 2 : BN) - 1) / (GU ? BN / 2 : BN);
     const long total = (long)G.mt * G.nt * G.splits;
     if (total <= 0 || total > 0x7fffffffL) return hipErrorInvalidValue;
-    k<<<dim3((unsigned)total), dim3(BM * 2), lds, s>>>(G);
+    k<<<dim3((unsigned)total), dim3(BM == 256 ? 512 : 256), lds, s>>>(G);
     return hipGetLastError();
 }
 

@@ -96,17 +96,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem
         }
         if (!P.x_scale) continue;
         row_reduce<TPR, 1, true>(amax, slot, turn);
-        const float s = i8_scale(amax[0]);
+        const float s = i8_scale(amax[0]), inv = 1.0f / s;
         if (live && t == 0) P.x_scale[row] = s;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             if (!live || col(v) >= H) continue;
             int8_t* o = (int8_t*)P.x_out + at0 + col(v);
             if (!RAGGED) {
-                uint32_t w[2] = {0, 0};
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) w[e / 4] |= i8_code(n[v][e], s) << (8 * (e % 4));
-                *(uint2*)o = make_uint2(w[0], w[1]);
+                *(uint2*)o = i8_codes8(n[v], s, inv);
             } else {
 #pragma unroll
                 for (int e = 0; e < kVec; ++e)

@@ -10,6 +10,10 @@
 // to the workspace and a second kernel adds them in a fixed order, so results
 // do not depend on timing.  Gates shorter than a run lie within one run, which
 // writes their gradients itself.
+//
+// dy and dres are stored past the caches, where they would push out rows that
+// are still to be read: 4096 x 7168 in bf16, 80 us against 87 (the forward step is
+// 41 us against 49 with such stores and does without).
 #include "norm_row.h"
 
 namespace moe {
@@ -128,7 +132,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
                 float o[kVec];
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) o[e] = P.res_scale * d[v][e];
-                store<RAGGED>(P.dres, P.r_f32, at0 + col(v), o, H - col(v));
+                store<RAGGED, true>(P.dres, P.r_f32, at0 + col(v), o, H - col(v));
             }
         }
         if (kAhead && i + 1 < R.rows) fetch(row + 1);
@@ -146,7 +150,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
                 dyh[v][e] = __builtin_fmaf(d[v][e], y[v][e] * p, dyh[v][e]);
                 o[e] = __builtin_fmaf(p, gw[v][e] * d[v][e] * pw[v][e], -b * y[v][e]);
             }
-            if (P.dy && live && col(v) < H) store<RAGGED>(P.dy, P.y_f32, at0 + col(v), o, H - col(v));
+            if (P.dy && live && col(v) < H) store<RAGGED, true>(P.dy, P.y_f32, at0 + col(v), o, H - col(v));
         }
         if (live && (row + 1 == end || (P.gate && (row + 1) % P.gate_div == 0))) {
             // the gate's last row here: its gradient, or this run's share of it

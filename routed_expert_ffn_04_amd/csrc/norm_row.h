@@ -31,9 +31,10 @@ __device__ __forceinline__ u32x4 get16(const void* p) {
     if constexpr (RAGGED) return *(const u32x4_any*)p;
     else return *(const u32x4*)p;
 }
-template <bool RAGGED>
+template <bool RAGGED, bool STREAM>
 __device__ __forceinline__ void put16(void* p, u32x4 v) {
     if constexpr (RAGGED) *(u32x4_any*)p = v;
+    else if constexpr (STREAM) __builtin_nontemporal_store(v, (u32x4*)p);
     else *(u32x4*)p = v;
 }
 
@@ -89,15 +90,15 @@ __device__ __forceinline__ void unpack(const Raw<WIDE>& r, int f32, float (&v)[k
     }
 }
 
-// n as in load, above zero.
-template <bool RAGGED>
+// n as in load, above zero.  STREAM: past the caches.
+template <bool RAGGED, bool STREAM = false>
 __device__ __forceinline__ void store(void* p, int f32, size_t at, const float (&v)[kVec], int n) {
     if (f32) {
         float* q = (float*)p + at;
         if (!RAGGED || n >= kVec) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                put16<RAGGED>(q + 4 * h, u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                put16<RAGGED, STREAM>(q + 4 * h, u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
                                                __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])});
         } else {
 #pragma unroll
@@ -110,7 +111,7 @@ __device__ __forceinline__ void store(void* p, int f32, size_t at, const float (
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
         if (!RAGGED || n >= kVec) {
-            put16<RAGGED>(q, w);
+            put16<RAGGED, STREAM>(q, w);
         } else {
 #pragma unroll
             for (int e = 0; e < kVec - 1; ++e)
