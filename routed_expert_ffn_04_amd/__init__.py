@@ -377,14 +377,26 @@ def layer_noalloc(x, w_router, bias, k: int, score: str, routed: Experts, shared
 
 # ---------------------------------------------------------------- around the layer
 
+torch = None        # imported by the first call below (the boundary itself does not need it)
+_FLOATS = ()
+_CODE = {}          # torch dtype -> moe_dtype_t
+
+
+def _import_torch():
+    global torch, _FLOATS, _CODE
+    import torch as t
+    _FLOATS = (t.float32, t.bfloat16)
+    _CODE = {t.float32: F32, t.bfloat16: BF16, t.int8: I8}
+    torch = t
+
+
 def _elsewhere(device, stream):
     """None if a call with tensors on `device` can go to the current stream as
     it is, else the context in which it can: the device and `stream` (default:
     the device's current stream) made current, so that what the call allocates
     belongs to the stream that uses it."""
-    import torch
     if stream is None:
-        if torch.cuda.current_device() == device.index:
+        if torch._C._cuda_getDevice() == device.index:
             return None
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
@@ -394,7 +406,6 @@ def _elsewhere(device, stream):
 
 def _current(device) -> int:
     """Handle of the device's current stream."""
-    import torch
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -414,7 +425,6 @@ def _tensor(device, name, t, shape, dtypes):
 
 def _empty(like, shape, dtype):
     """An output; `like`: a checked tensor on its device, often of its very shape and dtype (which is quicker)."""
-    import torch
     if like.dtype is dtype and like.shape == shape:
         return torch.empty_like(like)
     return torch.empty(shape, dtype=dtype, device=like.device)
@@ -422,6 +432,8 @@ def _empty(like, shape, dtype):
 
 def _matrix(name, t):
     """(rows, columns, device) of a 2-d device tensor."""
+    if torch is None:
+        _import_torch()
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name}: expected a 2-d tensor on a GPU, got {tuple(t.shape)} on {t.device}")
     return t.shape[0], t.shape[1], t.device
@@ -440,7 +452,6 @@ def _nbytes(ws) -> int:
 
 
 def _dense_bank(bank: Experts, H: int, device):
-    import torch
     bf = (torch.bfloat16,)
     if bank.w_gate.dim() != 3:
         raise ValueError("bank: weights are [1][I][H] and [1][H][I]")
@@ -454,7 +465,6 @@ def _dense_bank(bank: Experts, H: int, device):
 def ffn(x, bank: Experts, *, want_gu: bool = False, y_dtype=None, out=None, gu=None, ws=None, stream=None):
     """The dense gated FFN block (moe_ffn) with a bf16 bank of n = 1.  Returns
     y [T][H], or (y, gu) with want_gu: gu fp32 [T][2 I], what ffn_backward needs."""
-    import torch
     T, H, dev = _matrix("x", x)
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -462,17 +472,18 @@ def ffn(x, bank: Experts, *, want_gu: bool = False, y_dtype=None, out=None, gu=N
             return ffn(x, bank, want_gu=want_gu, y_dtype=y_dtype, out=out, gu=gu, ws=ws)
     st, I = _dense_bank(bank, H, dev)
     y_dtype = out.dtype if out is not None else (y_dtype or torch.bfloat16)
-    f32 = (torch.float32,)
+    if y_dtype not in _FLOATS:
+        raise TypeError(f"ffn: y {y_dtype}")
     _tensor(dev, "x", x, (T, H), (torch.bfloat16,))
-    _tensor(dev, "out", out, (T, H), (torch.bfloat16, torch.float32))
-    _tensor(dev, "gu", gu, (T, 2 * I), f32)
+    _tensor(dev, "out", out, (T, H), _FLOATS)
+    _tensor(dev, "gu", gu, (T, 2 * I), (torch.float32,))
     if out is None:
         out = _empty(x, (T, H), y_dtype)
     if gu is None and want_gu:
         gu = torch.empty((T, 2 * I), dtype=torch.float32, device=dev)
-    L = lib()
+    L = _lib or lib()
     ws = _scratch(ws, L.moe_ffn_workspace_size(T, H, I), dev)
-    _check(L.moe_ffn(x.data_ptr(), BF16, T, ctypes.byref(st), out.data_ptr(), _dt_of(out), _ptr(gu), ws.data_ptr(),
+    _check(L.moe_ffn(x.data_ptr(), BF16, T, ctypes.byref(st), out.data_ptr(), _CODE[out.dtype], _ptr(gu), ws.data_ptr(),
                      _nbytes(ws), _current(dev)))
     return (out, gu) if want_gu else out
 
@@ -481,7 +492,6 @@ def ffn_backward(dy, x, bank: Experts, gu=None, *, need=("dx", "dw_gate", "dw_up
     """Gradients of ffn (moe_ffn_backward): (dx [T][H], dw_gate, dw_up [1][I][H],
     dw_down [1][H][I]), None for those not in `need`.  gu: what ffn returned
     (None: computed again)."""
-    import torch
     T, H, dev = _matrix("x", x)
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -497,7 +507,7 @@ def ffn_backward(dy, x, bank: Experts, gu=None, *, need=("dx", "dw_gate", "dw_up
         raise ValueError(f"need: {need}")
     likes = (x, bank.w_gate, bank.w_up, bank.w_down)
     o = tuple(torch.empty_like(t) if k in need else None for k, t in zip(names, likes))
-    L = lib()
+    L = _lib or lib()
     ws = _scratch(ws, L.moe_ffn_backward_workspace_size(T, H, I, int(gu is not None)), dev)
     _check(L.moe_ffn_backward(dy.data_ptr(), x.data_ptr(), BF16, T, ctypes.byref(st), _ptr(gu), *map(_ptr, o),
                               ws.data_ptr(), _nbytes(ws), _current(dev)))
@@ -506,7 +516,6 @@ def ffn_backward(dy, x, bank: Experts, gu=None, *, need=("dx", "dw_gate", "dw_up
 
 def _norm_params(T, H, dev, post_w, gate, gate_div, pre_w):
     """(rows of the gate, weight dtype code) after the checks."""
-    import torch
     dtype = None
     for t in (post_w, gate, pre_w):
         if t is not None:
@@ -515,16 +524,15 @@ def _norm_params(T, H, dev, post_w, gate, gate_div, pre_w):
             dtype = t.dtype
     if dtype is None:
         return 0, F32
-    fl = (torch.float32, torch.bfloat16)
     G = 0
     if gate is not None:
         if gate_div < 1:
             raise ValueError(f"gate_div={gate_div}")
         G = -(-T // gate_div)
-        _tensor(dev, "gate", gate, (G, H), fl)
-    _tensor(dev, "post_w", post_w, (H,), fl)
-    _tensor(dev, "pre_w", pre_w, (H,), fl)
-    return G, F32 if dtype is torch.float32 else BF16
+        _tensor(dev, "gate", gate, (G, H), _FLOATS)
+    _tensor(dev, "post_w", post_w, (H,), _FLOATS)
+    _tensor(dev, "pre_w", pre_w, (H,), _FLOATS)
+    return G, _CODE[dtype]
 
 
 def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: float = 1.0, pre_w=None,
@@ -534,22 +542,20 @@ def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: f
     x_dtype torch.int8 x is the pair (codes [T][H], scales [T]).  r_dtype
     defaults to res's dtype (y's without res), x_dtype to y's.  r, x: optional
     output tensors; r may be res itself."""
-    import torch
     T, H, dev = _matrix("y", y)
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
             return norm(y, res, post_w=post_w, gate=gate, gate_div=gate_div, res_scale=res_scale, pre_w=pre_w, eps=eps,
                         r_dtype=r_dtype, x_dtype=x_dtype, want_r=want_r, want_x=want_x, r=r, x=x)
-    fl = (torch.float32, torch.bfloat16)
     _, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
     r_dtype = res.dtype if res is not None else r.dtype if r is not None else (r_dtype or y.dtype)
     q, scale = x if isinstance(x, tuple) else (x, None)
     x_dtype = q.dtype if q is not None else (x_dtype or y.dtype)
-    if r_dtype not in fl or x_dtype not in fl + (torch.int8,):
+    if r_dtype not in _FLOATS or x_dtype not in _CODE:
         raise TypeError(f"norm: r {r_dtype}, x {x_dtype}")
     i8 = x_dtype == torch.int8
-    _tensor(dev, "y", y, (T, H), fl)
+    _tensor(dev, "y", y, (T, H), _FLOATS)
     _tensor(dev, "res", res, (T, H), (r_dtype,))
     _tensor(dev, "r", r, (T, H), (r_dtype,))
     _tensor(dev, "x", q, (T, H), (x_dtype,))
@@ -560,9 +566,9 @@ def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: f
         q = _empty(y, (T, H), x_dtype)
     if q is not None and i8 and scale is None:
         scale = torch.empty((T,), dtype=torch.float32, device=dev)
-    _check(lib().moe_norm(y.data_ptr(), _dt_of(y), _ptr(res), F32 if r_dtype == torch.float32 else BF16, T, H,
-                          _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w), w_dt, res_scale, eps, _ptr(r), _ptr(q),
-                          I8 if i8 else F32 if x_dtype == torch.float32 else BF16, _ptr(scale), _current(dev)))
+    L = _lib or lib()
+    _check(L.moe_norm(y.data_ptr(), _CODE[y.dtype], _ptr(res), _CODE[r_dtype], T, H, _ptr(post_w), _ptr(gate), gate_div,
+                      _ptr(pre_w), w_dt, res_scale, eps, _ptr(r), _ptr(q), _CODE[x_dtype], _ptr(scale), _current(dev)))
     return r, ((q, scale) if i8 and q is not None else q)
 
 
@@ -572,7 +578,6 @@ def norm_backward(dx, dr, y, r, *, post_w=None, gate=None, gate_div: int = 1, re
     dtype), dres (r's), dpost_w, dgate and dpre_w (fp32); None for those that
     are not in `need` or have no input.  dx or dr may be None (zero), r with dx
     None, y without post_w and gate (dy then has dr's dtype, or r's)."""
-    import torch
     some = next((t for t in (y, r, dx, dr) if t is not None), None)
     if some is None:
         raise ValueError("norm_backward: no tensors")
@@ -582,15 +587,14 @@ def norm_backward(dx, dr, y, r, *, post_w=None, gate=None, gate_div: int = 1, re
         with there:
             return norm_backward(dx, dr, y, r, post_w=post_w, gate=gate, gate_div=gate_div, res_scale=res_scale,
                                  pre_w=pre_w, eps=eps, need=need, ws=ws)
-    fl = (torch.float32, torch.bfloat16)
     G, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
     r_dtype = r.dtype if r is not None else dr.dtype if dr is not None else torch.float32
     y_dtype = y.dtype if y is not None else r_dtype
-    _tensor(dev, "dx", dx, (T, H), fl)
+    _tensor(dev, "dx", dx, (T, H), _FLOATS)
     _tensor(dev, "dr", dr, (T, H), (r_dtype,))
-    _tensor(dev, "y", y, (T, H), fl)
-    _tensor(dev, "r", r, (T, H), fl)
-    if r_dtype not in fl:
+    _tensor(dev, "y", y, (T, H), _FLOATS)
+    _tensor(dev, "r", r, (T, H), _FLOATS)
+    if r_dtype not in _FLOATS:
         raise TypeError(f"norm_backward: dr has dtype {r_dtype}")
     f32 = torch.float32
     what = {"dy": (some if y is None else y, (T, H), y_dtype), "dres": (some if r is None else r, (T, H), r_dtype),
@@ -598,38 +602,37 @@ def norm_backward(dx, dr, y, r, *, post_w=None, gate=None, gate_div: int = 1, re
     if not set(need) <= set(what):
         raise ValueError(f"need: {need}")
     o = {k: _empty(*v) if k in need and v[0] is not None else None for k, v in what.items()}
-    L = lib()
+    L = _lib or lib()
     ws = _scratch(ws, L.moe_norm_backward_workspace_size(T, H, gate_div if gate is not None else 0), dev)
     _check(L.moe_norm_backward(
-        _ptr(dx), F32 if dx is None else _dt_of(dx), _ptr(dr), _ptr(y), F32 if y_dtype == torch.float32 else BF16,
-        _ptr(r), F32 if r_dtype == torch.float32 else BF16, T, H, _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w), w_dt,
+        _ptr(dx), F32 if dx is None else _CODE[dx.dtype], _ptr(dr), _ptr(y), _CODE[y_dtype],
+        _ptr(r), _CODE[r_dtype], T, H, _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w), w_dt,
         res_scale, eps, *map(_ptr, o.values()), ws.data_ptr(), _nbytes(ws), _current(dev)))
     return o
 
 
 def quant_i8(x, stream=None, out=None):
     """int8 codes [rows][cols], scales [rows] fp32 (moe_quant_i8)."""
-    import torch
     rows, cols, dev = _matrix("x", x)
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
             return quant_i8(x, out=out)
     q, scale = out if out is not None else (None, None)
-    _tensor(dev, "x", x, (rows, cols), (torch.float32, torch.bfloat16))
+    _tensor(dev, "x", x, (rows, cols), _FLOATS)
     _tensor(dev, "q", q, (rows, cols), (torch.int8,))
     _tensor(dev, "scale", scale, (rows,), (torch.float32,))
     if out is None:
         q = torch.empty((rows, cols), dtype=torch.int8, device=dev)
         scale = torch.empty((rows,), dtype=torch.float32, device=dev)
-    _check(lib().moe_quant_i8(x.data_ptr(), _dt_of(x), rows, cols, q.data_ptr(), scale.data_ptr(), _current(dev)))
+    L = _lib or lib()
+    _check(L.moe_quant_i8(x.data_ptr(), _CODE[x.dtype], rows, cols, q.data_ptr(), scale.data_ptr(), _current(dev)))
     return q, scale
 
 
 def linear_i8(q, q_scale, w, w_scale, bias=None, *, out_dtype=None, out=None, ws=None, stream=None):
     """out [T][N] = (q w^T) * q_scale[:, None] * w_scale + bias (moe_linear_i8):
     q [T][K] and w [N][K] int8, q_scale [T], w_scale and bias [N] fp32."""
-    import torch
     T, K, dev = _matrix("q", q)
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -638,7 +641,7 @@ def linear_i8(q, q_scale, w, w_scale, bias=None, *, out_dtype=None, out=None, ws
     N = _matrix("w", w)[0]
     f32, i8 = (torch.float32,), (torch.int8,)
     out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
-    if out_dtype not in (torch.float32, torch.bfloat16):
+    if out_dtype not in _FLOATS:
         raise TypeError(f"linear_i8: out {out_dtype}")
     _tensor(dev, "q", q, (T, K), i8)
     _tensor(dev, "w", w, (N, K), i8)
@@ -648,9 +651,9 @@ def linear_i8(q, q_scale, w, w_scale, bias=None, *, out_dtype=None, out=None, ws
     _tensor(dev, "out", out, (T, N), (out_dtype,))
     if out is None:
         out = torch.empty((T, N), dtype=out_dtype, device=dev)
-    L = lib()
+    L = _lib or lib()
     need = L.moe_linear_i8_workspace_size(T, K, N)
     ws = _scratch(ws, need, dev) if need or ws is not None else None
     _check(L.moe_linear_i8(q.data_ptr(), q_scale.data_ptr(), T, K, w.data_ptr(), w_scale.data_ptr(), _ptr(bias), N,
-                           out.data_ptr(), _dt_of(out), _ptr(ws), 0 if ws is None else _nbytes(ws), _current(dev)))
+                           out.data_ptr(), _CODE[out.dtype], _ptr(ws), 0 if ws is None else _nbytes(ws), _current(dev)))
     return out

@@ -37,32 +37,35 @@ Args base(int M, int N, int K) {
     return G;
 }
 
-struct Plans {
-    Plan gateup, down, dh, dx, dwgu, dw1, dwd;
-};
-Plans plans(int T, int H, int I) {
-    return Plans{plan_tiles(T, 2L * I, H, kKE, true),  plan_tiles(T, H, I, kKE, true),
-                 plan_tiles(T, I, H, kKE, false),      plan_tiles(T, H, 2 * I, kKE, false),
-                 plan_tiles(2L * I, H, T, kKE, false), plan_tiles(I, H, T, kKE, false),
-                 plan_tiles(H, I, T, kKE, false)};
-}
-
 size_t max2(size_t a, size_t b) { return a > b ? a : b; }
 
-struct Ws {
+struct Forward {
+    Plan gateup, down;
+    size_t h, part, total;   // workspace
+};
+Plan gateup_plan(int T, int H, int I) { return plan_tiles(T, 2L * I, H, kKE, true); }
+Forward forward(int T, int H, int I) {
+    Forward f;
+    f.gateup = gateup_plan(T, H, I);
+    f.down = plan_tiles(T, H, I, kKE, true);
+    f.h = 0;
+    f.part = align256((size_t)T * I * 2);
+    f.total = f.part + max2(part_bytes(f.gateup, T, 2L * I), part_bytes(f.down, T, H));
+    return f;
+}
+
+struct Backward {
+    Plan gateup, dh, dx, dwgu, dw1, dwd;   // dw1: one of the gate and up gradients alone
     size_t gu, dgu, h, part, total;
 };
-Ws forward_ws(int T, int H, int I) {
-    const Plans p = plans(T, H, I);
-    Ws w{};
-    w.h = 0;
-    w.part = align256((size_t)T * I * 2);
-    w.total = w.part + max2(part_bytes(p.gateup, T, 2L * I), part_bytes(p.down, T, H));
-    return w;
-}
-Ws backward_ws(int T, int H, int I, int has_gu) {
-    const Plans p = plans(T, H, I);
-    Ws w{};
+Backward backward(int T, int H, int I, bool has_gu) {
+    Backward w;
+    w.gateup = gateup_plan(T, H, I);
+    w.dh = plan_tiles(T, I, H, kKE, false);
+    w.dx = plan_tiles(T, H, 2 * I, kKE, false);
+    w.dwgu = plan_tiles(2L * I, H, T, kKE, false);
+    w.dw1 = plan_tiles(I, H, T, kKE, false);
+    w.dwd = plan_tiles(H, I, T, kKE, false);
     size_t o = 0;
     w.gu = o;
     o += has_gu ? 0 : align256((size_t)T * I * 8);
@@ -71,21 +74,21 @@ Ws backward_ws(int T, int H, int I, int has_gu) {
     w.h = o;
     o += align256((size_t)T * I * 2);
     w.part = o;
-    size_t most = max2(part_bytes(p.dh, T, I), part_bytes(p.dx, T, H));
-    most = max2(most, max2(part_bytes(p.dwgu, 2L * I, H), part_bytes(p.dw1, I, H)));
-    most = max2(most, part_bytes(p.dwd, H, I));
-    if (!has_gu) most = max2(most, part_bytes(p.gateup, T, 2L * I));
+    size_t most = max2(part_bytes(w.dh, T, I), part_bytes(w.dx, T, H));
+    most = max2(most, max2(part_bytes(w.dwgu, 2L * I, H), part_bytes(w.dw1, I, H)));
+    most = max2(most, part_bytes(w.dwd, H, I));
+    if (!has_gu) most = max2(most, part_bytes(w.gateup, T, 2L * I));
     w.total = o + most;
     return w;
 }
 
-hipError_t gateup(const FfnProblem& p, void* h, float* gu, float* part, hipStream_t s) {
+hipError_t gateup(const FfnProblem& p, const Plan& plan, void* h, float* gu, float* part, hipStream_t s) {
     Args G = base(p.T, p.I, p.H);
     G.A = rows(p.x, p.H, p.T);
     G.B = rows(p.wg, p.H, p.I, p.wu);
     G.out = h;
     G.out2 = gu;
-    return run<kBf16, kRow, kRow, kEpiGateUp>(G, plans(p.T, p.H, p.I).gateup, part, s);
+    return run<kBf16, kRow, kRow, kEpiGateUp>(G, plan, part, s);
 }
 
 // rows of zeros (the weight gradients of no tokens)
@@ -97,21 +100,21 @@ hipError_t zero_rows(void* out, int M, int N, hipStream_t s) {
 
 }  // namespace
 
-size_t ffn_ws_bytes(int T, int H, int I) { return T > 0 ? forward_ws(T, H, I).total : 0; }
-size_t ffn_backward_ws_bytes(int T, int H, int I, int has_gu) { return T > 0 ? backward_ws(T, H, I, has_gu).total : 0; }
+size_t ffn_ws_bytes(int T, int H, int I) { return T > 0 ? forward(T, H, I).total : 0; }
+size_t ffn_backward_ws_bytes(int T, int H, int I, int has_gu) { return T > 0 ? backward(T, H, I, has_gu != 0).total : 0; }
 
 hipError_t launch_ffn(const FfnProblem& p, void* ws, hipStream_t s) {
-    const Ws w = forward_ws(p.T, p.H, p.I);
+    const Forward w = forward(p.T, p.H, p.I);
     uint8_t* b = (uint8_t*)ws;
     float* part = (float*)(b + w.part);
-    hipError_t e = gateup(p, b + w.h, p.gu, part, s);
+    hipError_t e = gateup(p, w.gateup, b + w.h, p.gu, part, s);
     if (e != hipSuccess) return e;
     Args G = base(p.T, p.H, p.I);
     G.A = rows(b + w.h, p.I, p.T);
     G.B = rows(p.wd, p.I, p.H);
     G.out = p.y;
     G.out_f32 = p.y_f32;
-    return run<kBf16, kRow, kRow, kEpiOut>(G, plans(p.T, p.H, p.I).down, part, s);
+    return run<kBf16, kRow, kRow, kEpiOut>(G, w.down, part, s);
 }
 
 hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
@@ -123,8 +126,7 @@ hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
         return e;
     }
     const int T = p.T, H = p.H, I = p.I;
-    const Plans pl = plans(T, H, I);
-    const Ws w = backward_ws(T, H, I, p.gu_in != nullptr);
+    const Backward w = backward(T, H, I, p.gu_in != nullptr);
     uint8_t* b = (uint8_t*)ws;
     float* part = (float*)(b + w.part);
     uint8_t* dgu = b + w.dgu;
@@ -132,7 +134,7 @@ hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
     const float* gu = p.gu_in;
     if (!gu) {
         gu = (const float*)(b + w.gu);
-        e = gateup(p, h, (float*)(b + w.gu), part, s);
+        e = gateup(p, w.gateup, h, (float*)(b + w.gu), part, s);
         if (e != hipSuccess) return e;
     }
     {
@@ -142,14 +144,14 @@ hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
         G.gu = gu;
         G.out = dgu;
         G.out2 = h;
-        e = run<kBf16, kRow, kCol, kEpiGrad>(G, pl.dh, part, s);
+        e = run<kBf16, kRow, kCol, kEpiGrad>(G, w.dh, part, s);
     }
     if (e == hipSuccess && p.dx) {
         Args G = base(T, H, 2 * I);
         G.A = rows(dgu, 2L * I, T);
         G.B = cols(p.wg, H, H, p.wu, I);
         G.out = p.dx;
-        e = run<kBf16, kRow, kCol, kEpiOut>(G, pl.dx, part, s);
+        e = run<kBf16, kRow, kCol, kEpiOut>(G, w.dx, part, s);
     }
     if (e == hipSuccess && (p.dwg || p.dwu)) {
         // both at once; one alone: its half of dgu
@@ -160,14 +162,14 @@ hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
         G.out = p.dwg ? p.dwg : p.dwu;
         G.out2 = p.dwu;
         G.msplit = I;
-        e = run<kBf16, kCol, kCol, kEpiOut>(G, both ? pl.dwgu : pl.dw1, part, s);
+        e = run<kBf16, kCol, kCol, kEpiOut>(G, both ? w.dwgu : w.dw1, part, s);
     }
     if (e == hipSuccess && p.dwd) {
         Args G = base(H, I, T);
         G.A = cols(p.dy, H, H);
         G.B = cols(h, I, I);
         G.out = p.dwd;
-        e = run<kBf16, kCol, kCol, kEpiOut>(G, pl.dwd, part, s);
+        e = run<kBf16, kCol, kCol, kEpiOut>(G, w.dwd, part, s);
     }
     return e;
 }
