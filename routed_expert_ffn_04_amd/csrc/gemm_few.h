@@ -61,7 +61,8 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args G) {
             for (int h = 0; h < 2; ++h) {
                 const bool in = off + h * 16 < left;
                 w[u][h] = *(const i32x4*)(in ? wp + off + h * 16 : (const uint8_t*)kZeros);
-                x[u][h] = *(const i32x4*)(in ? xp + off + h * 16 : (const uint8_t*)kZeros);
+                x[u][h] = i32x4{};
+                if (in && r < G.M) x[u][h] = *(const i32x4*)(xp + off + h * 16);
             }
         }
         __builtin_amdgcn_sched_barrier(0);   // every load of the turn is out before the first product waits
