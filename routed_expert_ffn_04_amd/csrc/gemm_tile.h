@@ -304,96 +304,167 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256)
 
     const Frag<LA, BM> fa(wm * IB, lane);
     const Frag<LB, BN> fb(wn * (GU ? JB / 2 : JB), lane);
-    // A stage is two k-steps, each one part, or two in 256-row tiles (the halves
-    // of the wave's rows).  a: the rows' fragments of one part, b: the columns'
-    // of one k-step, both twice: one set multiplies while the next is read.
-    constexpr int AH = IB < 4 ? IB : 4, PK = IB / AH, kParts = 2 * PK;
-    i32x4 a[2][AH], b[2][JB];
-    auto read_a = [&](const uint8_t* half, int part, int i0, int i1) __attribute__((always_inline)) {
+    if constexpr (R == 10) {
+        // One or two workgroups per CU: a stage's fragments are read while the
+        // stage before multiplies (two register sets), since a wave alone on its
+        // SIMD has nothing else to do meanwhile: FFN of 1024 x 2048 x 1024 25 us
+        // against 28, int8 333 x 2064 x 1501 8.3 against 9.9.
+        i32x4 a[2][2][IB], b[2][2][JB];   // [set][k-step]
+        auto read = [&](const uint8_t* ha, const uint8_t* hb, int set, int ks) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = i0; i < i1; ++i) a[part & 1][i] = fa.read(half, part % PK * AH + i, part / PK);
-    };
-    auto read_b = [&](const uint8_t* half, int ks) __attribute__((always_inline)) {
+            for (int j = 0; j < JB; ++j)
+                b[set][ks][j] = fb.read(hb + (GU && j >= JB / 2 ? BN / 2 * kStage : 0), GU ? j % (JB / 2) : j, ks);
 #pragma unroll
-        for (int j = 0; j < JB; ++j)   // gate/up: half of the blocks gate columns, half up columns
-            b[ks][j] = fb.read(half + (GU && j >= JB / 2 ? BN / 2 * kStage : 0), GU ? j % (JB / 2) : j, ks);
-    };
-    auto mma = [&](int part, int i0, int i1) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = i0; i < i1; ++i)
-#pragma unroll
-            for (int j = 0; j < JB; ++j) {
-                auto& c = acc[part % PK * AH + i][j];
-                c = Acc<E>::mma(b[part / PK][j], a[part & 1][i], c);
-            }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    // The products of `part` while the next part's fragments are read.  LDS
-    // reads and direct loads go out a few at a time between products: together
-    // they would fill the memory pipes' queues and hold up the products behind
-    // them.
-    auto step = [&](int part, const uint8_t* ha, const uint8_t* hb, auto&& load) __attribute__((always_inline)) {
-        const int next = (part + 1) % kParts;
-        mma(part, 0, AH / 4);
-        if (next % PK == 0) read_b(hb, next / PK);
-        read_a(ha, next, 0, AH / 2);
-        __builtin_amdgcn_sched_barrier(0);
-        mma(part, AH / 4, AH / 2);
-        read_a(ha, next, AH / 2, AH);
-        __builtin_amdgcn_sched_barrier(0);
-        mma(part, AH / 2, AH - 1);
-        load();
-        __builtin_amdgcn_sched_barrier(0);
-        mma(part, AH - 1, AH);
-    };
-    // One stage from its halves rA, rB, beginning with the previous stage's
-    // last part; w0 and w1 are the halves that stage has left.  The restrict
-    // qualifiers state that the loads into w0 and w1 do not touch rA and rB;
-    // without them the compiler waits for every direct load before a
-    // transposing read.
-    auto turn = [&](uint8_t* __restrict__ w0, uint8_t* __restrict__ w1, const uint8_t* __restrict__ rA,
-                    const uint8_t* __restrict__ rB) __attribute__((always_inline)) {
-        // the halves' loads, in the order of the ring
-        auto fill = [&](int q0, int q1) __attribute__((always_inline)) {
-#pragma unroll
-            for (int q = q0; q < q1; q += 2)
-                if ((q < LD) == (R % 2 == 1)) issueB(q < LD ? w0 : w1, q % LD, q % LD + 2);
-                else issueA(q < LD ? w0 : w1, q % LD, q % LD + 2);
+            for (int i = 0; i < IB; ++i) a[set][ks][i] = fa.read(ha, i, ks);
+            __builtin_amdgcn_sched_barrier(0);
         };
-        constexpr int L = 2 * LD / kParts;
+        auto mma = [&](int set, int ks) __attribute__((always_inline)) {
 #pragma unroll
-        for (int p = 0; p < kParts; ++p)
-            step((p + kParts - 1) % kParts, rA, rB, [&]() __attribute__((always_inline)) { fill(p * L, p * L + L); });
-    };
-    auto none = []() __attribute__((always_inline)) {};
-    auto start = [&](uint8_t* __restrict__ w, const uint8_t* __restrict__ rA, const uint8_t* __restrict__ rB)
-                     __attribute__((always_inline)) {
+            for (int i = 0; i < IB; ++i)
 #pragma unroll
-        for (int h = 2; h < R; ++h)
-            if (h % 2) issueB(w + (h - 2) * kHalf, 0, LD);
-            else issueA(w + (h - 2) * kHalf, 0, LD);
-        barrier_vm<(R - 2) * LD>();   // the first two halves
-        read_b(rB, 0);
-        read_a(rA, 0, 0, AH);
+                for (int j = 0; j < JB; ++j) acc[i][j] = Acc<E>::mma(b[set][ks][j], a[set][ks][i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // The products of the stage in `set` while the next stage is read from
+        // rA and rB into the other one; everybody has read this stage's halves,
+        // w0 and w1 (see below for the restrict qualifiers).
+        auto turn = [&](int set, uint8_t* __restrict__ w0, uint8_t* __restrict__ w1, const uint8_t* __restrict__ rA,
+                        const uint8_t* __restrict__ rB) __attribute__((always_inline)) {
+            read(rA, rB, set ^ 1, 0);
+            mma(set, 0);
+            issueA(w0, 0, LD);
+            __builtin_amdgcn_sched_barrier(0);
+            read(rA, rB, set ^ 1, 1);
+            mma(set, 1);
+            issueB(w1, 0, LD);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto start = [&](uint8_t* __restrict__ w, const uint8_t* __restrict__ rA, const uint8_t* __restrict__ rB)
+                         __attribute__((always_inline)) {
 #pragma unroll
-        for (int p = 0; p + 1 < kParts; ++p) step(p, rA, rB, none);
-    };
+            for (int h = 2; h < R; ++h)
+                if (h % 2) issueB(w + (h - 2) * kHalf, 0, LD);
+                else issueA(w + (h - 2) * kHalf, 0, LD);
+            barrier_vm<(R - 2) * LD>();   // the first two halves
+            read(rA, rB, 0, 0);
+            read(rA, rB, 0, 1);
+        };
+        issueA(smem, 0, LD);
+        issueB(smem + kHalf, 0, LD);
+        start(smem + 2 * kHalf, smem, smem + kHalf);
+        int u = 0;   // slot of the current stage's A half
+        auto go = [&](int set) __attribute__((always_inline)) {
+            barrier_vm<(R - 4) * LD>();   // the next stage has landed
+            uint8_t* w = smem + u * kHalf;
+            u = u + 2 == R ? 0 : u + 2;
+            const uint8_t* r = smem + u * kHalf;
+            turn(set, w, w + kHalf, r, r + kHalf);
+        };
+        int s = 0;
+        for (; s + 2 < nst; s += 2) {
+            go(0);
+            go(1);
+        }
+        if (s + 1 < nst) {
+            go(0);
+            mma(1, 0);
+            mma(1, 1);
+        } else {
+            mma(0, 0);
+            mma(0, 1);
+        }
+    } else {
+        // A stage is two k-steps, each one part, or two in 256-row tiles (the halves
+        // of the wave's rows).  a: the rows' fragments of one part, b: the columns'
+        // of one k-step, both twice: one set multiplies while the next is read.
+        constexpr int AH = IB < 4 ? IB : 4, PK = IB / AH, kParts = 2 * PK;
+        i32x4 a[2][AH], b[2][JB];
+        auto read_a = [&](const uint8_t* half, int part, int i0, int i1) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = i0; i < i1; ++i) a[part & 1][i] = fa.read(half, part % PK * AH + i, part / PK);
+        };
+        auto read_b = [&](const uint8_t* half, int ks) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < JB; ++j)   // gate/up: half of the blocks gate columns, half up columns
+                b[ks][j] = fb.read(half + (GU && j >= JB / 2 ? BN / 2 * kStage : 0), GU ? j % (JB / 2) : j, ks);
+        };
+        auto mma = [&](int part, int i0, int i1) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = i0; i < i1; ++i)
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    auto& c = acc[part % PK * AH + i][j];
+                    c = Acc<E>::mma(b[part / PK][j], a[part & 1][i], c);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // The products of `part` while the next part's fragments are read.  LDS
+        // reads and direct loads go out a few at a time between products: together
+        // they would fill the memory pipes' queues and hold up the products behind
+        // them.
+        auto step = [&](int part, const uint8_t* ha, const uint8_t* hb, auto&& load) __attribute__((always_inline)) {
+            const int next = (part + 1) % kParts;
+            mma(part, 0, AH / 4);
+            if (next % PK == 0) read_b(hb, next / PK);
+            read_a(ha, next, 0, AH / 2);
+            __builtin_amdgcn_sched_barrier(0);
+            mma(part, AH / 4, AH / 2);
+            read_a(ha, next, AH / 2, AH);
+            __builtin_amdgcn_sched_barrier(0);
+            mma(part, AH / 2, AH - 1);
+            load();
+            __builtin_amdgcn_sched_barrier(0);
+            mma(part, AH - 1, AH);
+        };
+        // One stage from its halves rA, rB, beginning with the previous stage's
+        // last part; w0 and w1 are the halves that stage has left.  The restrict
+        // qualifiers state that the loads into w0 and w1 do not touch rA and rB;
+        // without them the compiler waits for every direct load before a
+        // transposing read.
+        auto turn = [&](uint8_t* __restrict__ w0, uint8_t* __restrict__ w1, const uint8_t* __restrict__ rA,
+                        const uint8_t* __restrict__ rB) __attribute__((always_inline)) {
+            // the halves' loads, in the order of the ring
+            auto fill = [&](int q0, int q1) __attribute__((always_inline)) {
+#pragma unroll
+                for (int q = q0; q < q1; q += 2)
+                    if ((q < LD) == (R % 2 == 1)) issueB(q < LD ? w0 : w1, q % LD, q % LD + 2);
+                    else issueA(q < LD ? w0 : w1, q % LD, q % LD + 2);
+            };
+            constexpr int L = 2 * LD / kParts;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+                step((p + kParts - 1) % kParts, rA, rB, [&]() __attribute__((always_inline)) { fill(p * L, p * L + L); });
+        };
+        auto none = []() __attribute__((always_inline)) {};
+        auto start = [&](uint8_t* __restrict__ w, const uint8_t* __restrict__ rA, const uint8_t* __restrict__ rB)
+                         __attribute__((always_inline)) {
+#pragma unroll
+            for (int h = 2; h < R; ++h)
+                if (h % 2) issueB(w + (h - 2) * kHalf, 0, LD);
+                else issueA(w + (h - 2) * kHalf, 0, LD);
+            barrier_vm<(R - 2) * LD>();   // the first two halves
+            read_b(rB, 0);
+            read_a(rA, 0, 0, AH);
+#pragma unroll
+            for (int p = 0; p + 1 < kParts; ++p) step(p, rA, rB, none);
+        };
 
-    issueA(smem, 0, LD);
-    issueB(smem + kHalf, 0, LD);
-    start(smem + 2 * kHalf, smem, smem + kHalf);
-    int u = 0;   // slot of the previous stage's A half; the ring's order is A B A B A ...
-    auto slot = [&](int i) __attribute__((always_inline)) { return smem + (u + i >= R ? u + i - R : u + i) * kHalf; };
-    for (int s = 1; s < nst; ++s) {
-        barrier_vm<(R - 4) * LD>();   // stage s has landed
-        uint8_t* w0 = slot(0);
-        uint8_t* w1 = slot(1);
-        const uint8_t* rA = slot(2);
-        const uint8_t* rB = slot(3);
-        u = u + 2 >= R ? u + 2 - R : u + 2;
-        turn(w0, w1, rA, rB);
+        issueA(smem, 0, LD);
+        issueB(smem + kHalf, 0, LD);
+        start(smem + 2 * kHalf, smem, smem + kHalf);
+        int u = 0;   // slot of the previous stage's A half; the ring's order is A B A B A ...
+        auto slot = [&](int i) __attribute__((always_inline)) { return smem + (u + i >= R ? u + i - R : u + i) * kHalf; };
+        for (int s = 1; s < nst; ++s) {
+            barrier_vm<(R - 4) * LD>();   // stage s has landed
+            uint8_t* w0 = slot(0);
+            uint8_t* w1 = slot(1);
+            const uint8_t* rA = slot(2);
+            const uint8_t* rB = slot(3);
+            u = u + 2 >= R ? u + 2 - R : u + 2;
+            turn(w0, w1, rA, rB);
+        }
+        mma(kParts - 1, 0, AH);
     }
-    mma(kParts - 1, 0, AH);
     // the prefetched (zero) stages land before the ring becomes the epilogue's scratch
     barrier_vm<0>();
 
