@@ -15,6 +15,9 @@
 // the matrix cores take them; g and u are kept in fp32, because rounding them
 // as well would put a second error of the same size on dx and the gate and up
 // gradients.  All sums are fp32.
+#include <algorithm>
+#include <utility>
+
 #include "gemm_plan.h"
 
 namespace moe {
@@ -91,6 +94,87 @@ hipError_t gateup(const FfnProblem& p, const Plan& plan, void* h, float* gu, flo
     return run<kBf16, kRow, kRow, kEpiGateUp>(G, plan, part, s);
 }
 
+// The last products of the backward pass, which do not depend on each other:
+// one launch whose workgroups take the tiles of all of them, the longest tiles
+// first.  The tiles of one product rarely fill their last round of CUs (4096 x 7168
+// x 2048: 1.75, 1.75 and 0.875 rounds, 4.375 together), and small products are
+// mostly launches.
+struct Product {
+    Args G;
+    Plan plan;   // its tiling if it runs alone
+    int weight;  // a weight gradient (both operands by columns), else dx
+};
+struct Products {
+    Args G[3];
+    int first[4];   // first workgroup of each
+    int weight[3];
+};
+
+template <int EDGE>
+__global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per_eu(tile_waves(EDGE, 5)))) void products_kernel(
+    Products P) {
+    const int b = blockIdx.x;
+    const int i = (b >= P.first[1]) + (b >= P.first[2]);
+    const int block = b - P.first[i], blocks = P.first[i + 1] - P.first[i];
+    if (P.weight[i]) tile<kBf16, kCol, kCol, kEpiOut, false, EDGE, EDGE, 5>(P.G[i], block, blocks);
+    else tile<kBf16, kRow, kCol, kEpiOut, false, EDGE, EDGE, 5>(P.G[i], block, blocks);
+}
+
+template <int EDGE>
+hipError_t launch_together(const Product* todo, int n, hipStream_t s) {
+    Products P{};
+    long total = 0;
+    for (int i = 0; i < n; ++i) {
+        P.G[i] = todo[i].G;
+        P.G[i].splits = 1;
+        P.G[i].kspan = (P.G[i].K + kKE - 1) / kKE * kKE;
+        P.weight[i] = todo[i].weight;
+        P.first[i] = (int)total;
+        total += count_tiles(P.G[i], EDGE, EDGE);
+        if (total > 0x7fffffffL) return hipErrorInvalidValue;
+    }
+    for (int i = n; i < 4; ++i) P.first[i] = (int)total;
+    static DeviceCache ready;
+    if (!allow_lds(ready, products_kernel<EDGE>, tile_lds(EDGE, 5))) return hipErrorInvalidValue;
+    products_kernel<EDGE><<<dim3((unsigned)total), dim3(tile_threads(EDGE)), tile_lds(EDGE, 5), s>>>(P);
+    return hipGetLastError();
+}
+
+hipError_t launch_products(Product* todo, int n, float* part, hipStream_t s) {
+    // longest reduction first
+    for (int i = 1; i < n; ++i)
+        for (int j = i; j > 0 && todo[j].G.K > todo[j - 1].G.K; --j) std::swap(todo[j], todo[j - 1]);
+    double apart = 0;
+    for (int i = 0; i < n; ++i) apart += todo[i].plan.us + 3;
+    // together: the work over all CUs and half a tile's time for the uneven end,
+    // at least one longest tile (the times of gemm_plan.h)
+    int best = 0;
+    for (int edge = 64; n > 1 && edge <= 256; edge *= 2) {
+        const double stage = edge == 256 ? 1.6 : edge == 128 ? 0.65 : 0.225, fixed = edge == 256 ? 10 : edge == 128 ? 1.5 : 0.75;
+        const double alone = edge == 256 ? 1.6 : edge == 128 ? 1.3 : 0.5;   // a stage's time within its workgroup
+        double work = 0, longest = 0;
+        for (int i = 0; i < n; ++i) {
+            const Args& G = todo[i].G;
+            const double tiles = (double)((G.M + edge - 1) / edge) * ((G.N + edge - 1) / edge), span = (G.K + kKE - 1) / kKE;
+            work += tiles * (span * stage + fixed) / 256;
+            longest = std::max(longest, span * alone + 3);
+        }
+        const double us = std::max(longest, work + longest / 2) + 3;
+        if (us < apart) {
+            apart = us;
+            best = edge;
+        }
+    }
+    if (best == 256) return launch_together<256>(todo, n, s);
+    if (best == 128) return launch_together<128>(todo, n, s);
+    if (best == 64) return launch_together<64>(todo, n, s);
+    hipError_t e = hipSuccess;
+    for (int i = 0; i < n && e == hipSuccess; ++i)
+        e = todo[i].weight ? run<kBf16, kCol, kCol, kEpiOut>(todo[i].G, todo[i].plan, part, s)
+                           : run<kBf16, kRow, kCol, kEpiOut>(todo[i].G, todo[i].plan, part, s);
+    return e;
+}
+
 // rows of zeros (the weight gradients of no tokens)
 hipError_t zero_rows(void* out, int M, int N, hipStream_t s) {
     Args G = base(M, N, 0);
@@ -146,15 +230,19 @@ hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
         G.out2 = h;
         e = run<kBf16, kRow, kCol, kEpiGrad>(G, w.dh, part, s);
     }
-    if (e == hipSuccess && p.dx) {
+    if (e != hipSuccess) return e;
+    // the products that are wanted: dx, the gate and up gradients (both at once, or
+    // one with its half of dgu), the down gradient
+    Product todo[3];
+    int n = 0;
+    if (p.dx) {
         Args G = base(T, H, 2 * I);
         G.A = rows(dgu, 2L * I, T);
         G.B = cols(p.wg, H, H, p.wu, I);
         G.out = p.dx;
-        e = run<kBf16, kRow, kCol, kEpiOut>(G, w.dx, part, s);
+        todo[n++] = {G, w.dx, 0};
     }
-    if (e == hipSuccess && (p.dwg || p.dwu)) {
-        // both at once; one alone: its half of dgu
+    if (p.dwg || p.dwu) {
         const bool both = p.dwg && p.dwu;
         Args G = base(both ? 2 * I : I, H, T);
         G.A = cols(dgu + (p.dwg ? 0 : (size_t)I * 2), 2L * I, both ? 2 * I : I);
@@ -162,16 +250,16 @@ hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
         G.out = p.dwg ? p.dwg : p.dwu;
         G.out2 = p.dwu;
         G.msplit = I;
-        e = run<kBf16, kCol, kCol, kEpiOut>(G, both ? w.dwgu : w.dw1, part, s);
+        todo[n++] = {G, both ? w.dwgu : w.dw1, 1};
     }
-    if (e == hipSuccess && p.dwd) {
+    if (p.dwd) {
         Args G = base(H, I, T);
         G.A = cols(p.dy, H, H);
         G.B = cols(h, I, I);
         G.out = p.dwd;
-        e = run<kBf16, kCol, kCol, kEpiOut>(G, w.dwd, part, s);
+        todo[n++] = {G, w.dwd, 1};
     }
-    return e;
+    return launch_products(todo, n, part, s);
 }
 
 }  // namespace moe

@@ -12,6 +12,7 @@ struct Plan {
     int edge;            // 256 x 256, 128 x 128 or 64 x 64 tiles
     int splits, kspan;
     int workgroups;
+    double us;           // estimated time
 };
 
 // Estimated time of wg workgroups of `span` stages each, in us.
@@ -42,7 +43,7 @@ inline Plan plan_tiles(long M, long mma_cols, int K, int stage_elems, bool rows)
             double us = tiling_us(edge, wg, span);
             if (n > 1) us += 4 + (double)n * M * mma_cols * 8 / 4e6;
             if (least == 0 || us < least) {
-                least = us;
+                least = best.us = us;
                 best.edge = edge;
                 best.splits = n;
                 best.kspan = span * stage_elems;

@@ -215,10 +215,15 @@ __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& t
     tm = band * 8 + t % rows;
 }
 
+// Launch shape of the tiles: threads, and workgroups per CU (by LDS).
+constexpr int tile_threads(int edge) { return edge == 256 ? 512 : 256; }
+constexpr int tile_lds(int edge, int ring) { return ring * edge * kStage; }
+constexpr int tile_waves(int edge, int ring) { return edge == 256 ? 2 : 163840 / tile_lds(edge, ring); }   // per SIMD
+
+// Workgroup `block` of the `blocks` that share out the tiles and splits of G.
 template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
-__global__ __launch_bounds__(BM == 256 ? 512 : 256)
-    __attribute__((amdgpu_waves_per_eu(BM == 256 ? 2 : 163840 / (R * BM * kStage)))) void tile_kernel(Args G) {
-    constexpr int kThreads = BM == 256 ? 512 : 256;
+__device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
+    constexpr int kThreads = tile_threads(BM);
     constexpr int EB = E == kI8 ? 1 : 2;
     constexpr int KE = kStage / EB;                            // k elements per stage
     constexpr int WN = BM == 256 ? 4 : 2, WM = 2;              // waves along n and m
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256)
     const int wm = wave / WN, wn = wave % WN;
 
     int tm, tn, split;
-    tile_of(blockIdx.x, G.mt, G.nt, gridDim.x, tm, tn, split);
+    tile_of(block, G.mt, G.nt, blocks, tm, tn, split);
     const int m0 = tm * BM, n0 = tn * kTileN;
     const int k0 = split * G.kspan;
     const int kn = min(G.K - k0, G.kspan);                     // k elements of this split
@@ -595,21 +600,35 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256)
     }
 }
 
+template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
+__global__ __launch_bounds__(tile_threads(BM)) __attribute__((amdgpu_waves_per_eu(tile_waves(BM, R)))) void tile_kernel(Args G) {
+    tile<E, LA, LB, EPI, GU, BM, BN, R>(G, blockIdx.x, gridDim.x);
+}
+
+// Raises a kernel's LDS limit, once on each device.
+template <class K>
+bool allow_lds(DeviceCache& ready, K* kernel, int bytes) {
+    return per_device(ready, [&] {
+        return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess ? 1 : 0;
+    }) != 0;
+}
+
+// Tiles of G: sets mt and nt and returns the number of workgroups.
+inline long count_tiles(Args& G, int edge, int cols) {
+    G.mt = (G.M + edge - 1) / edge;
+    G.nt = (G.N + cols - 1) / cols;
+    return (long)G.mt * G.nt * G.splits;
+}
+
 // Launches one tiling; mt, nt and the grid follow from the sizes in G.
 template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
 hipError_t launch_tiles(Args G, hipStream_t s) {
     auto* k = tile_kernel<E, LA, LB, EPI, GU, BM, BN, R>;
-    constexpr int lds = R * BM * kStage;
-    static DeviceCache ready;   // the LDS limit is a property of the function on each device
-    const int ok = per_device(ready, [&] {
-        return hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds) == hipSuccess ? 1 : 0;
-    });
-    if (!ok) return hipErrorInvalidValue;
-    G.mt = (G.M + BM - 1) / BM;
-    G.nt = (G.N + (GU ? BN / 2 : BN) - 1) / (GU ? BN / 2 : BN);
-    const long total = (long)G.mt * G.nt * G.splits;
+    static DeviceCache ready;
+    if (!allow_lds(ready, k, tile_lds(BM, R))) return hipErrorInvalidValue;
+    const long total = count_tiles(G, BM, GU ? BN / 2 : BN);
     if (total <= 0 || total > 0x7fffffffL) return hipErrorInvalidValue;
-    k<<<dim3((unsigned)total), dim3(BM == 256 ? 512 : 256), lds, s>>>(G);
+    k<<<dim3((unsigned)total), dim3(tile_threads(BM)), tile_lds(BM, R), s>>>(G);
     return hipGetLastError();
 }
 
