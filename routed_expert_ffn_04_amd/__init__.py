@@ -390,32 +390,37 @@ def _import_torch():
     torch = t
 
 
-def _elsewhere(device, stream):
-    """None if a call with tensors on `device` can go to the current stream as
-    it is, else the context in which it can: the device and `stream` (default:
+# These calls are a few microseconds of GPU time at decode sizes, so what they do
+# on the host is kept short: devices are compared by index, outputs are made
+# by new_empty (quicker than torch.empty with a device), errors are put
+# together only when there is one.
+
+def _elsewhere(device: int, stream):
+    """None if a call with tensors on GPU `device` can go to the current stream
+    as it is, else the context in which it can: the device and `stream` (default:
     the device's current stream) made current, so that what the call allocates
     belongs to the stream that uses it."""
     if stream is None:
-        if torch._C._cuda_getDevice() == device.index:
+        if torch._C._cuda_getDevice() == device:
             return None
         stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream of {stream.device} with tensors on {device}")
+    elif stream.device.index != device:
+        raise ValueError(f"stream of {stream.device} with tensors on cuda:{device}")
     return torch.cuda.stream(stream)
 
 
-def _current(device) -> int:
+def _current(device: int) -> int:
     """Handle of the device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _tensor(device, name, t, shape, dtypes):
+def _tensor(device: int, name, t, shape, dtypes):
     """Checks an argument (None passes): on the device, contiguous, of the
     shape and of one of the dtypes."""
-    if t is None or (t.shape == shape and t.dtype in dtypes and t.device == device and t.is_contiguous()):
+    if t is None or (t.shape == shape and t.dtype in dtypes and t.get_device() == device and t.is_contiguous()):
         return
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
@@ -424,31 +429,31 @@ def _tensor(device, name, t, shape, dtypes):
 
 
 def _empty(like, shape, dtype):
-    """An output; `like`: a checked tensor on its device, often of its very shape and dtype (which is quicker)."""
-    if like.dtype is dtype and like.shape == shape:
-        return torch.empty_like(like)
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    """An output on `like`'s device."""
+    if like.dtype is dtype:
+        return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def _matrix(name, t):
-    """(rows, columns, device) of a 2-d device tensor."""
+    """(rows, columns, device index) of a 2-d device tensor."""
     if torch is None:
         _import_torch()
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name}: expected a 2-d tensor on a GPU, got {tuple(t.shape)} on {t.device}")
-    return t.shape[0], t.shape[1], t.device
+    shape, device = t.shape, t.get_device()
+    if len(shape) != 2 or device < 0:
+        raise ValueError(f"{name}: expected a 2-d tensor on a GPU, got {tuple(shape)} on {t.device}")
+    return shape[0], shape[1], device
 
 
-def _scratch(ws, need, device):
+def _scratch(ws, need, like):
+    """(pointer, bytes) of the workspace given, or of a new one, and what keeps it alive."""
     if ws is None:
-        return _workspace(need, device)
-    if ws.device != device:
-        raise ValueError(f"ws is on {ws.device}, expected {device}")
-    return ws
-
-
-def _nbytes(ws) -> int:
-    return ws.numel() * ws.element_size()
+        need = max(need, 256)
+        ws = like.new_empty(need, dtype=torch.uint8)
+        return ws.data_ptr(), need, ws
+    if ws.get_device() != like.get_device():
+        raise ValueError(f"ws is on {ws.device}, expected {like.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def _dense_bank(bank: Experts, H: int, device):
@@ -480,11 +485,11 @@ def ffn(x, bank: Experts, *, want_gu: bool = False, y_dtype=None, out=None, gu=N
     if out is None:
         out = _empty(x, (T, H), y_dtype)
     if gu is None and want_gu:
-        gu = torch.empty((T, 2 * I), dtype=torch.float32, device=dev)
+        gu = _empty(x, (T, 2 * I), torch.float32)
     L = _lib or lib()
-    ws = _scratch(ws, L.moe_ffn_workspace_size(T, H, I), dev)
-    _check(L.moe_ffn(x.data_ptr(), BF16, T, ctypes.byref(st), out.data_ptr(), _CODE[out.dtype], _ptr(gu), ws.data_ptr(),
-                     _nbytes(ws), _current(dev)))
+    wp, wn, ws = _scratch(ws, L.moe_ffn_workspace_size(T, H, I), x)
+    _check(L.moe_ffn(x.data_ptr(), BF16, T, ctypes.byref(st), out.data_ptr(), _CODE[out.dtype], _ptr(gu), wp, wn,
+                     _current(dev)))
     return (out, gu) if want_gu else out
 
 
@@ -508,9 +513,9 @@ def ffn_backward(dy, x, bank: Experts, gu=None, *, need=("dx", "dw_gate", "dw_up
     likes = (x, bank.w_gate, bank.w_up, bank.w_down)
     o = tuple(torch.empty_like(t) if k in need else None for k, t in zip(names, likes))
     L = _lib or lib()
-    ws = _scratch(ws, L.moe_ffn_backward_workspace_size(T, H, I, int(gu is not None)), dev)
-    _check(L.moe_ffn_backward(dy.data_ptr(), x.data_ptr(), BF16, T, ctypes.byref(st), _ptr(gu), *map(_ptr, o),
-                              ws.data_ptr(), _nbytes(ws), _current(dev)))
+    wp, wn, ws = _scratch(ws, L.moe_ffn_backward_workspace_size(T, H, I, int(gu is not None)), x)
+    _check(L.moe_ffn_backward(dy.data_ptr(), x.data_ptr(), BF16, T, ctypes.byref(st), _ptr(gu), *map(_ptr, o), wp, wn,
+                              _current(dev)))
     return o
 
 
@@ -565,7 +570,7 @@ def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: f
     if q is None and want_x:
         q = _empty(y, (T, H), x_dtype)
     if q is not None and i8 and scale is None:
-        scale = torch.empty((T,), dtype=torch.float32, device=dev)
+        scale = _empty(y, (T,), torch.float32)
     L = _lib or lib()
     _check(L.moe_norm(y.data_ptr(), _CODE[y.dtype], _ptr(res), _CODE[r_dtype], T, H, _ptr(post_w), _ptr(gate), gate_div,
                       _ptr(pre_w), w_dt, res_scale, eps, _ptr(r), _ptr(q), _CODE[x_dtype], _ptr(scale), _current(dev)))
@@ -603,11 +608,11 @@ def norm_backward(dx, dr, y, r, *, post_w=None, gate=None, gate_div: int = 1, re
         raise ValueError(f"need: {need}")
     o = {k: _empty(*v) if k in need and v[0] is not None else None for k, v in what.items()}
     L = _lib or lib()
-    ws = _scratch(ws, L.moe_norm_backward_workspace_size(T, H, gate_div if gate is not None else 0), dev)
+    wp, wn, ws = _scratch(ws, L.moe_norm_backward_workspace_size(T, H, gate_div if gate is not None else 0), some)
     _check(L.moe_norm_backward(
         _ptr(dx), F32 if dx is None else _CODE[dx.dtype], _ptr(dr), _ptr(y), _CODE[y_dtype],
         _ptr(r), _CODE[r_dtype], T, H, _ptr(post_w), _ptr(gate), gate_div, _ptr(pre_w), w_dt,
-        res_scale, eps, *map(_ptr, o.values()), ws.data_ptr(), _nbytes(ws), _current(dev)))
+        res_scale, eps, *map(_ptr, o.values()), wp, wn, _current(dev)))
     return o
 
 
@@ -623,8 +628,8 @@ def quant_i8(x, stream=None, out=None):
     _tensor(dev, "q", q, (rows, cols), (torch.int8,))
     _tensor(dev, "scale", scale, (rows,), (torch.float32,))
     if out is None:
-        q = torch.empty((rows, cols), dtype=torch.int8, device=dev)
-        scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+        q = _empty(x, (rows, cols), torch.int8)
+        scale = _empty(x, (rows,), torch.float32)
     L = _lib or lib()
     _check(L.moe_quant_i8(x.data_ptr(), _CODE[x.dtype], rows, cols, q.data_ptr(), scale.data_ptr(), _current(dev)))
     return q, scale
@@ -650,10 +655,10 @@ def linear_i8(q, q_scale, w, w_scale, bias=None, *, out_dtype=None, out=None, ws
     _tensor(dev, "bias", bias, (N,), f32)
     _tensor(dev, "out", out, (T, N), (out_dtype,))
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=dev)
+        out = _empty(q_scale, (T, N), out_dtype)
     L = _lib or lib()
     need = L.moe_linear_i8_workspace_size(T, K, N)
-    ws = _scratch(ws, need, dev) if need or ws is not None else None
+    wp, wn, ws = _scratch(ws, need, q) if need else (None, 0, None)
     _check(L.moe_linear_i8(q.data_ptr(), q_scale.data_ptr(), T, K, w.data_ptr(), w_scale.data_ptr(), _ptr(bias), N,
-                           out.data_ptr(), _CODE[out.dtype], _ptr(ws), 0 if ws is None else _nbytes(ws), _current(dev)))
+                           out.data_ptr(), _CODE[out_dtype], wp, wn, _current(dev)))
     return out

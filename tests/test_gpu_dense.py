@@ -616,3 +616,75 @@ def test_runs_are_bitwise_equal():
         return [moe.ffn(f.x, f.bank), *moe.ffn_backward(f.dy, f.x, f.bank, gu), *n.values()]
     a, b = both(), both()
     assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("T,H,off", [(3, 1001, 0), (2, 264, 1), (70, 33, 0), (2, 9000, 0)])
+def test_norm_int8_rows_of_any_width(T, H, off):
+    c = norm_case(T, H, 11, gate_div=2, off=off)
+    kw = dict(post_w=c["post_w"], gate=c["gate"], gate_div=2, res_scale=0.75, pre_w=c["pre_w"])
+    q, gq = outbuf((T, H), I8)
+    s, gs = outbuf((T,), F32)
+    moe.norm(c["y"], c["res"], x=(q, s), **kw)
+    _, x32 = moe.norm(c["y"], c["res"], x_dtype=F32, **kw)
+    rq, rs = codes_of(x32)
+    assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+    gq()
+    gs()
+
+
+def test_norm_gradients_in_place():
+    """dres over dr and dy over dx, as the boundary allows for dres: every element is read before it is written."""
+    c = norm_case(70, 520, 12, gate_div=9)
+    want = check_norm_grads(c)
+    L, p = moe.lib(), lambda t: t.data_ptr()
+    dr = c["dr"].clone()
+    dy = torch.empty_like(c["y"])
+    ws = torch.empty(L.moe_norm_backward_workspace_size(70, 520, 9), dtype=torch.uint8, device="cuda")
+    st = L.moe_norm_backward(p(c["dx"]), 1, p(dr), p(c["y"]), 1, p(c["res"]), 1, 70, 520, p(c["post_w"]), p(c["gate"]), 9,
+                             p(c["pre_w"]), 0, 0.75, 1e-6, p(dy), p(dr), None, None, None, p(ws), ws.numel(),
+                             torch.cuda.current_stream().cuda_stream)
+    assert st == moe.MOE_OK
+    assert torch.equal(dr, want["dres"]) and torch.equal(dy, want["dy"])
+
+
+def test_one_bad_token_stays_alone():
+    """Inf and NaN in one token's row reach no other token's output."""
+    c = Ffn(70, 264, 136, 7)
+    good = moe.ffn(c.x, c.bank)
+    x = c.x.clone()
+    x[33] = float("inf")
+    x[33, 5] = float("nan")
+    y = moe.ffn(x, c.bank)
+    keep = torch.arange(70, device="cuda") != 33
+    assert torch.equal(y[keep], good[keep])
+    n = norm_case(9, 264, 13, gate_div=3)
+    r0, x0 = moe.norm(n["y"], n["res"], post_w=n["post_w"], gate=n["gate"], gate_div=3, pre_w=n["pre_w"])
+    yy = n["y"].clone()
+    yy[4] = float("nan")
+    r1, x1 = moe.norm(yy, n["res"], post_w=n["post_w"], gate=n["gate"], gate_div=3, pre_w=n["pre_w"])
+    keep = torch.arange(9, device="cuda") != 4
+    assert torch.equal(r0[keep], r1[keep]) and torch.equal(x0[keep], x1[keep])
+
+
+def test_two_graphs_with_one_workspace():
+    """Two captured calls that were given the same workspace, replayed in turn on one stream."""
+    a, b = Ffn(300, 264, 136, 8), Ffn(70, 520, 264, 9)
+    L = moe.lib()
+    ws = torch.empty(max(L.moe_ffn_workspace_size(300, 264, 136), L.moe_ffn_workspace_size(70, 520, 264)), dtype=torch.uint8,
+                     device="cuda")
+    want = [moe.ffn(c.x, c.bank) for c in (a, b)]
+    graphs, outs = [], []
+    for c in (a, b):
+        out = torch.empty_like(c.x)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.ffn(c.x, c.bank, out=out, ws=ws)
+        graphs.append(g)
+        outs.append(out)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
