@@ -458,13 +458,14 @@ def _scratch(ws, need, like):
 
 def _dense_bank(bank: Experts, H: int, device):
     bf = (torch.bfloat16,)
-    if bank.w_gate.dim() != 3:
-        raise ValueError("bank: weights are [1][I][H] and [1][H][I]")
-    I = bank.w_gate.shape[1]
-    _tensor(device, "w_gate", bank.w_gate, (1, I, H), bf)
-    _tensor(device, "w_up", bank.w_up, (1, I, H), bf)
-    _tensor(device, "w_down", bank.w_down, (1, H, I), bf)
-    return bank.struct(), I
+    wg, wu, wd = bank.w_gate, bank.w_up, bank.w_down
+    if wg.dim() != 3 or bank.dt not in (None, BF16):
+        raise ValueError("bank: bf16 weights [1][I][H] and [1][H][I]")
+    I = wg.shape[1]
+    _tensor(device, "w_gate", wg, (1, I, H), bf)
+    _tensor(device, "w_up", wu, (1, I, H), bf)
+    _tensor(device, "w_down", wd, (1, H, I), bf)
+    return ExpertsT(1, H, I, BF16, wg.data_ptr(), wu.data_ptr(), wd.data_ptr()), I
 
 
 def ffn(x, bank: Experts, *, want_gu: bool = False, y_dtype=None, out=None, gu=None, ws=None, stream=None):
