@@ -285,7 +285,7 @@ moe_status_t moe_layer_noalloc(const void* x, int32_t x_dt, int32_t T, int32_t H
  * model, or the always-on shared expert by itself), with its gradients:
  *     g = x W_gate, u = x W_up, h = silu(g) * u, y = h W_down
  * x: [T][H] MOE_BF16; bank: n = 1, dt MOE_BF16, H and I positive multiples of
- * 8 (the multiple of 128 that routed banks need does not apply here); y: [T][H]
+ * 8 up to 2^21 (the multiple of 128 that routed banks need does not apply here); y: [T][H]
  * MOE_BF16 or MOE_F32.  h is rounded to bf16 (nearest even) between the two
  * products; all sums are fp32.  gu: optional (NULL to skip) fp32 [T][2 I], row
  * t holding g[t][0..I) then u[t][0..I): what the backward pass needs of the

@@ -28,14 +28,17 @@ bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; 
 bool is_float(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 unsigned size_of(int dt) { return dt == MOE_F32 ? 4 : 2; }
 
+constexpr int kMaxFfn = 1 << 21;   // a tile's 256 rows of 2 I bf16 stay below 2^31 bytes
+
 // The bank of the dense block: n = 1, bf16, H and I multiples of 8.
 moe_status_t check_dense(const moe_experts_t* b, const char* name) {
     if (!b) return fail(MOE_ERR_INVALID, "%s: null bank", name);
     if (b->n != 1) return fail(MOE_ERR_INVALID, "%s: n = %d, expected 1", name, b->n);
     if (b->dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: weight dtype %d", name, b->dt);
     if (b->H <= 0 || b->I <= 0) return fail(MOE_ERR_INVALID, "%s: H=%d I=%d", name, b->H, b->I);
-    if (b->H % 8 || b->I % 8 || b->I > (1 << 29))
-        return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d I=%d must be multiples of 8", name, b->H, b->I);
+    if (b->H % 8 || b->I % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d I=%d must be multiples of 8", name, b->H, b->I);
+    if (b->H > kMaxFfn || b->I > kMaxFfn)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d I=%d > %d", name, b->H, b->I, kMaxFfn);
     if (!b->w_gate || !b->w_up || !b->w_down) return fail(MOE_ERR_INVALID, "%s: null weight pointer", name);
     if (!aligned(b->w_gate, 16) || !aligned(b->w_up, 16) || !aligned(b->w_down, 16))
         return fail(MOE_ERR_INVALID, "%s: weights must be 16-byte aligned", name);

@@ -28,10 +28,10 @@ namespace {
 constexpr int kKE = kStage / 2;
 
 Operand rows(const void* p, long ld, int n, const void* p2 = nullptr) {
-    return Operand{(const uint8_t*)p, (const uint8_t*)p2, (size_t)ld * 2, n, 0};
+    return Operand{(const uint8_t*)p, (const uint8_t*)p2, (size_t)ld * 2, n};
 }
-Operand cols(const void* p, long ld, int n, const void* p2 = nullptr, int split = 0) {
-    return Operand{(const uint8_t*)p, (const uint8_t*)p2, (size_t)ld * 2, n, split};
+Operand cols(const void* p, long ld, int n, const void* p2 = nullptr) {
+    return Operand{(const uint8_t*)p, (const uint8_t*)p2, (size_t)ld * 2, n};
 }
 
 Args base(int M, int N, int K) {
@@ -57,6 +57,9 @@ Forward forward(int T, int H, int I) {
     return f;
 }
 
+// k of dx = dg Wg + du Wu: dg's, and du's from the next stage on
+int turn_of(int I) { return (I + kKE - 1) / kKE * kKE; }
+
 struct Backward {
     Plan gateup, dh, dx, dwgu, dw1, dwd;   // dw1: one of the gate and up gradients alone
     size_t gu, dgu, h, part, total;
@@ -65,7 +68,7 @@ Backward backward(int T, int H, int I, bool has_gu) {
     Backward w;
     w.gateup = gateup_plan(T, H, I);
     w.dh = plan_tiles(T, I, H, kKE, false);
-    w.dx = plan_tiles(T, H, 2 * I, kKE, false);
+    w.dx = plan_tiles(T, H, turn_of(I) + I, kKE, false);
     w.dwgu = plan_tiles(2L * I, H, T, kKE, false);
     w.dw1 = plan_tiles(I, H, T, kKE, false);
     w.dwd = plan_tiles(H, I, T, kKE, false);
@@ -236,9 +239,11 @@ hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
     Product todo[3];
     int n = 0;
     if (p.dx) {
-        Args G = base(T, H, 2 * I);
-        G.A = rows(dgu, 2L * I, T);
-        G.B = cols(p.wg, H, H, p.wu, I);
+        Args G = base(T, H, turn_of(I) + I);
+        G.turn = turn_of(I);
+        G.len = I;
+        G.A = rows(dgu, 2L * I, T, dgu + (size_t)I * 2);
+        G.B = cols(p.wg, H, H, p.wu);
         G.out = p.dx;
         todo[n++] = {G, w.dx, 0};
     }

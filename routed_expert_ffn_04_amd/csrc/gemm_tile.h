@@ -31,7 +31,7 @@
 //
 // Bounds.  m and n past the end re-read the last row (last 16-byte chunk) and
 // are never stored; k past the end (the ragged last stage, and the stages that
-// the ring prefetches past it) reads a zero page, so it adds exactly nothing.
+// the ring prefetches past it) is loaded as zeros, so it adds exactly nothing.
 #pragma once
 #include "common.h"
 #include "gffn_common.h"
@@ -57,13 +57,13 @@ enum Epi {
 };
 
 constexpr int kStage = 128;  // bytes of k per stage
+constexpr uint32_t kFar = 1u << 31;   // past every byte of a tile: 256 rows of at most 2^23 bytes
 
 struct Operand {
     const uint8_t* p;    // element (row 0, k 0)
-    const uint8_t* p2;   // gate/up B: the up matrix; kCol with split < K: rows k >= split, as if they began at row split
+    const uint8_t* p2;   // gate/up B: the up matrix; with turn: element (row 0, k = turn)
     size_t ld;           // bytes from row to row (kRow: of m; kCol: of k)
     int n;               // rows m (kRow), columns m (kCol); gate/up B: I
-    int split;           // kCol: first k that p2 holds
 };
 
 struct Args {
@@ -71,6 +71,8 @@ struct Args {
     int M, N, K;         // N: output columns (gate/up: I)
     int mt, nt;          // tiles
     int splits, kspan;   // k-splits; k elements per split (a multiple of the stage)
+    int turn, len;       // a sum of two products (kRow A, kCol B; 0: none): k in [0, len) of p, k in [turn, K) of p2,
+                         // turn = len rounded up to the stage, so no stage has rows of both
     int vec;             // rows of the outputs allow 16-byte accesses
     void* out;           // kEpiOut / kEpiI8 / kEpiPart: [M][N]; kEpiGateUp: h; kEpiGrad: dgu
     void* out2;          // kEpiOut: rows m >= msplit, as if they began at row msplit; kEpiGrad: h; kEpiGateUp: gu (or null)
@@ -247,58 +249,75 @@ __device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
     const int kn = min(G.K - k0, G.kspan);                     // k elements of this split
     const int nst = (kn + KE - 1) / KE;
 
-    // ---- the lane's share of the direct loads: LD 16-byte slots in each half-stage
-    const uint8_t* pa[LD];
-    const uint8_t* pb[LD];
-    auto place = [&](int layout, const Operand& O, int r0, bool gu, const uint8_t*(&p)[LD]) __attribute__((always_inline)) {
+    // ---- the lane's share of the direct loads: LD 16-byte slots in each
+    // half-stage, at fixed offsets from a base that is the same in the whole wave
+    // (in scalar registers) and moves on by a stage
+    uint32_t offa[LD], offb[LD];
+    auto place = [&](int layout, const Operand& O, int r0, int half, uint32_t(&off)[LD]) __attribute__((always_inline)) {
 #pragma unroll
         for (int q = 0; q < LD; ++q) {
             const int at = (wave * LD + q) * 64 + lane;
             if (layout == kRow) {
                 const int r = at / 8, c = (at % 8) ^ row_key(r);
-                const bool up = gu && r >= BN / 2;
-                const int row = min(r0 + r - (up ? BN / 2 : 0), O.n - 1);
-                p[q] = (up ? O.p2 : O.p) + (size_t)row * O.ld + (size_t)k0 * EB + c * 16;
+                off[q] = (uint32_t)(min(r0 + r - half, O.n - 1) - r0) * (uint32_t)O.ld + c * 16;
             } else {
                 constexpr int per = BM * 2 / 16;                       // slots per k row
                 const int r = at / per, c = (at % per) ^ col_key<BM>(r);
-                p[q] = O.p + (size_t)(k0 + r) * O.ld + (size_t)min(r0 + c * 8, O.n - 8) * 2;
+                off[q] = (uint32_t)r * (uint32_t)O.ld + (min(r0 + c * 8, O.n - 8) - r0) * 2;
             }
         }
     };
-    place(LA, G.A, m0, false, pa);
-    place(LB, G.B, n0, GU, pb);
-    // k of a slot within its stage: kRow its chunk's first k, kCol its row
+    auto origin = [&](int layout, const Operand& O, const uint8_t* p, int r0) __attribute__((always_inline)) {
+        return layout == kRow ? p + (size_t)r0 * O.ld + (size_t)k0 * EB : p + (size_t)k0 * O.ld + (size_t)r0 * 2;
+    };
+    // gate/up: the waves that load the second half of the B rows take the up matrix
+    const bool up = GU && wave * LD * 8 >= BN / 2;
+    place(LA, G.A, m0, 0, offa);
+    place(LB, G.B, n0, up ? BN / 2 : 0, offb);
+    const uint8_t* pa = origin(LA, G.A, G.A.p, m0);
+    const uint8_t* pb = origin(LB, G.B, up ? G.B.p2 : G.B.p, n0);
+    // k of a slot within its stage: kRow its chunk's first, kCol its row
     const int kr = ((lane % 8) ^ (lane / 8)) * (16 / EB);             // q even; q odd: the neighbouring chunk
-    const int kc = wave * LD * (64 / (BM / 8)) + lane / (BM / 8);      // q = 0
+    const int kc = wave * LD * (64 / (BM / 8)) + lane / (BM / 8);     // q = 0
     auto k_of = [&](int layout, int q) __attribute__((always_inline)) {
         return layout == kRow ? kr ^ ((q & 1) * (16 / EB)) : kc + q * (64 / (BM / 8));
     };
-    // kCol B of two matrices (k < split in p, the rest in p2): the distance
-    // between the second's rows and where the first's would continue
-    const ptrdiff_t second = LB == kCol && G.B.p2 ? G.B.p2 - (G.B.p + (size_t)G.B.split * G.B.ld) : 0;
-    const int turn_at = LB == kCol && G.B.p2 ? G.B.split - k0 : 0x7fffffff;   // first k of this split in the second
+    // from where p would continue to p2, for the stages past the turn
+    constexpr bool TWO = LA == kRow && LB == kCol;
+    const int turn = TWO && G.turn ? G.turn - k0 : 0x7fffffff;
+    const ptrdiff_t past_a = TWO && G.turn ? G.A.p2 - (G.A.p + (size_t)G.turn * EB) : 0;
+    const ptrdiff_t past_b = TWO && G.turn ? G.B.p2 - (G.B.p + (size_t)G.turn * G.B.ld) : 0;
+    const int end1 = TWO && G.turn ? min(G.len - k0, kn) : kn;   // end of the stages before the turn
 
+    // Loads [q0, q1) of the half-stage that begins at k.  Buffer loads: base and
+    // bound in scalar registers, one 32-bit offset a lane, and slots past the end take
+    // an offset past the bound, which reads zero.
+    auto issue = [&](uint8_t* half, const uint8_t* p, ptrdiff_t past, const uint32_t(&off)[LD], int layout,
+                     int k, int q0, int q1) __attribute__((always_inline)) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass does not know the resource's type
+        const int left = (TWO && k >= turn ? kn : end1) - k;
+        auto rows = __builtin_amdgcn_make_buffer_rsrc((void*)(TWO && k >= turn ? p + past : p), 0, (int)kFar, 0x00027000);
+#pragma unroll
+        for (int q = q0; q < q1; ++q) {
+            const uint32_t at = k_of(layout, q) >= left ? kFar : off[q];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rows, (lds_void*)(half + (wave * LD + q) * 1024), 16, at, 0, 0, 0);
+        }
+#endif
+    };
     int ka = 0, kb = 0;   // first k of the next half-stages to load
     auto issueA = [&](uint8_t* half, int q0, int q1) __attribute__((always_inline)) {
-#pragma unroll
-        for (int q = q0; q < q1; ++q) {
-            const uint8_t* p = k_of(LA, q) < kn - ka ? pa[q] : (const uint8_t*)kZeros;
-            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)(half + (wave * LD + q) * 1024), 16, 0, 0);
-            pa[q] += LA == kRow ? (size_t)kStage : (size_t)KE * G.A.ld;
+        issue(half, pa, past_a, offa, LA, ka, q0, q1);
+        if (q1 == LD) {
+            ka += KE;
+            pa += LA == kRow ? (size_t)kStage : (size_t)KE * G.A.ld;
         }
-        if (q1 == LD) ka += KE;
     };
     auto issueB = [&](uint8_t* half, int q0, int q1) __attribute__((always_inline)) {
-#pragma unroll
-        for (int q = q0; q < q1; ++q) {
-            const uint8_t* p = pb[q];
-            if (LB == kCol) p += k_of(LB, q) >= turn_at - kb ? second : 0;
-            p = k_of(LB, q) < kn - kb ? p : (const uint8_t*)kZeros;
-            __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)(half + (wave * LD + q) * 1024), 16, 0, 0);
-            pb[q] += LB == kRow ? (size_t)kStage : (size_t)KE * G.B.ld;
+        issue(half, pb, past_b, offb, LB, kb, q0, q1);
+        if (q1 == LD) {
+            kb += KE;
+            pb += LB == kRow ? (size_t)kStage : (size_t)KE * G.B.ld;
         }
-        if (q1 == LD) kb += KE;
     };
 
     typename Acc<E>::type acc[IB][JB];

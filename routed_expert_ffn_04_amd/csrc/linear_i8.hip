@@ -97,8 +97,8 @@ size_t linear_i8_ws_bytes(int T, int K, int N) {
 hipError_t launch_linear_i8(const LinearI8Problem& p, void* ws, hipStream_t s) {
     Args G{};
     G.M = p.T; G.N = p.N; G.K = p.K; G.msplit = p.T;
-    G.A = Operand{(const uint8_t*)p.q, nullptr, (size_t)p.K, p.T, 0};
-    G.B = Operand{(const uint8_t*)p.w, nullptr, (size_t)p.K, p.N, 0};
+    G.A = Operand{(const uint8_t*)p.q, nullptr, (size_t)p.K, p.T};
+    G.B = Operand{(const uint8_t*)p.w, nullptr, (size_t)p.K, p.N};
     G.xs = p.xs; G.ws = p.ws; G.bias = p.bias;
     G.out = p.out;
     G.out_f32 = p.out_f32;

@@ -139,3 +139,10 @@ def test_binding_refuses_host_tensors():
     for call in (lambda: moe.quant_i8(x), lambda: moe.norm(x), lambda: moe.norm_backward(x, None, x, x)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("size", [dict(H=1 << 22), dict(I=1 << 22)])
+def test_ffn_refuses_rows_beyond_the_tile_offsets(size):
+    assert _ffn(bank=_bank(**size)) == moe.MOE_ERR_UNSUPPORTED
+    bank = _bank(**size)
+    assert moe.lib().moe_ffn_backward(P, P, moe.BF16, 4, ctypes.byref(bank), P, P, P, P, P, P, BIG, None) == moe.MOE_ERR_UNSUPPORTED

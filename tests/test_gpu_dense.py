@@ -688,3 +688,12 @@ def test_two_graphs_with_one_workspace():
             g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("T,H,I", [(20, 264, 72), (64, 512, 2504), (300, 264, 1000), (70, 1024, 2056), (600, 1032, 1144)])
+def test_ffn_dx_with_ragged_halves(T, H, I):
+    """dx sums over the gate's and the up's columns, whose last stages are not whole; alone it is split along k."""
+    c = Ffn(T, H, I, 11)
+    _, gu = moe.ffn(c.x, c.bank, want_gu=True)
+    c.check_grads(moe.ffn_backward(c.dy, c.x, c.bank, gu, need=("dx",)))
+    c.check_grads(moe.ffn_backward(c.dy, c.x, c.bank, gu, need=("dx", "dw_up")))
