@@ -1,5 +1,7 @@
 // Tile size and k-splits of a product, and the kernel that sums the splits.
 #pragma once
+#include <algorithm>
+
 #include "dense.h"
 #include "gemm_few.h"
 #include "gemm_tile.h"
@@ -15,12 +17,19 @@ struct Plan {
     double us;           // estimated time
 };
 
-// Estimated time of wg workgroups of `span` stages each, in us.
+// Estimated time of wg workgroups of `span` stages each, in us, fitted to
+// sweeps of every edge and number of splits.  64-row tiles share a CU's loads
+// (up to four at once, 0.21 us a stage each); 128-row tiles run two to a CU, where
+// a stage of each takes 0.95 us, against 0.5 with half of the CUs taken; a 256-row
+// tile's stage takes 1.1 us alone and 1.6 when the whole chip draws power.
 inline double tiling_us(int edge, long wg, int span) {
     auto rounds = [&](long at_once) { return (double)((wg + at_once - 1) / at_once); };
-    if (edge == 256) return rounds(256) * (span * 1.6 + 10);
-    if (edge == 128) return wg <= 256 ? span * 0.7 + 3 : rounds(512) * (span * 1.3 + 3);
-    return wg <= 256 ? span * 0.4 + 3 : wg <= 512 ? span * 0.5 + 3 : rounds(1024) * (span * 0.9 + 3);
+    if (edge == 256) {
+        const double full = std::min(1.0, wg / 256.0);
+        return rounds(256) * (span * (1.1 + 0.5 * full * full) + 10);
+    }
+    if (edge == 128) return wg <= 512 ? span * (0.35 + 0.6 * wg / 512.0) + 5 : rounds(512) * (span * 0.95 + 4) + 1;
+    return rounds(256) * (span * 0.21 + 0.25) + 3;
 }
 
 // The tiling with the least estimated time.
