@@ -5,13 +5,16 @@
 // A workgroup takes 16 weight rows (gate/up: 8 gate rows and the 8 up rows of
 // the same columns) for all tokens, its waves share out k in blocks of 128
 // bytes (whole cache lines), and every wave loads its MFMA operands straight
-// into registers, U blocks ahead.  Lane l holds weight row l % 16 and bytes [32
-// (l / 16), +32) of the block, the two 16-byte pieces for two MFMAs; tokens are
-// laid out the same way, so both sides agree on which k a piece holds.  The
+// into registers, one block ahead.  Lane l holds weight row l % 16 and bytes [16
+// (l / 16), +16) of the block's two halves, for two MFMAs; tokens are laid out the
+// same way, so both sides agree on which k a piece holds.  More blocks in flight a
+// wave cost more than they bring (four together, unpipelined: 7.4 us against 6.4 for
+// a token of 1024 x 512, 9.2 against 8.9 of 2048 x 1408, weights from HBM).  The
 // waves' sums meet in LDS in a fixed order and the epilogue follows, with no
 // second launch: k is split eight ways, and 16 rows a workgroup give enough
-// workgroups for every CU.  One token of the 7168 x 2048 block: 13.6 us and two
-// launches for 88 MB, 6.5 TB/s.
+// workgroups for every CU.  One token of the 7168 x 2048 block: 21.7 us and two
+// launches for 88 MB from HBM, 4.1 TB/s; two launches of next to nothing (256 x 512)
+// take 5.0.
 #pragma once
 #include "gemm_tile.h"
 
@@ -37,7 +40,6 @@ template <int E, int EPI, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args G) {
     constexpr bool GU = EPI == kEpiGateUp;
     constexpr int EB = E == kI8 ? 1 : 2;
-    constexpr int U = 4;   // blocks in flight per wave
     __shared__ __attribute__((aligned(16))) uint8_t sums[WAVES * 1024];
     const int lane = threadIdx.x % 64, r = lane % 16, c = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -47,30 +49,38 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args G) {
 
     const bool up = GU && r >= 8;
     const int wrow = min(n0 + (GU ? r % 8 : r), G.B.n - 1);
-    const uint8_t* wp = (up ? G.B.p2 : G.B.p) + (size_t)wrow * G.B.ld + c * 32;
-    const uint8_t* xp = G.A.p + (size_t)min(r, G.A.n - 1) * G.A.ld + c * 32;
-    const int left = kbytes - c * 32;   // bytes of the row from the lane's first piece on
+    const uint8_t* wp = (up ? G.B.p2 : G.B.p) + (size_t)wrow * G.B.ld + c * 16;
+    const uint8_t* xp = G.A.p + (size_t)min(r, G.A.n - 1) * G.A.ld + c * 16;
+    const int left = kbytes - c * 16;   // bytes of the row from the lane's first piece on
 
     typename Acc<E>::type acc{};
-    for (int b = wave; b < blocks; b += WAVES * U) {
-        i32x4 w[U][2], x[U][2];
+    struct Block { i32x4 w[2], x[2]; };
+    auto load = [&](int b, Block& t) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int off = (b + u * WAVES) * 128;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool in = off + h * 16 < left;
-                w[u][h] = *(const i32x4*)(in ? wp + off + h * 16 : (const uint8_t*)kZeros);
-                x[u][h] = i32x4{};
-                if (in && r < G.M) x[u][h] = *(const i32x4*)(xp + off + h * 16);
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int off = b * 128 + h * 64;
+            const bool in = off < left;
+            t.w[h] = *(const i32x4*)(in ? wp + off : (const uint8_t*)kZeros);
+            t.x[h] = i32x4{};
+            if (in && r < G.M) t.x[h] = *(const i32x4*)(xp + off);
         }
-        __builtin_amdgcn_sched_barrier(0);   // every load of the turn is out before the first product waits
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto mma = [&](const Block& t) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) acc = Acc<E>::mma(w[u][h], x[u][h], acc);
+        for (int h = 0; h < 2; ++h) acc = Acc<E>::mma(t.w[h], t.x[h], acc);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    Block even, odd;
+    int b = wave;
+    load(b, even);
+    for (; b + WAVES < blocks; b += 2 * WAVES) {
+        load(b + WAVES, odd);
+        mma(even);
+        if (b + 2 * WAVES < blocks) load(b + 2 * WAVES, even);
+        mma(odd);
     }
+    if (b < blocks) mma(even);
     *(typename Acc<E>::type*)(sums + threadIdx.x * 16) = acc;
     __syncthreads();
     if (wave > 0) return;
@@ -114,8 +124,9 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args G) {
     }
 }
 
-// Beyond 16 rows the 64-row tiles are faster (FFN of 7168 x 2048: 28 us here for 16
-// tokens, 40 for 32 in two blocks of 16, 33 in tiles for up to 64).
+// Beyond 16 rows the 64-row tiles take over.  At 16, weights from HBM: FFN of 1024 x
+// 512 7.6 us here and 9.7 in tiles, 4096 x 1024 14.1 and 17.3, 7168 x 2048 29.5 and
+// 27.6; two blocks of 16 rows here do not reach the tiles' 33 rows.
 constexpr int kFewRows = 16;
 
 template <int E, int EPI>
