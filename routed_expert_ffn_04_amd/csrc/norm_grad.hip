@@ -14,6 +14,8 @@
 // dy and dres are stored past the caches, where they would push out rows that
 // are still to be read: 4096 x 7168 in bf16, 80 us against 87 (the forward step is
 // 41 us against 49 with such stores and does without).
+#include <algorithm>
+
 #include "norm_row.h"
 
 namespace moe {
@@ -225,8 +227,15 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(int T, int H, Run
 }
 
 // Runs to aim for: one for each of the 256 CUs where a row takes 512 threads or more,
-// else two.
-inline int want_workers(int threads_per_row) { return threads_per_row >= 512 ? 256 : 512; }
+// two where it takes 256.  Where it takes a wave alone, the wave's own time for a row
+// (1.5 us) counts: four runs a CU and up to eight of 16 rows or more, as far as the
+// sums of that many runs (as many bytes as two rows each) cost less.  16384 x 512 in
+// bf16: 35 us with 1024 runs, 52 with 512; 2048 x 512: 16.7 and 15.0; 65536 x 128: 98
+// and 178, 67 with 2048.
+inline int want_workers(int threads_per_row, int T) {
+    if (threads_per_row > 64) return threads_per_row >= 512 ? 256 : 512;
+    return std::max(512, std::min({T / 4, std::max(1024, T / 16), 2048}));
+}
 
 // Threads per row and chunks per thread: the row, the weights and the gradients
 // of its columns all stay in registers.
@@ -245,7 +254,7 @@ inline int gate_rows(const NormProblem& p) { return p.gate ? (p.gate_div < p.T ?
 size_t norm_backward_ws_bytes(int T, int H, int gate_div) {
     using namespace norm;
     if (T <= 0) return 0;
-    const Runs r = runs_of(T, gate_div > 0 && gate_div < T ? gate_div : T, want_workers(shape_of(H).tpr));
+    const Runs r = runs_of(T, gate_div > 0 && gate_div < T ? gate_div : T, want_workers(shape_of(H).tpr, T));
     return 4 * align256((size_t)r.workers * H * 4);   // pre, post, two places for gates
 }
 
@@ -262,7 +271,7 @@ hipError_t launch_norm_backward(const NormProblem& p0, void* ws, hipStream_t s) 
                             !rows16(p.dgate);
         const bool wide = p.y_f32 || p.r_f32 || (p.dx && p.x_f32);
         const Shape sh = shape_of(p.H);
-        R = runs_of(p.T, gd, want_workers(sh.tpr));
+        R = runs_of(p.T, gd, want_workers(sh.tpr, p.T));
         const size_t step = align256((size_t)R.workers * p.H * 4);
         if (p.dpre_w) pre = (float*)ws;
         if (p.dpost_w) post = (float*)((uint8_t*)ws + step);

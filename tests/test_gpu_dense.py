@@ -697,3 +697,34 @@ def test_ffn_dx_with_ragged_halves(T, H, I):
     _, gu = moe.ffn(c.x, c.bank, want_gu=True)
     c.check_grads(moe.ffn_backward(c.dy, c.x, c.bank, gu, need=("dx",)))
     c.check_grads(moe.ffn_backward(c.dy, c.x, c.bank, gu, need=("dx", "dw_up")))
+
+
+@pytest.mark.parametrize("T,H,gate_div", [(4100, 72, 4100), (9000, 40, 7), (16500, 16, 300), (33000, 8, 33000)])
+def test_norm_backward_of_many_short_rows(T, H, gate_div):
+    """More and longer runs of rows: the parameter gradients against 64 bits, twice the same."""
+    c = norm_case(T, H, 5, gate_div=gate_div)
+    r, _ = moe.norm(c["y"], c["res"], post_w=c["post_w"], gate=c["gate"], gate_div=gate_div, pre_w=c["pre_w"], want_x=False)
+    call = lambda: moe.norm_backward(c["dx"], c["dr"], c["y"], r, post_w=c["post_w"], gate=c["gate"], gate_div=gate_div,
+                                     pre_w=c["pre_w"])
+    one, two = call(), call()
+    assert all(torch.equal(one[k], two[k]) for k in one)
+    y, rr, dx, dr = (t.double() for t in (c["y"], r, c["dx"], c["dr"]))
+    gate = c["gate"].double().repeat_interleave(gate_div, 0)[:T]
+    q = 1 / (rr.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    p = 1 / (y.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    g = dx * c["pre_w"].double()
+    d = dr + q * (g - rr * q * (g * rr * q).mean(1, keepdim=True))
+    # every term of a sum over the rows is off by its own few roundings (those of the row's
+    # sums, the root and the products: 40 at these widths), relative to the sizes of d's parts;
+    # the sums over the rows (runs of at most 64, then slices of the runs) by gamma of their depth
+    size = dr.abs() + q * (g.abs() + (rr * q).abs() * (g * rr * q).abs().mean(1, keepdim=True))
+    rel = 40 * 2.0 ** -24 + gamma(64 + 2048)
+    for name, ref, terms in (("dpre_w", (dx * rr * q).sum(0), (dx * rr * q).abs().sum(0)),
+                             ("dpost_w", (gate * d * y * p).sum(0), (gate.abs() * size * (y * p).abs()).sum(0))):
+        within(one[name], ref, rel * terms, name)
+    n = y * p * c["post_w"].double()
+    which = torch.arange(T, device="cuda") // gate_div
+    G = c["gate"].shape[0]
+    ref = torch.zeros(G, H, dtype=torch.float64, device="cuda").index_add_(0, which, d * n)
+    bound = torch.zeros(G, H, dtype=torch.float64, device="cuda").index_add_(0, which, size * n.abs())
+    within(one["dgate"], ref, rel * bound, "dgate")
