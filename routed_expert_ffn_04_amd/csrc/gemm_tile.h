@@ -20,6 +20,11 @@
 // third less from LDS but have nothing to run while they wait: T = 16384 FFN
 // 1187 us against 1179, T = 4096 gradients 729 against 664.
 //
+// What binds: the largest products the matrix cores at the clock the power limit
+// leaves (FFN of 16384 tokens, 7168 x 2048, 1110 us = 1.30 PFLOP/s; int8 8192 x 7168 x
+// 4096 200 us = 2.4 Pop/s; with every load from the same few lines 10 % less), small
+// tiles the loads into LDS (0.21 us a stage of 64 rows, 16 KiB).
+//
 // Row pieces of 128 bytes, whole cache lines: a kernel that only loads moves 32
 // KiB per CU into LDS in 0.36 us with 128-byte pieces and in 0.5 to 0.75 us
 // with 64-byte ones, and the loads are what limits a stage first.

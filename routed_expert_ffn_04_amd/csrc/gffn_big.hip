@@ -15,8 +15,7 @@
 //         block and stage: a whole 128-wide scaling block.  Its partial joins
 //         the fp32 accumulator with one FMA by (activation scale x weight
 //         scale); the products are formed once per row and stage in LDS.
-//   bf16: v_mfma_f32_32x32x16_bf16 (the 16x16x32 form runs at half rate on
-//         gfx950), four per 32x32 block and stage.
+//   bf16: v_mfma_f32_32x32x16_bf16, four per 32x32 block and stage.
 // The gate/up epilogue applies SwiGLU and quantises h per row and 128-column
 // block (e4m3) or rounds it (bf16); the down epilogue writes y.
 //
