@@ -289,7 +289,8 @@ moe_status_t moe_layer_noalloc(const void* x, int32_t x_dt, int32_t T, int32_t H
  * MOE_BF16 or MOE_F32.  h is rounded to bf16 (nearest even) between the two
  * products; all sums are fp32.  gu: optional (NULL to skip) fp32 [T][2 I], row
  * t holding g[t][0..I) then u[t][0..I): what the backward pass needs of the
- * forward pass.  All tensors 16-byte aligned. */
+ * forward pass.  All tensors 16-byte aligned, T at most 2^30; no output may
+ * overlap an input or another output. */
 moe_status_t moe_ffn(const void* x, int32_t x_dt, int32_t T, const moe_experts_t* bank, void* y, int32_t y_dt,
                      float* gu, void* ws, size_t ws_bytes, void* stream);
 /* 0 for invalid sizes and for T = 0. */
@@ -304,7 +305,8 @@ size_t moe_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
  * to.  Each output may be NULL (not computed).  gu: what moe_ffn wrote for the
  * same x and bank, or NULL to compute it again (the workspace then also holds
  * it: has_gu = 0 in the size query).  dg, du and h are rounded to bf16 before
- * the next product.  T = 0 writes zero weight gradients. */
+ * the next product.  T = 0 writes zero weight gradients.  No output may overlap
+ * an input or another output. */
 moe_status_t moe_ffn_backward(const void* dy, const void* x, int32_t dt, int32_t T, const moe_experts_t* bank,
                               const float* gu, void* dx, void* dw_gate, void* dw_up, void* dw_down, void* ws,
                               size_t ws_bytes, void* stream);
@@ -324,7 +326,8 @@ size_t moe_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I, int32_t 
  * per sequence, 1 one per token.  r_out or x_out may be NULL (not written, but
  * not both).  x is formed from r before r is rounded to r_dt.  fp32
  * arithmetic; 1 <= H <= 16384, any alignment to the element (16 bytes and H a
- * multiple of 8 are faster). */
+ * multiple of 8 are faster).  Apart from r_out and res, no output may overlap
+ * another tensor. */
 moe_status_t moe_norm(const void* y, int32_t y_dt, const void* res, int32_t r_dt, int32_t T, int32_t H,
                       const void* post_w, const void* gate, int32_t gate_div, const void* pre_w, int32_t w_dt,
                       float res_scale, float eps, void* r_out, void* x_out, int32_t x_dt, float* x_scale,
@@ -347,7 +350,8 @@ size_t moe_norm_backward_workspace_size(int32_t T, int32_t H, int32_t gate_div);
 /* ---- int8 product with a scale per token and per output channel ------------
  * moe_quant_i8, per row: scale = max|v| / 127 (1 where that is 0), code =
  * round-to-nearest-even(v / scale), both IEEE fp32 divisions, codes in
- * [-127, 127].  x: [rows][cols] MOE_F32 or MOE_BF16, cols % 16 == 0. */
+ * [-127, 127].  x: [rows][cols] MOE_F32 or MOE_BF16, cols % 16 == 0.  A row with
+ * infinities or NaN gets codes without meaning; other rows are as without it. */
 moe_status_t moe_quant_i8(const void* x, int32_t x_dt, int32_t rows, int32_t cols, int8_t* q, float* scale,
                           void* stream);
 
@@ -355,7 +359,8 @@ moe_status_t moe_quant_i8(const void* x, int32_t x_dt, int32_t rows, int32_t col
  * q: [T][K] codes with q_scale [T] (of moe_quant_i8, or of moe_norm with int8
  * x); w: [N][K] int8 with one scale per output channel w_scale [N]; bias: fp32
  * [N] or NULL; out: [T][N] MOE_F32 or MOE_BF16.  The sum is exact (int32); it
- * is rounded to fp32 once, then scaled.  K % 16 == 0, K <= 131071; any N. */
+ * is rounded to fp32 once, then scaled.  K % 16 == 0, K <= 131071; T and N up
+ * to 2^30. */
 moe_status_t moe_linear_i8(const int8_t* q, const float* q_scale, int32_t T, int32_t K, const int8_t* w,
                            const float* w_scale, const float* bias, int32_t N, void* out, int32_t out_dt, void* ws,
                            size_t ws_bytes, void* stream);

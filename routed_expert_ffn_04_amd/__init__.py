@@ -453,6 +453,8 @@ def _scratch(ws, need, like):
         return ws.data_ptr(), need, ws
     if ws.get_device() != like.get_device():
         raise ValueError(f"ws is on {ws.device}, expected {like.device}")
+    if not ws.is_contiguous():   # its bytes are taken in one piece
+        raise ValueError("ws is not contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 

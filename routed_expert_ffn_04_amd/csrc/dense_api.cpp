@@ -28,7 +28,8 @@ bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; 
 bool is_float(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 unsigned size_of(int dt) { return dt == MOE_F32 ? 4 : 2; }
 
-constexpr int kMaxFfn = 1 << 21;   // a tile's 256 rows of 2 I bf16 stay below 2^31 bytes
+constexpr int kMaxFfn = 1 << 21;    // a tile's 256 rows of 2 I bf16 stay below 2^31 bytes
+constexpr int kMaxRows = 1 << 30;   // rows and tiles are counted in 32 bits
 
 // The bank of the dense block: n = 1, bf16, H and I multiples of 8.
 moe_status_t check_dense(const moe_experts_t* b, const char* name) {
@@ -43,6 +44,10 @@ moe_status_t check_dense(const moe_experts_t* b, const char* name) {
     if (!aligned(b->w_gate, 16) || !aligned(b->w_up, 16) || !aligned(b->w_down, 16))
         return fail(MOE_ERR_INVALID, "%s: weights must be 16-byte aligned", name);
     return MOE_OK;
+}
+
+bool dense_sizes(int T, int H, int I) {
+    return T >= 0 && T <= kMaxRows && H > 0 && I > 0 && H % 8 == 0 && I % 8 == 0 && H <= kMaxFfn && I <= kMaxFfn;
 }
 
 constexpr int kMaxNormH = 16384;
@@ -66,7 +71,7 @@ extern "C" {
 
 // ------------------------------------------------------------------ dense FFN
 size_t moe_ffn_workspace_size(int32_t T, int32_t H, int32_t I) {
-    if (T < 0 || H <= 0 || I <= 0 || H % 8 || I % 8) return 0;
+    if (!dense_sizes(T, H, I)) return 0;
     return moe::ffn_ws_bytes(T, H, I);
 }
 
@@ -75,6 +80,7 @@ moe_status_t moe_ffn(const void* x, int32_t x_dt, int32_t T, const moe_experts_t
     moe_status_t st = check_dense(bank, "ffn");
     if (st) return st;
     if (T < 0) return fail(MOE_ERR_INVALID, "ffn: T=%d", T);
+    if (T > kMaxRows) return fail(MOE_ERR_UNSUPPORTED, "ffn: T=%d > %d", T, kMaxRows);
     if (x_dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "ffn: x dtype %d", x_dt);
     if (!is_float(y_dt)) return fail(MOE_ERR_UNSUPPORTED, "ffn: y dtype %d", y_dt);
     if (T == 0) return MOE_OK;
@@ -91,7 +97,7 @@ moe_status_t moe_ffn(const void* x, int32_t x_dt, int32_t T, const moe_experts_t
 }
 
 size_t moe_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I, int32_t has_gu) {
-    if (T < 0 || H <= 0 || I <= 0 || H % 8 || I % 8) return 0;
+    if (!dense_sizes(T, H, I)) return 0;
     return moe::ffn_backward_ws_bytes(T, H, I, has_gu);
 }
 
@@ -101,6 +107,7 @@ moe_status_t moe_ffn_backward(const void* dy, const void* x, int32_t dt, int32_t
     moe_status_t st = check_dense(bank, "ffn_backward");
     if (st) return st;
     if (T < 0) return fail(MOE_ERR_INVALID, "ffn_backward: T=%d", T);
+    if (T > kMaxRows) return fail(MOE_ERR_UNSUPPORTED, "ffn_backward: T=%d > %d", T, kMaxRows);
     if (dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "ffn_backward: dtype %d", dt);
     if (!aligned(dx, 16) || !aligned(dw_gate, 16) || !aligned(dw_up, 16) || !aligned(dw_down, 16) || !aligned(dy, 16) ||
         !aligned(x, 16) || !aligned(gu, 16))
@@ -194,7 +201,7 @@ moe_status_t moe_quant_i8(const void* x, int32_t x_dt, int32_t rows, int32_t col
 }
 
 size_t moe_linear_i8_workspace_size(int32_t T, int32_t K, int32_t N) {
-    if (T < 0 || K <= 0 || N <= 0 || K % 16 || K > kMaxI8K) return 0;
+    if (T < 0 || K <= 0 || N <= 0 || K % 16 || K > kMaxI8K || T > kMaxRows || N > kMaxRows) return 0;
     return moe::linear_i8_ws_bytes(T, K, N);
 }
 
@@ -204,6 +211,7 @@ moe_status_t moe_linear_i8(const int8_t* q, const float* q_scale, int32_t T, int
     if (T < 0 || K <= 0 || N <= 0) return fail(MOE_ERR_INVALID, "linear_i8: T=%d K=%d N=%d", T, K, N);
     if (K % 16 || K > kMaxI8K)
         return fail(MOE_ERR_UNSUPPORTED, "linear_i8: K=%d must be a multiple of 16, at most %d", K, kMaxI8K);
+    if (T > kMaxRows || N > kMaxRows) return fail(MOE_ERR_UNSUPPORTED, "linear_i8: T=%d N=%d > %d", T, N, kMaxRows);
     if (!is_float(out_dt)) return fail(MOE_ERR_UNSUPPORTED, "linear_i8: out dtype %d", out_dt);
     if (T == 0) return MOE_OK;
     if (!q || !q_scale || !w || !w_scale || !out) return fail(MOE_ERR_INVALID, "%s", "linear_i8: null pointer");

@@ -134,7 +134,7 @@ hipError_t launch_together(const Product* todo, int n, hipStream_t s) {
         P.weight[i] = todo[i].weight;
         P.first[i] = (int)total;
         total += count_tiles(P.G[i], EDGE, EDGE);
-        if (total > 0x7fffffffL) return hipErrorInvalidValue;
+        if (!grid_fits(total, tile_threads(EDGE))) return hipErrorInvalidValue;
     }
     for (int i = n; i < 4; ++i) P.first[i] = (int)total;
     static DeviceCache ready;

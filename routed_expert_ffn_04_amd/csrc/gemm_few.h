@@ -132,7 +132,9 @@ constexpr int kFewRows = 16;
 template <int E, int EPI>
 hipError_t launch_few(const Args& G, hipStream_t s) {
     constexpr int cols = EPI == kEpiGateUp ? 8 : 16;
-    few_kernel<E, EPI, 8><<<dim3((G.N + cols - 1) / cols), dim3(512), 0, s>>>(G);
+    const long blocks = ((long)G.N + cols - 1) / cols;
+    if (!grid_fits(blocks, 512)) return hipErrorInvalidValue;
+    few_kernel<E, EPI, 8><<<dim3((unsigned)blocks), dim3(512), 0, s>>>(G);
     return hipGetLastError();
 }
 

@@ -158,8 +158,8 @@ template <int EPI>
 hipError_t launch_reduce(const Args& G, const float* part, int splits, hipStream_t s) {
     const long threads = (long)G.M * ((G.N + 7) / 8);
     const long blocks = (threads + 255) / 256;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
+    if (!grid_fits(blocks, 256)) return hipErrorInvalidValue;
     reduce_kernel<EPI><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(G, part, splits);
     return hipGetLastError();
 }

@@ -222,6 +222,9 @@ __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& t
     tm = band * 8 + t % rows;
 }
 
+// A grid holds fewer than 2^32 threads.
+inline bool grid_fits(long blocks, int threads) { return blocks > 0 && blocks <= 0xffffffffL / threads; }
+
 // Launch shape of the tiles: threads, and workgroups per CU (by LDS).
 constexpr int tile_threads(int edge) { return edge == 256 ? 512 : 256; }
 constexpr int tile_lds(int edge, int ring) { return ring * edge * kStage; }
@@ -651,7 +654,7 @@ hipError_t launch_tiles(Args G, hipStream_t s) {
     static DeviceCache ready;
     if (!allow_lds(ready, k, tile_lds(BM, R))) return hipErrorInvalidValue;
     const long total = count_tiles(G, BM, GU ? BN / 2 : BN);
-    if (total <= 0 || total > 0x7fffffffL) return hipErrorInvalidValue;
+    if (!grid_fits(total, tile_threads(BM))) return hipErrorInvalidValue;
     k<<<dim3((unsigned)total), dim3(tile_threads(BM)), tile_lds(BM, R), s>>>(G);
     return hipGetLastError();
 }

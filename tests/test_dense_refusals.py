@@ -146,3 +146,14 @@ def test_ffn_refuses_rows_beyond_the_tile_offsets(size):
     assert _ffn(bank=_bank(**size)) == moe.MOE_ERR_UNSUPPORTED
     bank = _bank(**size)
     assert moe.lib().moe_ffn_backward(P, P, moe.BF16, 4, ctypes.byref(bank), P, P, P, P, P, P, BIG, None) == moe.MOE_ERR_UNSUPPORTED
+
+
+def test_row_counts_beyond_32_bit_tiles_are_refused():
+    most = (1 << 31) - 1
+    assert _ffn(T=most) == moe.MOE_ERR_UNSUPPORTED
+    assert moe.lib().moe_ffn_workspace_size(most, 64, 32) == 0
+    bank = _bank()
+    assert moe.lib().moe_ffn_backward(P, P, moe.BF16, most, ctypes.byref(bank), P, P, P, P, P, P, BIG, None) == moe.MOE_ERR_UNSUPPORTED
+    for T, N in ((most, 8), (4, most)):
+        assert moe.lib().moe_linear_i8(P, P, T, 64, P, P, None, N, P, moe.F32, P, BIG, None) == moe.MOE_ERR_UNSUPPORTED
+        assert moe.lib().moe_linear_i8_workspace_size(T, 64, N) == 0

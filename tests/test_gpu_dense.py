@@ -728,3 +728,24 @@ def test_norm_backward_of_many_short_rows(T, H, gate_div):
     ref = torch.zeros(G, H, dtype=torch.float64, device="cuda").index_add_(0, which, d * n)
     bound = torch.zeros(G, H, dtype=torch.float64, device="cuda").index_add_(0, which, size * n.abs())
     within(one["dgate"], ref, rel * bound, "dgate")
+
+
+def test_workspace_in_pieces_is_refused():
+    """A workspace whose elements are not one piece of memory: more bytes than it has would be written."""
+    c = Ffn(40, 64, 64, 4)
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20),
+               torch.empty(1 << 11, 1 << 10, dtype=torch.uint8, device="cuda")[:, :1 << 9]):
+        with pytest.raises(ValueError, match="contiguous"):
+            moe.ffn(c.x, c.bank, ws=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            moe.ffn_backward(c.dy, c.x, c.bank, ws=ws)
+
+
+def test_quant_i8_of_more_rows_than_a_grid_holds():
+    rows, cols = (1 << 24) + 3, 16
+    x = (torch.arange(rows, device="cuda", dtype=torch.int32)[:, None] % 251 - 125).to(BF) * torch.ones(cols, dtype=BF, device="cuda")
+    x[:, 0] = 127
+    q, s = moe.quant_i8(x)
+    assert bool((s == 1).all())
+    assert torch.equal(q[:, 0], torch.full((rows,), 127, dtype=torch.int8, device="cuda"))
+    assert torch.equal(q[:, 15].to(torch.int32), torch.arange(rows, device="cuda", dtype=torch.int32) % 251 - 125)
