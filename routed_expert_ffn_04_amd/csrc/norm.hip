@@ -134,7 +134,7 @@ hipError_t launch_norm(const NormProblem& p, hipStream_t s) {
     }
 #define X(TPR, NV, PERCU) \
     Y(TPR, NV, false, false, PERCU) Y(TPR, NV, true, false, PERCU) Y(TPR, NV, false, true, PERCU) Y(TPR, NV, true, true, PERCU)
-    X(64, 1, 8) X(256, 1, 8) X(512, 2, 2) X(1024, 2, 1)
+    X(64, 1, 8) X(128, 1, 8) X(256, 1, 8) X(512, 2, 2) X(1024, 2, 1)
 #undef X
 #undef Y
     return hipErrorInvalidValue;

@@ -227,13 +227,14 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(int T, int H, Run
 }
 
 // Runs to aim for: one for each of the 256 CUs where a row takes 512 threads or more,
-// two where it takes 256.  Where it takes a wave alone, the wave's own time for a row
+// two where it takes 256.  Where it takes a wave or two, their own time for a row
 // (1.5 us) counts: four runs a CU and up to eight of 16 rows or more, as far as the
-// sums of that many runs (as many bytes as two rows each) cost less.  16384 x 512 in
-// bf16: 35 us with 1024 runs, 52 with 512; 2048 x 512: 16.7 and 15.0; 65536 x 128: 98
-// and 178, 67 with 2048.
+// sums of that many runs (as many bytes as two rows each) cost less.  bf16: 16384 x 512
+// 35 us with 1024 runs and 52 with 512, 2048 x 512 16.7 and 15.0, 65536 x 128 98 and 178,
+// 67 with 2048; 16384 x 1024 52 with 1024 and 63 with 512 (75 in 256 threads a row, half of
+// them idle).
 inline int want_workers(int threads_per_row, int T) {
-    if (threads_per_row > 64) return threads_per_row >= 512 ? 256 : 512;
+    if (threads_per_row > 128) return threads_per_row >= 512 ? 256 : 512;
     return std::max(512, std::min({T / 4, std::max(1024, T / 16), 2048}));
 }
 
@@ -244,7 +245,7 @@ struct Shape {
 };
 inline Shape shape_of(int H) {
     const int units = (H + kVec - 1) / kVec;
-    return units <= 64 ? Shape{64, 1} : units <= 256 ? Shape{256, 1} : units <= 1024 ? Shape{512, 2} : Shape{1024, 2};
+    return units <= 64 ? Shape{64, 1} : units <= 128 ? Shape{128, 1} : units <= 256 ? Shape{256, 1} : units <= 1024 ? Shape{512, 2} : Shape{1024, 2};
 }
 
 inline int gate_rows(const NormProblem& p) { return p.gate ? (p.gate_div < p.T ? p.gate_div : p.T) : (p.T > 0 ? p.T : 1); }
@@ -282,7 +283,7 @@ hipError_t launch_norm_backward(const NormProblem& p0, void* ws, hipStream_t s) 
     if (sh.tpr == TPR && wide == WIDE && ragged == RAGGED)            \
         norm_grad_kernel<TPR, NV, WIDE, RAGGED><<<dim3(grid), dim3(threads), 0, s>>>(p, R, pre, post, gate);
 #define X(TPR, NV) Y(TPR, NV, false, false) Y(TPR, NV, true, false) Y(TPR, NV, false, true) Y(TPR, NV, true, true)
-        X(64, 1) X(256, 1) X(512, 2) X(1024, 2)
+        X(64, 1) X(128, 1) X(256, 1) X(512, 2) X(1024, 2)
 #undef X
 #undef Y
         const hipError_t e = hipGetLastError();

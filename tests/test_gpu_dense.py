@@ -749,3 +749,15 @@ def test_quant_i8_of_more_rows_than_a_grid_holds():
     assert bool((s == 1).all())
     assert torch.equal(q[:, 0], torch.full((rows,), 127, dtype=torch.int8, device="cuda"))
     assert torch.equal(q[:, 15].to(torch.int32), torch.arange(rows, device="cuda", dtype=torch.int32) % 251 - 125)
+
+
+@pytest.mark.parametrize("T,H", [(1, 1024), (5, 520), (131, 1001), (700, 768), (9, 1023)])
+@pytest.mark.parametrize("y,r,w", [(BF, BF, F32), (F32, F32, BF)])
+def test_norm_of_medium_rows(T, H, y, r, w):
+    """Rows of two waves: both directions against the 64-bit form, with a gate that ends inside a run."""
+    c = norm_case(T, H, 7, y=y, r=r, w=w, gate_div=3)
+    ref_r, ref_x, er, ex = norm_ref(c)
+    got_r, got_x = moe.norm(c["y"], c["res"], post_w=c["post_w"], gate=c["gate"], gate_div=3, res_scale=0.75,
+                            pre_w=c["pre_w"], x_dtype=F32)
+    within(got_r, ref_r, er + HALF[r] * (ref_r.abs() + er), "r")
+    within(got_x, ref_x, ex + HALF[F32] * (ref_x.abs() + ex), "x")
