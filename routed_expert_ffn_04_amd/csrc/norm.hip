@@ -123,6 +123,8 @@ hipError_t launch_norm(const NormProblem& p, hipStream_t s) {
     const bool wide = p.y_f32 || (p.res && p.r_f32);
     const int units = (p.H + kVec - 1) / kVec;
     // The narrowest shape that holds a row; runs that give every CU PERCU workgroups, or one row each.
+    // Half-empty shapes cost: 16384 x 1024 in bf16 26 us in 128 threads a row and 37.5 in 256,
+    // 8192 x 2560 31 in 256 threads of two chunks and 50 in 512.
 #define Y(TPR, NV, WIDE, RAGGED, PERCU)                                                                  \
     if (ragged == RAGGED && wide == WIDE && units <= TPR * NV) {                                         \
         constexpr int threads = TPR < 256 ? 256 : TPR, workers = threads / TPR;                          \
@@ -134,7 +136,7 @@ hipError_t launch_norm(const NormProblem& p, hipStream_t s) {
     }
 #define X(TPR, NV, PERCU) \
     Y(TPR, NV, false, false, PERCU) Y(TPR, NV, true, false, PERCU) Y(TPR, NV, false, true, PERCU) Y(TPR, NV, true, true, PERCU)
-    X(64, 1, 8) X(128, 1, 8) X(256, 1, 8) X(512, 2, 2) X(1024, 2, 1)
+    X(64, 1, 8) X(128, 1, 8) X(256, 1, 8) X(256, 2, 4) X(512, 2, 2) X(1024, 2, 1)
 #undef X
 #undef Y
     return hipErrorInvalidValue;

@@ -761,3 +761,18 @@ def test_norm_of_medium_rows(T, H, y, r, w):
                             pre_w=c["pre_w"], x_dtype=F32)
     within(got_r, ref_r, er + HALF[r] * (ref_r.abs() + er), "r")
     within(got_x, ref_x, ex + HALF[F32] * (ref_x.abs() + ex), "x")
+
+
+@pytest.mark.parametrize("T,H", [(1, 2056), (37, 2560), (1100, 4096), (300, 4095), (3, 2049)])
+@pytest.mark.parametrize("y,r,w", [(BF, BF, F32), (F32, F32, BF), (BF, F32, F32)])
+def test_norm_of_rows_of_two_chunks(T, H, y, r, w):
+    """Rows that a thread holds in two chunks, with runs of more than one row."""
+    c = norm_case(T, H, 8, y=y, r=r, w=w, gate_div=5)
+    ref_r, ref_x, er, ex = norm_ref(c)
+    kw = dict(post_w=c["post_w"], gate=c["gate"], gate_div=5, res_scale=0.75, pre_w=c["pre_w"])
+    got_r, got_x = moe.norm(c["y"], c["res"], x_dtype=F32, **kw)
+    within(got_r, ref_r, er + HALF[r] * (ref_r.abs() + er), "r")
+    within(got_x, ref_x, ex + HALF[F32] * (ref_x.abs() + ex), "x")
+    _, (q, s) = moe.norm(c["y"], c["res"], x_dtype=torch.int8, **kw)
+    off = (q.double() * s.double()[:, None] - ref_x).abs()   # half a step, and x's own error
+    assert bool((off <= 0.5 * s.double()[:, None] * (1 + 2.0 ** -16) + 2 * ex).all())
