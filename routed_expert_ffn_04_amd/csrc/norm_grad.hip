@@ -95,7 +95,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
 #pragma unroll
             for (int v = 0; v < NV; ++v) weights<RAGGED>(P.gate, P.w_f32, g0 + col(v), H - col(v), gw[v]);
         }
-        // absent weights are ones, absent gradients and rows zeros: one formula for all
+        // absent weights are ones, absent gradients and rows zeros: one formula for all.
+        // The rows that a run lacks at its end take an eps of their own: with P.eps = 0 their
+        // 1 / rms would be infinite, and its products with their zeros NaN in the sums
+        const float eps = live ? P.eps : 1.0f;
         float d[NV][kVec], y[NV][kVec];
         float q = 0.0f, c = 0.0f;   // 1 / rms(r), mean(dx pre_w r) / rms(r)^3
         if (P.dx) {
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
                 }
             }
             row_reduce<TPR, 2>(sum, slot, turn);
-            q = 1.0f / sqrtf(sum[0] * inv_h + P.eps);
+            q = 1.0f / sqrtf(sum[0] * inv_h + eps);
             c = sum[1] * inv_h * q * q * q;
         }
         float sy[2] = {0.0f, 0.0f};   // y y, dn post_w y
@@ -141,7 +144,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormPr
         float p = 1.0f, b = 0.0f;   // 1 / rms(y), mean(dn post_w y) / rms(y)^3
         if (P.post_w) {
             row_reduce<TPR, 2>(sy, slot, turn);
-            p = 1.0f / sqrtf(sy[0] * inv_h + P.eps);
+            p = 1.0f / sqrtf(sy[0] * inv_h + eps);
             b = sy[1] * inv_h * p * p * p;
         }
 #pragma unroll
