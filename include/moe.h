@@ -350,8 +350,10 @@ size_t moe_norm_backward_workspace_size(int32_t T, int32_t H, int32_t gate_div);
 /* ---- int8 product with a scale per token and per output channel ------------
  * moe_quant_i8, per row: scale = max|v| / 127 (1 where that is 0), code =
  * round-to-nearest-even(v / scale), both IEEE fp32 divisions, codes in
- * [-127, 127].  x: [rows][cols] MOE_F32 or MOE_BF16, cols % 16 == 0.  A row with
- * infinities or NaN gets codes without meaning; other rows are as without it. */
+ * [-127, 127].  x: [rows][cols] MOE_F32 or MOE_BF16, cols % 16 == 0.  A row with a
+ * NaN gets the scale NaN, one with infinities an infinite scale, and both codes
+ * without meaning: the row's outputs of moe_linear_i8 are then NaN or infinite.
+ * Other rows are as without it. */
 moe_status_t moe_quant_i8(const void* x, int32_t x_dt, int32_t rows, int32_t cols, int8_t* q, float* scale,
                           void* stream);
 

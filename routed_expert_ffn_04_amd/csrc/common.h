@@ -74,10 +74,16 @@ __device__ __forceinline__ float mx_inv_scale(uint32_t E) { return __uint_as_flo
 // ---- int8 with one fp32 scale per row -----------------------------------------
 // scale = amax / 127 (1 where that is 0), code = rne(v / scale), both IEEE fp32
 // divisions.  The clamp only acts where the scale is subnormal and has lost
-// bits.
+// bits.  A NaN anywhere in the row makes amax, and with it the scale, NaN, so that
+// it reaches whatever is formed from the codes (which cannot hold it).
 __device__ __forceinline__ float i8_scale(float amax) {
     const float s = amax / 127.0f;
-    return s > 0.0f ? s : 1.0f;
+    return s == 0.0f ? 1.0f : s;
+}
+// The larger of two magnitudes (sign bit clear), by their bits: these order like
+// the values, with NaN above infinity, where fmaxf would drop it.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
 }
 __device__ __forceinline__ uint32_t i8_code(float v, float scale) {
     return (uint32_t)(int)fminf(fmaxf(rintf(v / scale), -127.0f), 127.0f) & 0xFFu;

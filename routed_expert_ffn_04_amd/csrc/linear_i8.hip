@@ -1,6 +1,6 @@
 // int8 product with a scale per token and per output channel (moe_linear_i8),
 // and the per-token quantisation that feeds it (moe_quant_i8).
-//   q[t][k] = rne(x[t][k] / s_t),  s_t = amax_t / 127 (IEEE divisions; 1 where that is 0)
+//   q[t][k] = rne(x[t][k] / s_t),  s_t = amax_t / 127 (IEEE divisions; 1 where that is 0, NaN with a NaN in the row)
 //   out[t][n] = (sum_k q[t][k] w[n][k]) * (s_t * w_scale[n]) + bias[n]
 // The sum is exact in int32 (K <= 131071 keeps 128 * 128 * K below 2^31); it is
 // converted to fp32 once (nearest even) and scaled.
@@ -50,18 +50,18 @@ __global__ __launch_bounds__(256) void quant_i8_kernel(const void* __restrict__ 
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(held[i][e]));
+        for (int e = 0; e < 8; ++e) amax = max_magnitude(amax, fabsf(held[i][e]));
     for (int c = kWide + tid * 8; c < cols; c += 2048) {
         float v[8];
         load(c, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+        for (int e = 0; e < 8; ++e) amax = max_magnitude(amax, fabsf(v[e]));
     }
 #pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m, kWave));
+    for (int m = 32; m >= 1; m >>= 1) amax = max_magnitude(amax, __shfl_xor(amax, m, kWave));
     if (tid % 64 == 0) part[tid / 64] = amax;
     __syncthreads();
-    amax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    amax = max_magnitude(max_magnitude(part[0], part[1]), max_magnitude(part[2], part[3]));
     const float s = i8_scale(amax), inv = 1.0f / s;
     if (tid == 0) scale[row] = s;
 #pragma unroll

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormProblem
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 n[v][e] = n[v][e] * q * xw[v][e];
-                if (P.x_scale) amax[0] = fmaxf(amax[0], fabsf(n[v][e]));
+                if (P.x_scale) amax[0] = max_magnitude(amax[0], fabsf(n[v][e]));
             }
             if (!P.x_scale && live && col(v) < H) store<RAGGED>(P.x_out, P.x_f32, at0 + col(v), n[v], H - col(v));
         }

@@ -129,9 +129,9 @@ __device__ __forceinline__ void weights(const void* p, int f32, size_t at, int n
 }
 
 template <bool MAX>
-__device__ __forceinline__ float join(float a, float b) { return MAX ? fmaxf(a, b) : a + b; }
+__device__ __forceinline__ float join(float a, float b) { return MAX ? max_magnitude(a, b) : a + b; }
 
-// Sum (maximum) over the 16 lanes of a DPP row, in all of them.
+// Sum (largest magnitude) over the 16 lanes of a DPP row, in all of them.
 template <bool MAX>
 __device__ __forceinline__ float row16(float v) {
     auto other = [](float x, auto ctrl) {
@@ -143,7 +143,7 @@ __device__ __forceinline__ float row16(float v) {
     return join<MAX>(v, other(v, std::integral_constant<int, 0x140>{}));   // mirrored in 16
 }
 
-// Sums (or maxima) over the TPR threads of a row, the same value in all of
+// Sums (or largest magnitudes) over the TPR threads of a row, the same value in all of
 // them: 16 lanes by DPP, the rest through LDS (slot: 2 sets of 2 values for
 // every 16 threads of the workgroup, used in turn so that one barrier a call is
 // enough).

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import routed_expert_ffn_04_amd as moe
-from test_gpu_dense import BF, F32, HALF, norm_case, norm_grad_ref, norm_ref, within
+from test_gpu_dense import BF, F32, HALF, I8, norm_case, norm_grad_ref, norm_ref, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,42 @@ def test_norm_with_another_eps(T, H, eps):
         assert {k for k, v in got.items() if v is not None} == set(ref)
         for k, (v, e) in ref.items():
             within(got[k], v, e + HALF[got[k].dtype] * (v.abs() + e), f"{k} gate_div={gate_div}")
+
+
+# ---------------------------------------------------------------- int8
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [16, 2064, 9008, 20000])
+def test_a_nan_keeps_its_row_through_int8(cols, dtype):
+    """One NaN (of either sign, anywhere in the row): the row's scale is NaN, and so is its row
+    of the product; an infinity makes the scale infinite.  Other rows are as without them."""
+    g = torch.Generator().manual_seed(cols)
+    x = rand(g, (7, cols), 1.0, dtype)
+    w = torch.randint(-127, 128, (24, cols), generator=g).to(I8).cuda()
+    ws = torch.rand(24, generator=g).cuda()
+    q0, s0 = moe.quant_i8(x)
+    good = moe.linear_i8(q0, s0, w, ws, out_dtype=F32)
+    bad = x.clone()
+    nan = torch.tensor(float("nan"), dtype=dtype, device="cuda")
+    bad[1, 0], bad[2, cols - 1], bad[4, cols // 2], bad[5] = nan, torch.copysign(nan, -torch.ones_like(nan)), nan, nan
+    bad[4, 1], bad[6, 3] = float("inf"), -float("inf")
+    q, s = moe.quant_i8(bad)
+    y = moe.linear_i8(q, s, w, ws, out_dtype=F32)
+    for t in (1, 2, 4, 5):
+        assert bool(torch.isnan(s[t])) and bool(torch.isnan(y[t]).all()), t
+    assert bool(torch.isinf(s[6]))
+    for t in (0, 3):
+        assert torch.equal(q[t], q0[t]) and torch.equal(s[t], s0[t]) and torch.equal(y[t], good[t])
+
+
+@pytest.mark.parametrize("H", [264, 1001, 2560, 7168, 16384])
+def test_a_nan_keeps_its_row_through_the_norm_to_int8(H):
+    c = norm_case(9, H, 23, gate_div=3)
+    kw = dict(post_w=c["post_w"], gate=c["gate"], gate_div=3, pre_w=c["pre_w"], x_dtype=I8)
+    _, (q0, s0) = moe.norm(c["y"], c["res"], **kw)
+    y, res = c["y"].clone(), c["res"].clone()
+    y[4, H // 2], res[7, H - 1] = float("nan"), float("nan")
+    _, (q, s) = moe.norm(y, res, **kw)
+    assert torch.isnan(s).nonzero().flatten().tolist() == [4, 7]
+    keep = [0, 1, 2, 3, 5, 6, 8]
+    assert torch.equal(q[keep], q0[keep]) and torch.equal(s[keep], s0[keep])
