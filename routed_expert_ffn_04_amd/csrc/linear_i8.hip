@@ -21,8 +21,8 @@ __global__ __launch_bounds__(256) void quant_i8_kernel(const void* __restrict__ 
     const size_t row = first + blockIdx.x;
     const int tid = threadIdx.x;
     __shared__ float part[4];
-    constexpr int kWide = 2048 * NV;   // columns held
-    auto load = [&](int c, float(&v)[8]) __attribute__((always_inline)) {
+    constexpr int kWide = 2048 * NV;   // columns held; the steps past the last column of 2^31 - 16 leave an int's range
+    auto load = [&](uint32_t c, float(&v)[8]) __attribute__((always_inline)) {
         if (F32) {
             const float4* p = (const float4*)((const float*)x + row * cols + c);
             const float4 a = p[0], b = p[1];
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void quant_i8_kernel(const void* __restrict__ 
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = max_magnitude(amax, fabsf(held[i][e]));
-    for (int c = kWide + tid * 8; c < cols; c += 2048) {
+    for (uint32_t c = kWide + tid * 8; c < (uint32_t)cols; c += 2048) {
         float v[8];
         load(c, v);
 #pragma unroll
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void quant_i8_kernel(const void* __restrict__ 
         const int c = (i * 256 + tid) * 8;
         if (c < cols) *(uint2*)(q + row * cols + c) = i8_codes8(held[i], s, inv);
     }
-    for (int c = kWide + tid * 8; c < cols; c += 2048) {
+    for (uint32_t c = kWide + tid * 8; c < (uint32_t)cols; c += 2048) {
         float v[8];
         load(c, v);
         *(uint2*)(q + row * cols + c) = i8_codes8(v, s, inv);

@@ -74,3 +74,21 @@ def test_a_nan_keeps_its_row_through_the_norm_to_int8(H):
     assert torch.isnan(s).nonzero().flatten().tolist() == [4, 7]
     keep = [0, 1, 2, 3, 5, 6, 8]
     assert torch.equal(q[keep], q0[keep]) and torch.equal(s[keep], s0[keep])
+
+
+def test_quant_i8_of_the_longest_row():
+    """2^31 - 16 columns, the most that the boundary takes: the steps of a thread pass 2^31."""
+    cols = (1 << 31) - 16
+    x = torch.empty(1, cols, dtype=BF, device="cuda")
+    step = 1 << 28
+    value = lambda at: (torch.arange(at, min(at + step, cols), device="cuda") % 251 - 125).to(BF)
+    for at in range(0, cols, step):
+        x[0, at:at + step] = value(at)
+    x[0, cols - 1] = 127
+    q, s = moe.quant_i8(x)
+    assert s.tolist() == [1.0]
+    for at in range(0, cols, step):
+        want = value(at).to(I8)
+        if at + step >= cols:
+            want[-1] = 127
+        assert torch.equal(q[0, at:at + step], want), at
