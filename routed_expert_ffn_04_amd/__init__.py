@@ -435,6 +435,9 @@ def _empty(like, shape, dtype):
     return like.new_empty(shape, dtype=dtype)
 
 
+_MOST = 2 ** 31 - 1   # sizes cross the boundary as int32; ctypes would pass a larger one's low bits
+
+
 def _matrix(name, t):
     """(rows, columns, device index) of a 2-d device tensor."""
     if torch is None:
@@ -442,7 +445,10 @@ def _matrix(name, t):
     shape, device = t.shape, t.get_device()
     if len(shape) != 2 or device < 0:
         raise ValueError(f"{name}: expected a 2-d tensor on a GPU, got {tuple(shape)} on {t.device}")
-    return shape[0], shape[1], device
+    rows, columns = shape
+    if rows > _MOST or columns > _MOST:
+        raise ValueError(f"{name}: {tuple(shape)} has a size above {_MOST}")
+    return rows, columns, device
 
 
 def _scratch(ws, need, like):
@@ -464,6 +470,8 @@ def _dense_bank(bank: Experts, H: int, device):
     if wg.dim() != 3 or bank.dt not in (None, BF16):
         raise ValueError("bank: bf16 weights [1][I][H] and [1][H][I]")
     I = wg.shape[1]
+    if I > _MOST:
+        raise ValueError(f"bank: I={I} is above {_MOST}")
     _tensor(device, "w_gate", wg, (1, I, H), bf)
     _tensor(device, "w_up", wu, (1, I, H), bf)
     _tensor(device, "w_down", wd, (1, H, I), bf)
@@ -523,7 +531,8 @@ def ffn_backward(dy, x, bank: Experts, gu=None, *, need=("dx", "dw_gate", "dw_up
 
 
 def _norm_params(T, H, dev, post_w, gate, gate_div, pre_w):
-    """(rows of the gate, weight dtype code) after the checks."""
+    """(rows of the gate, gate_div, weight dtype code) after the checks.  A
+    gate_div of T or more is one gate for all tokens, whatever its size."""
     dtype = None
     for t in (post_w, gate, pre_w):
         if t is not None:
@@ -531,7 +540,7 @@ def _norm_params(T, H, dev, post_w, gate, gate_div, pre_w):
                 raise TypeError(f"post_w, gate and pre_w have different dtypes: {dtype}, {t.dtype}")
             dtype = t.dtype
     if dtype is None:
-        return 0, F32
+        return 0, 1, F32
     G = 0
     if gate is not None:
         if gate_div < 1:
@@ -540,7 +549,7 @@ def _norm_params(T, H, dev, post_w, gate, gate_div, pre_w):
         _tensor(dev, "gate", gate, (G, H), _FLOATS)
     _tensor(dev, "post_w", post_w, (H,), _FLOATS)
     _tensor(dev, "pre_w", pre_w, (H,), _FLOATS)
-    return G, _CODE[dtype]
+    return G, min(gate_div, _MOST), _CODE[dtype]
 
 
 def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: float = 1.0, pre_w=None,
@@ -556,7 +565,7 @@ def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: f
         with there:
             return norm(y, res, post_w=post_w, gate=gate, gate_div=gate_div, res_scale=res_scale, pre_w=pre_w, eps=eps,
                         r_dtype=r_dtype, x_dtype=x_dtype, want_r=want_r, want_x=want_x, r=r, x=x)
-    _, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
+    _, gate_div, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
     r_dtype = res.dtype if res is not None else r.dtype if r is not None else (r_dtype or y.dtype)
     q, scale = x if isinstance(x, tuple) else (x, None)
     x_dtype = q.dtype if q is not None else (x_dtype or y.dtype)
@@ -595,7 +604,7 @@ def norm_backward(dx, dr, y, r, *, post_w=None, gate=None, gate_div: int = 1, re
         with there:
             return norm_backward(dx, dr, y, r, post_w=post_w, gate=gate, gate_div=gate_div, res_scale=res_scale,
                                  pre_w=pre_w, eps=eps, need=need, ws=ws)
-    G, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
+    G, gate_div, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
     r_dtype = r.dtype if r is not None else dr.dtype if dr is not None else torch.float32
     y_dtype = y.dtype if y is not None else r_dtype
     _tensor(dev, "dx", dx, (T, H), _FLOATS)

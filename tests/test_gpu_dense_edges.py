@@ -92,3 +92,26 @@ def test_quant_i8_of_the_longest_row():
         if at + step >= cols:
             want[-1] = 127
         assert torch.equal(q[0, at:at + step], want), at
+
+
+# ---------------------------------------------------------------- sizes beyond an int32
+
+def test_norm_of_more_rows_than_an_int32_holds_is_refused():
+    y = torch.empty((1 << 32) + 4, 1, dtype=BF, device="cuda")
+    with pytest.raises(ValueError):
+        moe.norm(y)
+    with pytest.raises(ValueError):
+        moe.norm_backward(y, None, y, y)
+
+
+@pytest.mark.parametrize("gate_div", [9, 10, 2 ** 31, 2 ** 32 + 1, 2 ** 40])
+def test_one_gate_for_more_rows_than_there_are(gate_div):
+    """However large gate_div is: the one gate applies to every row."""
+    c = norm_case(9, 264, 25, gate_div=9)
+    kw = dict(post_w=c["post_w"], gate=c["gate"], res_scale=0.75, pre_w=c["pre_w"])
+    want = moe.norm(c["y"], c["res"], gate_div=9, **kw)
+    got = moe.norm(c["y"], c["res"], gate_div=gate_div, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    want = moe.norm_backward(c["dx"], c["dr"], c["y"], c["res"], gate_div=9, **kw)
+    got = moe.norm_backward(c["dx"], c["dr"], c["y"], c["res"], gate_div=gate_div, **kw)
+    assert all(torch.equal(got[k], want[k]) for k in want)
