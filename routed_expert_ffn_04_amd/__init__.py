@@ -428,6 +428,15 @@ def _tensor(device: int, name, t, shape, dtypes):
     raise ValueError(f"{name} is not contiguous")
 
 
+def _out_dtype(name, t, dtype, default):
+    """dtype of an output: that of t, which `dtype` may repeat but not contradict."""
+    if t is None:
+        return dtype or default
+    if dtype is not None and dtype is not t.dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, but {dtype} is asked for")
+    return t.dtype
+
+
 def _empty(like, shape, dtype):
     """An output on `like`'s device."""
     if like.dtype is dtype:
@@ -487,7 +496,7 @@ def ffn(x, bank: Experts, *, want_gu: bool = False, y_dtype=None, out=None, gu=N
         with there:
             return ffn(x, bank, want_gu=want_gu, y_dtype=y_dtype, out=out, gu=gu, ws=ws)
     st, I = _dense_bank(bank, H, dev)
-    y_dtype = out.dtype if out is not None else (y_dtype or torch.bfloat16)
+    y_dtype = _out_dtype("out", out, y_dtype, torch.bfloat16)
     if y_dtype not in _FLOATS:
         raise TypeError(f"ffn: y {y_dtype}")
     _tensor(dev, "x", x, (T, H), (torch.bfloat16,))
@@ -556,9 +565,9 @@ def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: f
          eps: float = 1e-6, r_dtype=None, x_dtype=None, want_r: bool = True, want_x: bool = True, r=None, x=None,
          stream=None):
     """The norm step between two blocks (moe_norm).  Returns (r, x); with
-    x_dtype torch.int8 x is the pair (codes [T][H], scales [T]).  r_dtype
-    defaults to res's dtype (y's without res), x_dtype to y's.  r, x: optional
-    output tensors; r may be res itself."""
+    x_dtype torch.int8 x is the pair (codes [T][H], scales [T]).  r has res's
+    dtype, without res r_dtype (default: y's); x_dtype defaults to y's.  r, x:
+    optional output tensors; r may be res itself."""
     T, H, dev = _matrix("y", y)
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -566,12 +575,14 @@ def norm(y, res=None, *, post_w=None, gate=None, gate_div: int = 1, res_scale: f
             return norm(y, res, post_w=post_w, gate=gate, gate_div=gate_div, res_scale=res_scale, pre_w=pre_w, eps=eps,
                         r_dtype=r_dtype, x_dtype=x_dtype, want_r=want_r, want_x=want_x, r=r, x=x)
     _, gate_div, w_dt = _norm_params(T, H, dev, post_w, gate, gate_div, pre_w)
-    r_dtype = res.dtype if res is not None else r.dtype if r is not None else (r_dtype or y.dtype)
+    r_dtype = _out_dtype("r", r, r_dtype, y.dtype) if res is None else _out_dtype("res", res, r_dtype, None)
     q, scale = x if isinstance(x, tuple) else (x, None)
-    x_dtype = q.dtype if q is not None else (x_dtype or y.dtype)
+    x_dtype = _out_dtype("x", q, x_dtype, y.dtype)
     if r_dtype not in _FLOATS or x_dtype not in _CODE:
         raise TypeError(f"norm: r {r_dtype}, x {x_dtype}")
     i8 = x_dtype == torch.int8
+    if scale is not None and not i8:
+        raise TypeError(f"norm: a scale for x of dtype {x_dtype}")
     _tensor(dev, "y", y, (T, H), _FLOATS)
     _tensor(dev, "res", res, (T, H), (r_dtype,))
     _tensor(dev, "r", r, (T, H), (r_dtype,))
@@ -657,7 +668,7 @@ def linear_i8(q, q_scale, w, w_scale, bias=None, *, out_dtype=None, out=None, ws
             return linear_i8(q, q_scale, w, w_scale, bias, out_dtype=out_dtype, out=out, ws=ws)
     N = _matrix("w", w)[0]
     f32, i8 = (torch.float32,), (torch.int8,)
-    out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
+    out_dtype = _out_dtype("out", out, out_dtype, torch.bfloat16)
     if out_dtype not in _FLOATS:
         raise TypeError(f"linear_i8: out {out_dtype}")
     _tensor(dev, "q", q, (T, K), i8)

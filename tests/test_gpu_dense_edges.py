@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import routed_expert_ffn_04_amd as moe
-from test_gpu_dense import BF, F32, HALF, I8, norm_case, norm_grad_ref, norm_ref, rand, within
+from test_gpu_dense import BF, F32, Ffn, HALF, I8, norm_case, norm_grad_ref, norm_ref, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,29 @@ def test_one_gate_for_more_rows_than_there_are(gate_div):
     want = moe.norm_backward(c["dx"], c["dr"], c["y"], c["res"], gate_div=9, **kw)
     got = moe.norm_backward(c["dx"], c["dr"], c["y"], c["res"], gate_div=gate_div, **kw)
     assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+# ---------------------------------------------------------------- arguments that contradict each other
+
+def test_dtypes_that_contradict_a_tensor_are_refused():
+    """An output's dtype is the given tensor's; another one asked for beside it is an error."""
+    f, c = Ffn(4, 64, 32), norm_case(4, 64, 26)
+    new = lambda dtype, *shape: torch.empty(shape or (4, 64), dtype=dtype, device="cuda")
+    q, w, one = new(I8), new(I8, 8, 64), new(F32, 4)
+    for call in (lambda: moe.norm(c["y"], c["res"], r_dtype=F32),                     # r is kept like res
+                 lambda: moe.norm(c["y"], r=new(BF), r_dtype=F32),
+                 lambda: moe.norm(c["y"], c["res"], r=new(F32)),
+                 lambda: moe.norm(c["y"], c["res"], x=new(BF), x_dtype=F32),
+                 lambda: moe.norm(c["y"], c["res"], x=(q, one), x_dtype=BF),
+                 lambda: moe.norm(c["y"], c["res"], x=(new(BF), one)),                # scales go with int8 codes
+                 lambda: moe.norm(c["y"], c["res"], x=(None, one)),
+                 lambda: moe.ffn(f.x, f.bank, out=new(BF), y_dtype=F32),
+                 lambda: moe.linear_i8(q, one, w, new(F32, 8), out=new(F32, 4, 8), out_dtype=BF)):
+        with pytest.raises(TypeError):
+            call()
+    # the same dtype again is no contradiction
+    assert moe.norm(c["y"], c["res"], r_dtype=BF, x=new(F32), x_dtype=F32)[0].dtype is BF
+    assert moe.norm(c["y"], r_dtype=F32)[0].dtype is F32
+    assert moe.norm(c["y"], c["res"], x=(q, one), x_dtype=I8)[1][0] is q
+    assert moe.norm(c["y"], c["res"], x=(None, one), x_dtype=I8)[1][1] is one
+    assert moe.ffn(f.x, f.bank, out=new(F32), y_dtype=F32).dtype is F32
