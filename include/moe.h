@@ -290,10 +290,11 @@ moe_status_t moe_layer_noalloc(const void* x, int32_t x_dt, int32_t T, int32_t H
  * products; all sums are fp32.  gu: optional (NULL to skip) fp32 [T][2 I], row
  * t holding g[t][0..I) then u[t][0..I): what the backward pass needs of the
  * forward pass.  All tensors 16-byte aligned, T at most 2^30; no output may
- * overlap an input or another output. */
+ * overlap an input or another output.  Sizes for which a product has 2^23 or
+ * more tiles of 256 x 256 outputs (MOE_ERR_UNSUPPORTED) exceed a GPU's memory. */
 moe_status_t moe_ffn(const void* x, int32_t x_dt, int32_t T, const moe_experts_t* bank, void* y, int32_t y_dt,
                      float* gu, void* ws, size_t ws_bytes, void* stream);
-/* 0 for invalid sizes and for T = 0. */
+/* 0 for sizes that moe_ffn refuses and for T = 0. */
 size_t moe_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
 
 /* Gradients of moe_ffn for the output gradient dy [T][H], with
@@ -362,7 +363,7 @@ moe_status_t moe_quant_i8(const void* x, int32_t x_dt, int32_t rows, int32_t col
  * x); w: [N][K] int8 with one scale per output channel w_scale [N]; bias: fp32
  * [N] or NULL; out: [T][N] MOE_F32 or MOE_BF16.  The sum is exact (int32); it
  * is rounded to fp32 once, then scaled.  K % 16 == 0, K <= 131071; T and N up
- * to 2^30. */
+ * to 2^30, fewer than 2^23 tiles of 256 x 256 outputs. */
 moe_status_t moe_linear_i8(const int8_t* q, const float* q_scale, int32_t T, int32_t K, const int8_t* w,
                            const float* w_scale, const float* bias, int32_t N, void* out, int32_t out_dt, void* ws,
                            size_t ws_bytes, void* stream);

@@ -9,6 +9,9 @@
 
 namespace moe {
 
+// What the workspace sizes below return for a product that no kernel's grid holds.
+constexpr size_t kUnfit = ~(size_t)0;
+
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct FfnProblem {

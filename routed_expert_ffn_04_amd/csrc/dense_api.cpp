@@ -50,6 +50,8 @@ bool dense_sizes(int T, int H, int I) {
     return T >= 0 && T <= kMaxRows && H > 0 && I > 0 && H % 8 == 0 && I % 8 == 0 && H <= kMaxFfn && I <= kMaxFfn;
 }
 
+size_t or_zero(size_t bytes) { return bytes == moe::kUnfit ? 0 : bytes; }
+
 constexpr int kMaxNormH = 16384;
 constexpr int kMaxI8K = 131071;   // 128 * 128 * K stays below 2^31
 
@@ -72,7 +74,7 @@ extern "C" {
 // ------------------------------------------------------------------ dense FFN
 size_t moe_ffn_workspace_size(int32_t T, int32_t H, int32_t I) {
     if (!dense_sizes(T, H, I)) return 0;
-    return moe::ffn_ws_bytes(T, H, I);
+    return or_zero(moe::ffn_ws_bytes(T, H, I));
 }
 
 moe_status_t moe_ffn(const void* x, int32_t x_dt, int32_t T, const moe_experts_t* bank, void* y, int32_t y_dt,
@@ -87,7 +89,9 @@ moe_status_t moe_ffn(const void* x, int32_t x_dt, int32_t T, const moe_experts_t
     if (!x || !y) return fail(MOE_ERR_INVALID, "%s", "ffn: null x or y");
     if (!aligned(x, 16) || !aligned(y, 16) || !aligned(gu, 16))
         return fail(MOE_ERR_INVALID, "%s", "ffn: x, y and gu must be 16-byte aligned");
-    if (!ws || !aligned(ws, 256) || ws_bytes < moe::ffn_ws_bytes(T, bank->H, bank->I))
+    const size_t need = moe::ffn_ws_bytes(T, bank->H, bank->I);
+    if (need == moe::kUnfit) return fail(MOE_ERR_UNSUPPORTED, "ffn: T=%d H=%d I=%d", T, bank->H, bank->I);
+    if (!ws || !aligned(ws, 256) || ws_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "%s", "ffn: workspace");
     moe::FfnProblem p{};
     p.x = x; p.wg = bank->w_gate; p.wu = bank->w_up; p.wd = bank->w_down;
@@ -98,7 +102,7 @@ moe_status_t moe_ffn(const void* x, int32_t x_dt, int32_t T, const moe_experts_t
 
 size_t moe_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I, int32_t has_gu) {
     if (!dense_sizes(T, H, I)) return 0;
-    return moe::ffn_backward_ws_bytes(T, H, I, has_gu);
+    return or_zero(moe::ffn_backward_ws_bytes(T, H, I, has_gu));
 }
 
 moe_status_t moe_ffn_backward(const void* dy, const void* x, int32_t dt, int32_t T, const moe_experts_t* bank,
@@ -115,7 +119,9 @@ moe_status_t moe_ffn_backward(const void* dy, const void* x, int32_t dt, int32_t
     if (!dx && !dw_gate && !dw_up && !dw_down) return MOE_OK;
     if (T > 0) {
         if (!dy || !x) return fail(MOE_ERR_INVALID, "%s", "ffn_backward: null dy or x");
-        if (!ws || !aligned(ws, 256) || ws_bytes < moe::ffn_backward_ws_bytes(T, bank->H, bank->I, gu != nullptr))
+        const size_t need = moe::ffn_backward_ws_bytes(T, bank->H, bank->I, gu != nullptr);
+        if (need == moe::kUnfit) return fail(MOE_ERR_UNSUPPORTED, "ffn_backward: T=%d H=%d I=%d", T, bank->H, bank->I);
+        if (!ws || !aligned(ws, 256) || ws_bytes < need)
             return fail(MOE_ERR_WORKSPACE, "%s", "ffn_backward: workspace");
     }
     moe::FfnProblem p{};
@@ -202,7 +208,7 @@ moe_status_t moe_quant_i8(const void* x, int32_t x_dt, int32_t rows, int32_t col
 
 size_t moe_linear_i8_workspace_size(int32_t T, int32_t K, int32_t N) {
     if (T < 0 || K <= 0 || N <= 0 || K % 16 || K > kMaxI8K || T > kMaxRows || N > kMaxRows) return 0;
-    return moe::linear_i8_ws_bytes(T, K, N);
+    return or_zero(moe::linear_i8_ws_bytes(T, K, N));
 }
 
 moe_status_t moe_linear_i8(const int8_t* q, const float* q_scale, int32_t T, int32_t K, const int8_t* w,
@@ -219,6 +225,7 @@ moe_status_t moe_linear_i8(const int8_t* q, const float* q_scale, int32_t T, int
         !aligned(out, size_of(out_dt)))
         return fail(MOE_ERR_INVALID, "%s", "linear_i8: misaligned tensor");
     const size_t need = moe::linear_i8_ws_bytes(T, K, N);
+    if (need == moe::kUnfit) return fail(MOE_ERR_UNSUPPORTED, "linear_i8: T=%d K=%d N=%d", T, K, N);
     if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return fail(MOE_ERR_WORKSPACE, "%s", "linear_i8: workspace");
     moe::LinearI8Problem p{};
     p.q = q; p.xs = q_scale; p.w = w; p.ws = w_scale; p.bias = bias; p.T = T; p.K = K; p.N = N;

@@ -54,6 +54,7 @@ Forward forward(int T, int H, int I) {
     f.h = 0;
     f.part = align256((size_t)T * I * 2);
     f.total = f.part + max2(part_bytes(f.gateup, T, 2L * I), part_bytes(f.down, T, H));
+    if (!fits(f.gateup) || !fits(f.down)) f.total = kUnfit;
     return f;
 }
 
@@ -85,6 +86,8 @@ Backward backward(int T, int H, int I, bool has_gu) {
     most = max2(most, part_bytes(w.dwd, H, I));
     if (!has_gu) most = max2(most, part_bytes(w.gateup, T, 2L * I));
     w.total = o + most;
+    if ((!has_gu && !fits(w.gateup)) || !fits(w.dh) || !fits(w.dx) || !fits(w.dwgu) || !fits(w.dw1) || !fits(w.dwd))
+        w.total = kUnfit;
     return w;
 }
 
@@ -158,13 +161,15 @@ hipError_t launch_products(Product* todo, int n, float* part, hipStream_t s) {
         if (edge == 256) t = {1.7, 4.6, 0.41, 1.25};
         else if (edge == 128) t = {0.48, 0.8, 0.39, 0.6};
         else t = {0.2, 0, 0.44, 0.19};
-        double work = 0, longest = 0;
+        double work = 0, longest = 0, all = 0;
         for (int i = 0; i < n; ++i) {
             const Args& G = todo[i].G;
             const double tiles = (double)((G.M + edge - 1) / edge) * ((G.N + edge - 1) / edge), span = (G.K + kKE - 1) / kKE;
+            all += tiles;
             work += tiles * (span * t.stage + t.tile) / 256;
             longest = std::max(longest, span);
         }
+        if (!grid_fits((long)all, tile_threads(edge))) continue;
         const double us = std::max(longest * t.alone + 5, work + longest * t.end) + 2;
         if (us < apart) {
             apart = us;
@@ -181,11 +186,14 @@ hipError_t launch_products(Product* todo, int n, float* part, hipStream_t s) {
     return e;
 }
 
-// rows of zeros (the weight gradients of no tokens)
+// A matrix of zeros (the weight gradients of no tokens): M and N are multiples of 8.
+__global__ __launch_bounds__(256) void zero_kernel(uint4* out, size_t n) {
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) out[i] = uint4{0, 0, 0, 0};
+}
 hipError_t zero_rows(void* out, int M, int N, hipStream_t s) {
-    Args G = base(M, N, 0);
-    G.out = out;
-    return launch_reduce<kEpiOut>(G, nullptr, 0, s);
+    const size_t n = (size_t)M * N / 8;
+    zero_kernel<<<dim3((unsigned)std::min((n + 255) / 256, (size_t)4096)), dim3(256), 0, s>>>((uint4*)out, n);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -17,6 +17,7 @@
 // take 5.0.
 #pragma once
 #include "gemm_tile.h"
+#include "tile_plan.h"
 
 namespace moe {
 namespace gemm {
@@ -124,17 +125,12 @@ __global__ __launch_bounds__(WAVES * 64) void few_kernel(Args G) {
     }
 }
 
-// Beyond 16 rows the 64-row tiles take over.  At 16, weights from HBM: FFN of 1024 x
-// 512 7.6 us here and 9.7 in tiles, 4096 x 1024 14.1 and 17.3, 7168 x 2048 29.5 and
-// 27.6; two blocks of 16 rows here do not reach the tiles' 33 rows.
-constexpr int kFewRows = 16;
-
 template <int E, int EPI>
 hipError_t launch_few(const Args& G, hipStream_t s) {
     constexpr int cols = EPI == kEpiGateUp ? 8 : 16;
     const long blocks = ((long)G.N + cols - 1) / cols;
-    if (!grid_fits(blocks, 512)) return hipErrorInvalidValue;
-    few_kernel<E, EPI, 8><<<dim3((unsigned)blocks), dim3(512), 0, s>>>(G);
+    if (!grid_fits(blocks, kFewThreads)) return hipErrorInvalidValue;
+    few_kernel<E, EPI, kFewThreads / 64><<<dim3((unsigned)blocks), dim3(kFewThreads), 0, s>>>(G);
     return hipGetLastError();
 }
 

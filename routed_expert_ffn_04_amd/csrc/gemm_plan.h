@@ -1,74 +1,20 @@
-// Tile size and k-splits of a product, and the kernel that sums the splits.
+// A product by its plan: the launch of its tiles, and the kernel that sums the k-splits.
 #pragma once
 #include <algorithm>
 
 #include "dense.h"
 #include "gemm_few.h"
 #include "gemm_tile.h"
+#include "tile_plan.h"
 
 namespace moe {
 namespace gemm {
-
-struct Plan {
-    int few;             // the kernel for a few rows
-    int edge;            // 256 x 256, 128 x 128 or 64 x 64 tiles
-    int splits, kspan;
-    int workgroups;
-    double us;           // estimated time
-};
-
-// Estimated time of wg workgroups of `span` stages each, in us, fitted to
-// sweeps of every edge and number of splits.  64-row tiles share a CU's loads
-// (up to four at once, 0.21 us a stage each); 128-row tiles run two to a CU, where
-// a stage of each takes 0.95 us, against 0.5 with half of the CUs taken; a 256-row
-// tile's stage takes 1.1 us alone and 1.6 when the whole chip draws power.
-inline double tiling_us(int edge, long wg, int span) {
-    auto rounds = [&](long at_once) { return (double)((wg + at_once - 1) / at_once); };
-    if (edge == 256) {
-        const double full = std::min(1.0, wg / 256.0);
-        return rounds(256) * (span * (1.1 + 0.5 * full * full) + 10);
-    }
-    if (edge == 128) return wg <= 512 ? span * (0.35 + 0.6 * wg / 512.0) + 5 : rounds(512) * (span * 0.95 + 4) + 1;
-    return rounds(256) * (span * 0.21 + 0.25) + 3;
-}
-
-// The tiling with the least estimated time.
-// mma_cols: MFMA columns of the product (gate/up: both matrices' columns).
-// rows: both operands have k contiguous.
-inline Plan plan_tiles(long M, long mma_cols, int K, int stage_elems, bool rows) {
-    Plan best{};
-    const int stages = (K + stage_elems - 1) / stage_elems;
-    if (rows && M <= kFewRows) {
-        best.few = best.splits = 1;
-        best.kspan = stages * stage_elems;
-        return best;
-    }
-    double least = 0;
-    for (int edge = 64; edge <= 256; edge *= 2) {
-        const long tiles = ((M + edge - 1) / edge) * ((mma_cols + edge - 1) / edge);
-        for (int s = 1; s <= 16 && (s == 1 || (stages / s >= 2 && tiles * s <= 512)); ++s) {
-            const int span = (stages + s - 1) / s, n = (stages + span - 1) / span;
-            const long wg = tiles * n;
-            double us = tiling_us(edge, wg, span);
-            if (n > 1) us += 4 + (double)n * M * mma_cols * 8 / 4e6;
-            if (least == 0 || us < least) {
-                least = best.us = us;
-                best.edge = edge;
-                best.splits = n;
-                best.kspan = span * stage_elems;
-                best.workgroups = (int)(wg < 0x7fffffff ? wg : 0x7fffffff);
-            }
-        }
-    }
-    return best;
-}
 
 // bytes of the partial sums
 inline size_t part_bytes(const Plan& p, long M, long cols) { return p.splits > 1 ? align256((size_t)p.splits * M * cols * 4) : 0; }
 
 // Sums the k-splits in their order and applies the product's epilogue.  A
-// thread takes eight consecutive columns of one row.  splits = 0: the
-// outputs of an empty sum.
+// thread takes eight consecutive columns of one row.
 template <int EPI>
 __global__ __launch_bounds__(256) void reduce_kernel(Args G, const float* __restrict__ part, int splits) {
     const int groups = (G.N + 7) / 8;

@@ -40,6 +40,7 @@
 #pragma once
 #include "common.h"
 #include "gffn_common.h"
+#include "tile_plan.h"
 
 namespace moe {
 namespace gemm {
@@ -61,7 +62,6 @@ enum Epi {
     kEpiI8 = 4,        // acc * x_scale[m] * w_scale[n] + bias[n], bf16 or fp32
 };
 
-constexpr int kStage = 128;  // bytes of k per stage
 constexpr uint32_t kFar = 1u << 31;   // past every byte of a tile: 256 rows of at most 2^23 bytes
 
 struct Operand {
@@ -222,11 +222,7 @@ __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& t
     tm = band * 8 + t % rows;
 }
 
-// A grid holds fewer than 2^32 threads.
-inline bool grid_fits(long blocks, int threads) { return blocks > 0 && blocks <= 0xffffffffL / threads; }
-
-// Launch shape of the tiles: threads, and workgroups per CU (by LDS).
-constexpr int tile_threads(int edge) { return edge == 256 ? 512 : 256; }
+// Launch shape of the tiles: LDS, and waves per SIMD by it.
 constexpr int tile_lds(int edge, int ring) { return ring * edge * kStage; }
 constexpr int tile_waves(int edge, int ring) { return edge == 256 ? 2 : 163840 / tile_lds(edge, ring); }   // per SIMD
 

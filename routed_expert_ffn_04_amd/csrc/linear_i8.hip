@@ -98,7 +98,9 @@ hipError_t launch_quant_i8(const void* x, int x_f32, int rows, int cols, int8_t*
 }
 
 size_t linear_i8_ws_bytes(int T, int K, int N) {
-    return T > 0 ? part_bytes(plan_tiles(T, N, K, kStage, true), T, N) : 0;
+    if (T == 0) return 0;
+    const Plan p = plan_tiles(T, N, K, kStage, true);
+    return fits(p) ? part_bytes(p, T, N) : kUnfit;
 }
 
 hipError_t launch_linear_i8(const LinearI8Problem& p, void* ws, hipStream_t s) {

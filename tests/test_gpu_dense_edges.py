@@ -141,3 +141,29 @@ def test_dtypes_that_contradict_a_tensor_are_refused():
     assert moe.norm(c["y"], c["res"], x=(q, one), x_dtype=I8)[1][0] is q
     assert moe.norm(c["y"], c["res"], x=(None, one), x_dtype=I8)[1][1] is one
     assert moe.ffn(f.x, f.bank, out=new(F32), y_dtype=F32).dtype is F32
+
+
+# ---------------------------------------------------------------- grids
+
+def test_linear_i8_of_more_columns_than_the_few_row_grid_holds():
+    """One token and 2^27 + 16 output channels: beyond the grid of the kernel for a few rows."""
+    N, K = (1 << 27) + 16, 16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.randint(-127, 128, (N, K), generator=gen, dtype=I8, device="cuda")
+    ws = torch.rand(N, generator=gen, device="cuda")
+    q = torch.randint(-127, 128, (1, K), generator=gen, dtype=I8, device="cuda")
+    qs = torch.tensor([0.37], device="cuda")
+    out = moe.linear_i8(q, qs, w, ws, out_dtype=F32)
+    step = 1 << 24
+    for at in range(0, N, step):
+        total = (w[at:at + step].int() * q.int()).sum(1)       # exact, and so is its conversion: below 2^24
+        assert torch.equal(out[0, at:at + step], total.float() * (qs * ws[at:at + step])), at
+
+
+def test_gradients_of_no_tokens_are_zero_in_large_matrices():
+    H, I = 4096, 4104
+    bank = moe.Experts(*(torch.zeros(s, dtype=BF, device="cuda") for s in ((1, I, H), (1, I, H), (1, H, I))))
+    none = torch.empty(0, H, dtype=BF, device="cuda")
+    torch.full((3 * H * I,), float("nan"), dtype=BF, device="cuda")      # what the outputs' memory may hold
+    for g in moe.ffn_backward(none, none, bank)[1:]:
+        assert bool((g == 0).all())
