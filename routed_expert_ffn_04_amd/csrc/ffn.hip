@@ -151,31 +151,12 @@ hipError_t launch_products(Product* todo, int n, float* part, hipStream_t s) {
     for (int i = 1; i < n; ++i)
         for (int j = i; j > 0 && todo[j].G.K > todo[j - 1].G.K; --j) std::swap(todo[j], todo[j - 1]);
     double apart = 0;
-    for (int i = 0; i < n; ++i) apart += todo[i].plan.us + 2;
-    // together, fitted to 36 shapes like the times in gemm_plan.h: the work of a CU
-    // (a stage, a tile's beginning and end) and the uneven end in units of the longest
-    // tile, at least that tile alone; off by 6 to 11 % (256- to 64-row tiles)
-    struct { double stage, tile, end, alone; } t;
-    int best = 0;
-    for (int edge = 64; n > 1 && edge <= 256; edge *= 2) {
-        if (edge == 256) t = {1.7, 4.6, 0.41, 1.25};
-        else if (edge == 128) t = {0.48, 0.8, 0.39, 0.6};
-        else t = {0.2, 0, 0.44, 0.19};
-        double work = 0, longest = 0, all = 0;
-        for (int i = 0; i < n; ++i) {
-            const Args& G = todo[i].G;
-            const double tiles = (double)((G.M + edge - 1) / edge) * ((G.N + edge - 1) / edge), span = (G.K + kKE - 1) / kKE;
-            all += tiles;
-            work += tiles * (span * t.stage + t.tile) / 256;
-            longest = std::max(longest, span);
-        }
-        if (!grid_fits((long)all, tile_threads(edge))) continue;
-        const double us = std::max(longest * t.alone + 5, work + longest * t.end) + 2;
-        if (us < apart) {
-            apart = us;
-            best = edge;
-        }
+    Size sizes[3];
+    for (int i = 0; i < n; ++i) {
+        apart += todo[i].plan.us + 2;
+        sizes[i] = {todo[i].G.M, todo[i].G.N, todo[i].G.K};
     }
+    const int best = plan_together(sizes, n, kKE, apart);
     if (best == 256) return launch_together<256>(todo, n, s);
     if (best == 128) return launch_together<128>(todo, n, s);
     if (best == 64) return launch_together<64>(todo, n, s);

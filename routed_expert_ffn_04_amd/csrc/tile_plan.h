@@ -74,6 +74,38 @@ inline Plan plan_tiles(long M, long mma_cols, int K, int stage_elems, bool rows)
     return best;
 }
 
+// Tile edge of n products that go out as one launch, or 0 where `apart` (us, one
+// after the other) is less.  Fitted to 36 shapes like the times above: the work of a
+// CU (a stage, a tile's beginning and end) and the uneven end in units of the
+// longest tile, at least that tile alone; off by 6 to 11 % (256- to 64-row tiles).
+struct Size {
+    int M, N, K;
+};
+inline int plan_together(const Size* p, int n, int stage_elems, double apart) {
+    struct { double stage, tile, end, alone; } t;
+    int best = 0;
+    for (int edge = 64; n > 1 && edge <= 256; edge *= 2) {
+        if (edge == 256) t = {1.7, 4.6, 0.41, 1.25};
+        else if (edge == 128) t = {0.48, 0.8, 0.39, 0.6};
+        else t = {0.2, 0, 0.44, 0.19};
+        double work = 0, longest = 0, all = 0;
+        for (int i = 0; i < n; ++i) {
+            const double tiles = (double)((p[i].M + edge - 1) / edge) * ((p[i].N + edge - 1) / edge);
+            const double span = (p[i].K + stage_elems - 1) / stage_elems;
+            all += tiles;
+            work += tiles * (span * t.stage + t.tile) / 256;
+            longest = std::max(longest, span);
+        }
+        if (!grid_fits((long)all, tile_threads(edge))) continue;
+        const double us = std::max(longest * t.alone + 5, work + longest * t.end) + 2;
+        if (us < apart) {
+            apart = us;
+            best = edge;
+        }
+    }
+    return best;
+}
+
 inline bool fits(const Plan& p) { return p.few || p.edge; }
 
 }  // namespace gemm

@@ -6,6 +6,7 @@ import subprocess
 import pytest
 
 import routed_expert_ffn_04_amd as moe
+from dense_plan_cases import FFN, I8
 
 
 class Shape:
@@ -66,16 +67,27 @@ extern "C" int plan_tiles(long M, long cols, int K, int stage, int rows, int* ou
     out[0] = p.few; out[1] = p.edge; out[2] = p.splits; out[3] = p.kspan; out[4] = p.workgroups;
     return moe::gemm::fits(p);
 }
+extern "C" int plan_together(const int* sizes, int n, int stage) {   // of products with operands by columns
+    double apart = 0;
+    moe::gemm::Size s[3];
+    for (int i = 0; i < n; ++i) {
+        s[i] = {sizes[3 * i], sizes[3 * i + 1], sizes[3 * i + 2]};
+        apart += moe::gemm::plan_tiles(s[i].M, s[i].N, s[i].K, stage, false).us + 2;
+    }
+    return moe::gemm::plan_together(s, n, stage, apart);
+}
 ''')
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, str(d / "plan.cpp"), "-o", str(d / "plan.so")],
                    check=True)
-    f = ctypes.CDLL(str(d / "plan.so")).plan_tiles
+    L = ctypes.CDLL(str(d / "plan.so"))
+    f = L.plan_tiles
     f.argtypes = [ctypes.c_long, ctypes.c_long, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
 
     def call(M, cols, K, stage, rows):
         out = (ctypes.c_int * 5)()
         ok = f(M, cols, K, stage, rows, out)
         return dict(zip(("few", "edge", "splits", "kspan", "workgroups"), out), fits=bool(ok))
+    call.together = lambda sizes: L.plan_together((ctypes.c_int * 9)(*(v for s in sizes for v in s)), len(sizes), 64)
     return call
 
 
@@ -93,3 +105,23 @@ def test_plans_take_kernels_whose_grid_holds_the_product(plan, T, K, N):
         tiles = -(-T // p["edge"]) * -(-N // p["edge"])
         assert p["workgroups"] == tiles * p["splits"]
         assert p["workgroups"] * (512 if p["edge"] == 256 else 256) < 2 ** 32
+
+
+@pytest.mark.parametrize("product,tiling,sizes", FFN + I8)
+def test_the_sizes_tested_on_a_gpu_reach_their_tilings(plan, product, tiling, sizes):
+    """As launch_tiling and launch_products choose."""
+    if product == "i8":
+        p = plan(sizes[0], sizes[2], sizes[1], 128, 1)
+    else:
+        T, H, I = sizes
+        K = -(-I // 64) * 64 + I                # of dx: du's half begins on a stage
+        if product == "grads":
+            edge = plan.together([(T, H, K), (2 * I, H, T), (H, I, T)])
+            assert (f"joint{edge}" if edge else "apart") == tiling
+            return
+        M, cols, k, rows = {"gateup": (T, 2 * I, H, 1), "down": (T, H, I, 1), "dh": (T, I, H, 0), "dx": (T, H, K, 0),
+                            "dwgu": (2 * I, H, T, 0), "dw1": (I, H, T, 0), "dwd": (H, I, T, 0)}[product]
+        p = plan(M, cols, k, 64, rows)
+    assert not p["few"]
+    deep = p["edge"] < 256 and p["workgroups"] <= (512 if p["edge"] == 64 else 256)
+    assert f"{p['edge']}r{10 if deep else 5}{'/k' if p['splits'] > 1 else ''}" == tiling

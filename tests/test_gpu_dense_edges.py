@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import routed_expert_ffn_04_amd as moe
-from test_gpu_dense import BF, F32, Ffn, HALF, I8, norm_case, norm_grad_ref, norm_ref, rand, within
+from dense_plan_cases import FFN as FFN_TILINGS, I8 as I8_TILINGS
+from test_gpu_dense import BF, F32, Ffn, HALF, I8, norm_case, norm_grad_ref, norm_ref, outbuf, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +168,52 @@ def test_gradients_of_no_tokens_are_zero_in_large_matrices():
     torch.full((3 * H * I,), float("nan"), dtype=BF, device="cuda")      # what the outputs' memory may hold
     for g in moe.ffn_backward(none, none, bank)[1:]:
         assert bool((g == 0).all())
+
+
+# ---------------------------------------------------------------- every tiling of the products
+
+FORWARD = sorted({sizes for product, _, sizes in FFN_TILINGS if product in ("gateup", "down")})
+BACKWARD = sorted({(product, sizes) for product, _, sizes in FFN_TILINGS if product not in ("gateup", "down")})
+NEED = {"dh": ("dw_up",), "dx": ("dx",), "dwgu": ("dw_gate", "dw_up"), "dw1": ("dw_up",), "dwd": ("dw_down",),
+        "grads": ("dx", "dw_gate", "dw_up", "dw_down")}
+
+
+@pytest.mark.parametrize("T,H,I", FORWARD)
+def test_ffn_tilings(T, H, I):
+    c = Ffn(T, H, I, 31)
+    out, guard = outbuf((T, H), BF)
+    gu, guard_gu = outbuf((T, 2 * I), F32)
+    y, gu = moe.ffn(c.x, c.bank, want_gu=True, out=out, gu=gu)
+    c.check_y(y)
+    c.check_gu(gu)
+    guard()
+    guard_gu()
+    assert torch.equal(moe.ffn(c.x, c.bank), y)
+    c.check_y(moe.ffn(c.x, c.bank, y_dtype=F32), "fp32 y")
+
+
+@pytest.mark.parametrize("product,sizes", BACKWARD)
+def test_ffn_gradient_tilings(product, sizes):
+    c = Ffn(*sizes, 32)
+    _, gu = moe.ffn(c.x, c.bank, want_gu=True)
+    grads = moe.ffn_backward(c.dy, c.x, c.bank, gu, need=NEED[product])
+    assert [g is not None for g in grads] == [n in NEED[product] for n in NEED["grads"]]
+    c.check_grads(grads)
+    if product == "dw1":
+        c.check_grads(moe.ffn_backward(c.dy, c.x, c.bank, gu, need=("dw_gate",)))
+
+
+@pytest.mark.parametrize("T,K,N", [sizes for _, _, sizes in I8_TILINGS])
+def test_linear_i8_tilings(T, K, N):
+    """The sum is exact and its three fp32 roundings are those of the formula, so fp32 outputs are equal bit for bit."""
+    gen = torch.Generator(device="cuda").manual_seed(T + K + N)
+    q, w = (torch.randint(-128, 128, s, generator=gen, dtype=I8, device="cuda") for s in ((T, K), (N, K)))
+    qs, ws, b = (torch.randn(n, generator=gen, device="cuda") for n in (T, N, N))
+    total = (q.double() @ w.double().t()).float()                # exact in 64 bits
+    ref = total * (qs[:, None] * ws)
+    for bias, out in ((None, F32), (b, F32), (None, BF), (b, BF)):
+        o, guard = outbuf((T, N), out)
+        moe.linear_i8(q, qs, w, ws, bias, out=o)
+        want = ref if bias is None else ref + bias
+        assert torch.equal(o, want.to(out)), (bias is not None, out)
+        guard()
