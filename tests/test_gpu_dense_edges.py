@@ -1,12 +1,14 @@
 """The operators around the MoE layer at the edges of what their boundary
 allows, against their formulas in 64 bits; inputs, formulas and bounds are those
 of test_gpu_dense.py."""
+import numpy as np
 import pytest
 import torch
 
 import routed_expert_ffn_04_amd as moe
 from dense_plan_cases import FFN as FFN_TILINGS, I8 as I8_TILINGS
-from test_gpu_dense import BF, F32, Ffn, HALF, I8, norm_case, norm_grad_ref, norm_ref, outbuf, rand, within
+from test_gpu_dense import (BF, F32, Ffn, HALF, I8, check_norm_grads, codes_of, norm_case, norm_grad_ref, norm_ref, outbuf,
+                            rand, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -36,6 +38,46 @@ def test_norm_with_another_eps(T, H, eps):
         assert {k for k, v in got.items() if v is not None} == set(ref)
         for k, (v, e) in ref.items():
             within(got[k], v, e + HALF[got[k].dtype] * (v.abs() + e), f"{k} gate_div={gate_div}")
+
+
+# rows that 64, 128, 256 (one and two chunks), 512 and 1024 threads hold; more rows than workers in the
+# forward step, so that a worker takes several: the next row in flight, both LDS sets of the row sums
+LONG_RUNS = [(9001, 264), (5001, 1001), (5003, 1024), (2501, 2003), (2500, 2048), (1201, 4104), (1200, 8192), (603, 8200),
+             (600, 16383)]
+TYPES = [(BF, BF, F32), (F32, F32, BF), (BF, F32, F32)]
+
+
+@pytest.mark.parametrize("T,H", LONG_RUNS)
+@pytest.mark.parametrize("y,r,w", TYPES)
+def test_norm_with_several_rows_a_worker(T, H, y, r, w):
+    """Forward, with gates that change inside a run of rows and one gate for all."""
+    for gate_div, off in ((5, 0), (T, 0), (1, 1)):
+        c = norm_case(T, H, 27, y, r, w, gate_div, off=off)
+        kw = dict(post_w=c["post_w"], gate=c["gate"], gate_div=gate_div, res_scale=0.75, pre_w=c["pre_w"])
+        ro, guard = outbuf((T, H), r)
+        got_r, got_x = moe.norm(c["y"], c["res"], r=ro, x_dtype=F32, **kw)
+        rr, xx, er, ex = norm_ref(c)
+        within(got_r, rr, er + HALF[r] * (rr.abs() + er), "r")
+        within(got_x, xx, ex + HALF[F32] * (xx.abs() + ex), "x")
+        guard()
+        _, (q, s) = moe.norm(c["y"], c["res"], x_dtype=I8, **kw)
+        rq, rs = codes_of(got_x)
+        assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+
+
+@pytest.mark.parametrize("T,H", [(777, 1001), (1500, 1024), (1100, 2003), (1025, 2048), (600, 4104), (1031, 7168), (520, 8200),
+                                 (513, 16384)])
+@pytest.mark.parametrize("y,r,w", TYPES)
+def test_norm_gradients_with_several_rows_a_run(T, H, y, r, w):
+    """Runs of two to five rows, the last one short: gates that end inside a run, that are whole
+    runs, that span runs, and none; with and without post_w and the gradient of x or r."""
+    for gate_div in (None, 1, 2, 3, 37, T):
+        check_norm_grads(norm_case(T, H, 28, y, r, w, gate_div))
+    check_norm_grads(norm_case(T, H, 29, y, r, w, 37, post=False))
+    c = norm_case(T, H, 30, y, r, w, 5)
+    check_norm_grads(c, use_dx=False)
+    check_norm_grads(c, use_dr=False)
+    check_norm_grads(norm_case(T, H, 31, y, r, w, 7, off=1))
 
 
 # ---------------------------------------------------------------- int8
