@@ -325,10 +325,10 @@ size_t moe_ffn_backward_workspace_size(int32_t T, int32_t H, int32_t I, int32_t 
  * post_w, pre_w: [H], gate: [ceil(T / gate_div)][H], all of w_dt (MOE_F32 or
  * MOE_BF16).  gate_div = T gives one gate for all tokens, a sequence length one
  * per sequence, 1 one per token.  r_out or x_out may be NULL (not written, but
- * not both).  x is formed from r before r is rounded to r_dt.  fp32
- * arithmetic; 1 <= H <= 16384, any alignment to the element (16 bytes and H a
- * multiple of 8 are faster).  Apart from r_out and res, no output may overlap
- * another tensor. */
+ * not both).  x is formed from r before r is rounded to r_dt.  eps >= 0; with
+ * eps = 0 a row of zeros has no norm (NaN).  fp32 arithmetic; 1 <= H <= 16384,
+ * any alignment to the element (16 bytes and H a multiple of 8 are faster).
+ * Apart from r_out and res, no output may overlap another tensor. */
 moe_status_t moe_norm(const void* y, int32_t y_dt, const void* res, int32_t r_dt, int32_t T, int32_t H,
                       const void* post_w, const void* gate, int32_t gate_div, const void* pre_w, int32_t w_dt,
                       float res_scale, float eps, void* r_out, void* x_out, int32_t x_dt, float* x_scale,

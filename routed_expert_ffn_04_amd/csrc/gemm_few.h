@@ -9,12 +9,13 @@
 // (l / 16), +16) of the block's two halves, for two MFMAs; tokens are laid out the
 // same way, so both sides agree on which k a piece holds.  More blocks in flight a
 // wave cost more than they bring (four together, unpipelined: 7.4 us against 6.4 for
-// a token of 1024 x 512, 9.2 against 8.9 of 2048 x 1408, weights from HBM).  The
+// a token of 1024 x 512, 9.2 against 8.9 of 2048 x 1408, in one run).  The
 // waves' sums meet in LDS in a fixed order and the epilogue follows, with no
 // second launch: k is split eight ways, and 16 rows a workgroup give enough
-// workgroups for every CU.  One token of the 7168 x 2048 block: 21.7 us and two
-// launches for 88 MB from HBM, 4.1 TB/s; two launches of next to nothing (256 x 512)
-// take 5.0.
+// workgroups for every CU.  One token of the 7168 x 2048 block: 22 us and two
+// launches for 88 MB from HBM, 4.0 TB/s; two launches of next to nothing (256 x 512)
+// take 5.1.  With 16 tokens as many bytes of x as of weights pass through a wave
+// (from L2): 30 us.
 #pragma once
 #include "gemm_tile.h"
 #include "tile_plan.h"

@@ -11,14 +11,16 @@
 // columns, each lane gets the 4 k values of one column).
 //
 // Tile.  BM x BN outputs per workgroup, 128 bytes of k per stage (64 bf16 or
-// 128 int8).  LDS is a ring of five half-stages (the A part or the B part of a
-// stage) filled by direct global->LDS 16-byte loads.  256 x 256 tiles: 8 waves
-// (2 x 4) of 128 x 64, all 160 KiB of LDS, one workgroup per CU.  128 x 128
-// tiles: 4 waves (2 x 2) of 64 x 64, 80 KiB, two workgroups per CU.  Each wave's
-// product is formed transposed (the n side is the MFMA row operand), so a lane
-// holds four consecutive n of one row m.  Four waves of 128 x 128 instead read a
-// third less from LDS but have nothing to run while they wait: T = 16384 FFN
-// 1187 us against 1179, T = 4096 gradients 729 against 664.
+// 128 int8).  LDS is a ring of R half-stages (the A part or the B part of a
+// stage) filled by direct global->LDS 16-byte loads.
+//   256 x 256: 8 waves (2 x 4) of 128 x 64; R = 5, 160 KiB, one workgroup per CU
+//   128 x 128: 4 waves (2 x 2) of 64 x 64;  R = 5, 80 KiB, two per CU, or R = 10, 160 KiB, one
+//    64 x 64:  4 waves (2 x 2) of 32 x 32;  R = 5, 40 KiB, four per CU, or R = 10, 80 KiB, two
+// The rings of ten are for products with few workgroups (launch_tiling).  Each
+// wave's product is formed transposed (the n side is the MFMA row operand), so a
+// lane holds four consecutive n of one row m.  Four waves of 128 x 128 for the
+// 256-row tiles read a third less from LDS but have nothing to run while they
+// wait: T = 16384 FFN 1187 us against 1179, T = 4096 gradients 729 against 664.
 //
 // What binds: the largest products the matrix cores at the clock the power limit
 // leaves (FFN of 16384 tokens, 7168 x 2048, 1110 us = 1.30 PFLOP/s; int8 8192 x 7168 x
@@ -29,10 +31,13 @@
 // KiB per CU into LDS in 0.36 us with 128-byte pieces and in 0.5 to 0.75 us
 // with 64-byte ones, and the loads are what limits a stage first.
 //
-// One barrier per stage, after the last fragments of a stage have been read
-// and before its last quarter multiplies: after it both halves of the stage are
-// free and take the B half one stage and the A half two stages ahead, which
-// leaves at least a whole stage of products for every load to land in.
+// One barrier per stage.  R = 5: after the last fragments of a stage have been
+// read and before its last quarter (256-row tiles) or half multiplies: after it
+// both halves of the stage are free and take the B half one stage and the A half
+// two stages ahead, which leaves at least a whole stage of products for every load
+// to land in.  R = 10: a stage's fragments are all in registers before it
+// multiplies, so its halves are free by then and take the stage five further on,
+// while the next stage's fragments are read.
 //
 // Bounds.  m and n past the end re-read the last row (last 16-byte chunk) and
 // are never stored; k past the end (the ragged last stage, and the stages that

@@ -8,7 +8,7 @@
 // its stored type.  A worker (the threads that share a row) takes a run of
 // consecutive rows: the weights are read once a run (at 7168 columns of fp32 they
 // are as many bytes as a row's own), and the next row's y and res are on their way
-// while a row is reduced.  16384 x 7168 with fp32 r: 280 us, 5.0 TB/s (half of the bytes
+// while a row is reduced.  16384 x 7168 with fp32 r: 282 us, 5.0 TB/s (half of the bytes
 // are writes; a copy reaches 4.9).  128 rows: 5 us, the latency of one row.
 #include "norm_row.h"
 

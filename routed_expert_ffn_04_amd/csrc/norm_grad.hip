@@ -242,7 +242,9 @@ inline int want_workers(int threads_per_row, int T) {
 }
 
 // Threads per row and chunks per thread: the row, the weights and the gradients
-// of its columns all stay in registers.
+// of its columns stay in registers up to 8192 columns.  Beyond, 1024 threads have 128
+// registers each, which do not hold them, and the rest goes through scratch memory:
+// 2048 x 16384 in bf16 315 us, 1.3 TB/s, where 4096 x 7168 has 4.2.
 struct Shape {
     int tpr, nv;
 };

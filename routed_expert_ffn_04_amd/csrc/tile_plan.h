@@ -14,9 +14,12 @@ inline bool grid_fits(long blocks, int threads) { return blocks > 0 && blocks <=
 constexpr int tile_threads(int edge) { return edge == 256 ? 512 : 256; }
 constexpr int kFewThreads = 512;
 
-// Beyond 16 rows the 64-row tiles take over.  At 16, weights from HBM: FFN of 1024 x
-// 512 7.6 us here and 9.7 in tiles, 4096 x 1024 14.1 and 17.3, 7168 x 2048 29.5 and
-// 27.6; two blocks of 16 rows here do not reach the tiles' 33 rows.
+// Up to 16 rows (one MFMA block) go to the kernel for a few rows, more to the tiles.
+// 16 rows, weights from HBM, there and in tiles: FFN of 256 x 512 5.8 and 7.5 us, of
+// 1024 x 512 8.1 and 11.4, 2048 x 1408 12.5 and 19.2, 4096 x 1024 15.3 and 19.1, 7168 x
+// 2048 30 to 32 and 30; int8 of 7168 x 4096 11.9 and 12.6.  Fewer rows gain more (4 rows
+// of 7168 x 2048 24.7 and 29.3).  Two blocks of 16 rows there do not reach the tiles'
+// 33 rows.
 constexpr int kFewRows = 16;
 
 struct Plan {
