@@ -259,3 +259,77 @@ def test_linear_i8_tilings(T, K, N):
         want = ref if bias is None else ref + bias
         assert torch.equal(o, want.to(out)), (bias is not None, out)
         guard()
+
+
+# ---------------------------------------------------------------- tensors of more than 2^31 elements
+
+def test_ffn_of_more_elements_than_an_int32_counts():
+    """Only the last rows are not zero, so everything, the weights' gradients too, is as for them alone."""
+    T, H, I, n = 524400, 4104, 264, 400
+    assert (T - n) * H > 1 << 31
+    c = Ffn(n, H, I, 33)
+    x, dy = (torch.zeros(T, H, dtype=BF, device="cuda") for _ in range(2))
+    x[-n:], dy[-n:] = c.x, c.dy
+    y, gu = moe.ffn(x, c.bank, want_gu=True)
+    c.check_y(y[-n:])
+    c.check_gu(gu[-n:])
+    assert not bool(y[:-n].any())
+    dx, *dw = moe.ffn_backward(dy, x, c.bank, gu)
+    c.check_grads([dx[-n:], *dw])
+    assert not bool(dx[:-n].any())
+
+
+def test_norm_of_more_elements_than_an_int32_counts():
+    """Rows do not depend on each other: the last ones are as in a call of their own."""
+    T, H, n = 262400, 8192, 200
+    assert (T - n) * H > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    y, res, dx = (torch.empty(T, H, dtype=BF, device="cuda").normal_(generator=gen) for _ in range(3))
+    w = torch.rand(H, generator=gen, device="cuda") + 0.5
+    kw = dict(post_w=w, pre_w=w, res_scale=0.75)
+    for x_dtype in (BF, I8):
+        r, x = moe.norm(y, res, x_dtype=x_dtype, **kw)
+        r1, x1 = moe.norm(y[-n:], res[-n:], x_dtype=x_dtype, **kw)
+        assert torch.equal(r[-n:], r1)
+        for a, b in zip(x, x1) if x_dtype is I8 else ((x, x1),):
+            assert torch.equal(a[-n:], b)
+    g = moe.norm_backward(dx, res, y, r, **kw)
+    g1 = moe.norm_backward(dx[-n:], res[-n:], y[-n:], r1, **kw)
+    assert torch.equal(g["dy"][-n:], g1["dy"]) and torch.equal(g["dres"][-n:], g1["dres"])
+
+
+@pytest.mark.parametrize("T,K,N", [(131200, 16400, 72), (3, 16400, 131200), (40, 16400, 131200), (131200, 16, 16500)])
+def test_linear_i8_of_more_elements_than_an_int32_counts(T, K, N):
+    """Codes, weights (few rows and tiles) and outputs: the last rows and columns, bit for bit."""
+    assert max(T * K, N * K, T * N) > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    q, w = (torch.randint(-128, 128, s, generator=gen, dtype=I8, device="cuda") for s in ((T, K), (N, K)))
+    qs, ws = torch.rand(T, generator=gen, device="cuda"), torch.rand(N, generator=gen, device="cuda")
+    out = moe.linear_i8(q, qs, w, ws, out_dtype=F32)
+    t, n = slice(max(0, T - 150), T), slice(max(0, N - 150), N)
+    total = (q[t].double() @ w[n].double().t()).float()
+    assert torch.equal(out[t, n], total * (qs[t, None] * ws[n]))
+
+
+# ---------------------------------------------------------------- streams
+
+def test_norm_and_int8_on_streams_of_their_own():
+    """Two streams at once, each call's scratch and outputs its own."""
+    c = norm_case(1500, 520, 34, gate_div=37)
+    w = torch.randint(-127, 128, (130, 512), dtype=I8, device="cuda")
+    ws = torch.rand(130, device="cuda")
+    x = c["y"][:, :512].contiguous()
+    kw = dict(post_w=c["post_w"], gate=c["gate"], gate_div=37, pre_w=c["pre_w"])
+
+    def calls(stream=None):
+        q, s = moe.quant_i8(x, stream=stream)
+        return [*moe.norm(c["y"], c["res"], stream=stream, **kw),
+                *moe.norm_backward(c["dx"], c["dr"], c["y"], c["res"], stream=stream, **kw).values(),
+                q, s, moe.linear_i8(q, s, w, ws, stream=stream)]
+    want = calls()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [calls(s) for _ in range(3) for s in streams]
+    torch.cuda.synchronize()
+    for one in got:
+        assert all(torch.equal(a, b) for a, b in zip(one, want))
