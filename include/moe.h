@@ -370,6 +370,98 @@ moe_status_t moe_linear_i8(const int8_t* q, const float* q_scale, int32_t T, int
 /* May be 0 (no workspace needed: ws may be NULL). */
 size_t moe_linear_i8_workspace_size(int32_t T, int32_t K, int32_t N);
 
+/* ---- training step of the layer ---------------------------------------------
+ * The routed half of the layer with its gradients, on rows sorted by expert:
+ * moe_route, moe_permute, moe_dispatch, moe_experts_ffn, moe_combine forward;
+ * moe_combine_backward, moe_experts_ffn_backward, moe_dispatch_backward back.
+ * (The shared expert: moe_ffn, moe_ffn_backward.)
+ *
+ * Activation checkpoints in 8 bits.  What the backward pass needs of the forward
+ * pass, x and the pre-activations, may be held as blocks of 16 consecutive values
+ * of a row: int8 codes and one E8M0 exponent per block (the last block of a row may be
+ * shorter).  With f the exponent field of the block's largest magnitude as fp32:
+ *     E = max(f - 6, 1),  code = round-to-nearest-even(v * 2^(127 - E)) clamped to [-127, 127]
+ *     value = code * 2^(E - 127)          (exact in fp32 and in bf16)
+ * A step 2^(E - 127) is at most 1/64 of the block's largest magnitude (of magnitudes of 2^-119
+ * and more), and a value is off by at most half a step, or less than one where 127.5
+ * steps and more are held as 127.  A block with an infinity or a
+ * NaN has E = 255, codes 0 and the value NaN. */
+
+/* x: [rows][cols] MOE_F32 or MOE_BF16, cols a positive multiple of 8; q: codes [rows][cols];
+ * e8: [rows][ceil(cols / 16)].  x, out 16-byte, q 8-byte aligned. */
+moe_status_t moe_quant_i8x16(const void* x, int32_t x_dt, int32_t rows, int32_t cols, int8_t* q, uint8_t* e8,
+                             void* stream);
+/* The values, as MOE_F32 or MOE_BF16 (both exact). */
+moe_status_t moe_dequant_i8x16(const int8_t* q, const uint8_t* e8, int32_t rows, int32_t cols, void* out,
+                               int32_t out_dt, void* stream);
+
+/* xs[dest[t * k + j]] = x[t]: the tokens' rows sorted by expert.  dest: [T][k], of
+ * moe_permute, or with values outside [0, R) for assignments that have no row here
+ * (another GPU's experts), which are skipped; no row may be named twice.  Rows
+ * that are not named stay as they are.  x: [T][H] MOE_F32, MOE_BF16, or MOE_I8: codes of
+ * moe_quant_i8x16 with the exponents x_e8 [T][ceil(H / 16)] (NULL otherwise).  xs: [R][H] of x's type,
+ * MOE_BF16 for MOE_I8.  H a positive multiple of 8; rows 16-byte aligned (codes 8); T, R and T * k at most 2^30. */
+moe_status_t moe_dispatch(const void* x, int32_t x_dt, const uint8_t* x_e8, int32_t T, int32_t H, const int32_t* dest,
+                          int32_t k, int32_t R, void* xs, void* stream);
+
+/* Gradient of moe_dispatch: dx[t] = add[t] + sum_j dxs[dest[t * k + j]], fp32, in this order
+ * (assignments without a row here add nothing).  dxs: [R][H], add: [T][H] or NULL (0;
+ * the gradient of x from elsewhere, e.g. the shared expert), dx: [T][H], which may be add itself
+ * if their types agree; each MOE_F32 or MOE_BF16, 16-byte aligned, H a positive multiple of 8. */
+moe_status_t moe_dispatch_backward(const void* dxs, int32_t dxs_dt, int32_t R, const int32_t* dest, int32_t T,
+                                   int32_t k, int32_t H, const void* add, int32_t add_dt, void* dx, int32_t dx_dt,
+                                   void* stream);
+
+/* Gradients of moe_combine for the output gradient dout [T][H] (MOE_F32 or MOE_BF16):
+ *     dy[dest[t * k + j]] = topk_w[t][j] * dout[t]        dw[t][j] = sum_h dout[t][h] * y[dest[t * k + j]][h]
+ * (the gradient of y_sh is dout itself).  y: what moe_combine read, [R][H] MOE_F32, MOE_BF16 or
+ * MOE_E4M3 with y_scale; may be NULL without dw.  dy: [R][H] MOE_F32 or MOE_BF16, rows that
+ * dest does not name stay as they are; dw: [T][k] fp32, 0 for assignments without a row
+ * here.  Either may be NULL.  Sums are fp32.  H a positive multiple of 8 (128 with MOE_E4M3 y); rows
+ * 16-byte aligned (codes 8). */
+moe_status_t moe_combine_backward(const void* dout, int32_t dout_dt, const void* y, int32_t y_dt, const float* y_scale,
+                                  int32_t R, const int32_t* dest, const float* topk_w, int32_t T, int32_t k, int32_t H,
+                                  void* dy, int32_t dy_dt, float* dw, void* stream);
+
+/* The gated FFN of n experts on rows sorted by expert (moe_ffn with the weights of
+ * expert e for the rows p in [offsets[e], offsets[e + 1])).
+ * xs: [R][H] MOE_BF16; offsets: [n + 1] int32 on the device, ascending, offsets[n] <= R; bank: MOE_BF16,
+ * 1 <= n <= 1024, H and I positive multiples of 8 up to 2^21; y: [R][H] MOE_BF16 or MOE_F32.  Rows
+ * outside every expert's are not read, and are written nowhere.  What the backward pass needs:
+ * gu, NULL to skip, with gu_dt MOE_F32: [R][2 I], row p holding g then u, or
+ * MOE_I8: codes [R][2 I] with the exponents gu_e8 [R][2 ceil(I / 16)], g's blocks
+ * then u's.  16-byte aligned (gu_e8: any); R at most 2^30; no output may overlap another tensor. */
+moe_status_t moe_experts_ffn(const void* xs, int32_t x_dt, const int32_t* offsets, int32_t R, const moe_experts_t* bank,
+                             void* y, int32_t y_dt, void* gu, int32_t gu_dt, uint8_t* gu_e8, void* ws, size_t ws_bytes,
+                             void* stream);
+/* 0 for sizes that moe_experts_ffn refuses and for R = 0. */
+size_t moe_experts_ffn_workspace_size(int32_t R, int32_t n, int32_t H, int32_t I);
+
+/* Gradients of moe_experts_ffn (those of moe_ffn_backward, each expert over its own
+ * rows).  dy, dx: [R][H] MOE_BF16; xs: [R][H], x_dt MOE_BF16, or MOE_I8 with exponents
+ * x_e8; gu, gu_dt, gu_e8: as moe_experts_ffn wrote them, or NULL (computed again from xs).
+ * dw_gate, dw_up: [n][I][H], dw_down: [n][H][I], MOE_BF16, written, with zeros for an expert
+ * without rows.  Each output may be NULL. */
+moe_status_t moe_experts_ffn_backward(const void* dy, const void* xs, int32_t x_dt, const uint8_t* x_e8,
+                                      const int32_t* offsets, int32_t R, const moe_experts_t* bank, const void* gu,
+                                      int32_t gu_dt, const uint8_t* gu_e8, void* dx, void* dw_gate, void* dw_up,
+                                      void* dw_down, void* ws, size_t ws_bytes, void* stream);
+size_t moe_experts_ffn_backward_workspace_size(int32_t R, int32_t n, int32_t H, int32_t I, int32_t has_gu,
+                                               int32_t x_dt);
+
+/* moe_ffn and moe_ffn_backward with checkpoints in 8 bits: gu as codes [T][2 I] with
+ * exponents gu_e8 [T][2 ceil(I / 16)] (required); in the backward pass xs as MOE_BF16, or
+ * MOE_I8 with exponents x_e8. */
+moe_status_t moe_ffn_ckpt(const void* x, int32_t x_dt, int32_t T, const moe_experts_t* bank, void* y, int32_t y_dt,
+                          int8_t* gu, uint8_t* gu_e8, void* ws, size_t ws_bytes, void* stream);
+size_t moe_ffn_ckpt_workspace_size(int32_t T, int32_t H, int32_t I);
+/* gu_dt: MOE_I8, or MOE_F32 (what moe_ffn wrote, or NULL to compute it again). */
+moe_status_t moe_ffn_ckpt_backward(const void* dy, const void* x, int32_t x_dt, const uint8_t* x_e8, int32_t T,
+                                   const moe_experts_t* bank, const void* gu, int32_t gu_dt, const uint8_t* gu_e8,
+                                   void* dx, void* dw_gate, void* dw_up, void* dw_down, void* ws, size_t ws_bytes,
+                                   void* stream);
+size_t moe_ffn_ckpt_backward_workspace_size(int32_t T, int32_t H, int32_t I, int32_t has_gu, int32_t x_dt);
+
 /* Name of a status code; text of the calling thread's last error ("" if none). */
 const char* moe_status_string(int32_t status);
 const char* moe_last_error(void);

@@ -7,8 +7,10 @@ first use and a missing library is an error (there is no fallback path).
 
 Entry points mirror the C ABI: route, permute, quant_e4m3_1x128,
 quant_mxfp8, grouped_ffn, combine, layer, layer_noalloc (plus
-workspace-size queries), and around the layer: ffn, ffn_backward, norm,
-norm_backward, quant_i8, linear_i8.
+workspace-size queries), around the layer: ffn, ffn_backward, norm,
+norm_backward, quant_i8, linear_i8, and for its training step: dispatch,
+dispatch_backward, combine_backward, experts_ffn, experts_ffn_backward,
+quant_i8x16, dequant_i8x16.
 """
 from __future__ import annotations
 
@@ -36,6 +38,10 @@ EXPORTS = [
     "moe_ffn", "moe_ffn_workspace_size", "moe_ffn_backward", "moe_ffn_backward_workspace_size",
     "moe_norm", "moe_norm_backward", "moe_norm_backward_workspace_size",
     "moe_quant_i8", "moe_linear_i8", "moe_linear_i8_workspace_size",
+    "moe_quant_i8x16", "moe_dequant_i8x16", "moe_dispatch", "moe_dispatch_backward", "moe_combine_backward",
+    "moe_experts_ffn", "moe_experts_ffn_workspace_size", "moe_experts_ffn_backward",
+    "moe_experts_ffn_backward_workspace_size", "moe_ffn_ckpt", "moe_ffn_ckpt_workspace_size", "moe_ffn_ckpt_backward",
+    "moe_ffn_ckpt_backward_workspace_size",
     "moe_status_string", "moe_last_error",
 ]
 
@@ -93,6 +99,21 @@ def lib() -> ctypes.CDLL:
             "moe_quant_i8": ([_P, _I32, _I32, _I32, _P, _P, _P], _I32),
             "moe_linear_i8": ([_P, _P, _I32, _I32, _P, _P, _P, _I32, _P, _I32, _P, _SZ, _P], _I32),
             "moe_linear_i8_workspace_size": ([_I32] * 3, _SZ),
+            "moe_quant_i8x16": ([_P, _I32, _I32, _I32, _P, _P, _P], _I32),
+            "moe_dequant_i8x16": ([_P, _P, _I32, _I32, _P, _I32, _P], _I32),
+            "moe_dispatch": ([_P, _I32, _P, _I32, _I32, _P, _I32, _I32, _P, _P], _I32),
+            "moe_dispatch_backward": ([_P, _I32, _I32, _P, _I32, _I32, _I32, _P, _I32, _P, _I32, _P], _I32),
+            "moe_combine_backward": ([_P, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _P, _I32, _P, _P], _I32),
+            "moe_experts_ffn": ([_P, _I32, _P, _I32, ctypes.POINTER(ExpertsT), _P, _I32, _P, _I32, _P, _P, _SZ, _P], _I32),
+            "moe_experts_ffn_workspace_size": ([_I32] * 4, _SZ),
+            "moe_experts_ffn_backward": ([_P, _P, _I32, _P, _P, _I32, ctypes.POINTER(ExpertsT), _P, _I32, _P,
+                                          _P, _P, _P, _P, _P, _SZ, _P], _I32),
+            "moe_experts_ffn_backward_workspace_size": ([_I32] * 6, _SZ),
+            "moe_ffn_ckpt": ([_P, _I32, _I32, ctypes.POINTER(ExpertsT), _P, _I32, _P, _P, _P, _SZ, _P], _I32),
+            "moe_ffn_ckpt_workspace_size": ([_I32] * 3, _SZ),
+            "moe_ffn_ckpt_backward": ([_P, _P, _I32, _P, _I32, ctypes.POINTER(ExpertsT), _P, _I32, _P,
+                                       _P, _P, _P, _P, _P, _SZ, _P], _I32),
+            "moe_ffn_ckpt_backward_workspace_size": ([_I32] * 5, _SZ),
             "moe_status_string": ([_I32], ctypes.c_char_p),
             "moe_last_error": ([], ctypes.c_char_p),
         }
@@ -487,55 +508,156 @@ def _dense_bank(bank: Experts, H: int, device):
     return ExpertsT(1, H, I, BF16, wg.data_ptr(), wu.data_ptr(), wd.data_ptr()), I
 
 
-def ffn(x, bank: Experts, *, want_gu: bool = False, y_dtype=None, out=None, gu=None, ws=None, stream=None):
+# ---- checkpoints in 8 bits: a pair (codes int8 [rows][cols], exponents uint8 [rows][blocks of 16])
+
+_BLOCK = 16
+
+
+def _pair(device: int, name, t, rows, cols, parts=1):
+    """Checks such a pair; `parts` matrices side by side have blocks of their own."""
+    q, e = t
+    _tensor(device, name, q, (rows, parts * cols), (torch.int8,))
+    _tensor(device, f"{name}'s exponents", e, (rows, parts * -(-cols // _BLOCK)), (torch.uint8,))
+
+
+def _saved(device: int, gu, rows, I):
+    """(pointer, dtype code, pointer of the exponents) of the saved pre-activations given."""
+    if isinstance(gu, tuple):
+        _pair(device, "gu", gu, rows, I, 2)
+        return gu[0].data_ptr(), I8, gu[1].data_ptr()
+    _tensor(device, "gu", gu, (rows, 2 * I), (torch.float32,))
+    return _ptr(gu), F32, None
+
+
+def _to_save(device: int, like, gu, want_gu, gu_dtype, rows, I):
+    """The saved pre-activations to write: those given, new ones, or None."""
+    if gu_dtype not in (None, torch.float32, torch.int8):
+        raise TypeError(f"gu {gu_dtype}")
+    if gu is not None:
+        if gu_dtype is not None and isinstance(gu, tuple) != (gu_dtype is torch.int8):
+            raise TypeError(f"gu is {'int8 blocks' if isinstance(gu, tuple) else gu.dtype}, but {gu_dtype} is asked for")
+    elif want_gu:
+        if gu_dtype is torch.int8:
+            gu = (_empty(like, (rows, 2 * I), torch.int8), _empty(like, (rows, 2 * -(-I // _BLOCK)), torch.uint8))
+        else:
+            gu = _empty(like, (rows, 2 * I), torch.float32)
+    return gu
+
+
+def quant_i8x16(x, stream=None, out=None):
+    """8-bit checkpoint of x [rows][cols] (moe_quant_i8x16): int8 codes [rows][cols]
+    and uint8 exponents [rows][ceil(cols / 16)]."""
+    rows, cols, dev = _matrix("x", x)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return quant_i8x16(x, out=out)
+    _tensor(dev, "x", x, (rows, cols), _FLOATS)
+    if out is None:
+        out = (_empty(x, (rows, cols), torch.int8), _empty(x, (rows, -(-cols // _BLOCK)), torch.uint8))
+    else:
+        _pair(dev, "out", out, rows, cols)
+    q, e = out
+    L = _lib or lib()
+    _check(L.moe_quant_i8x16(x.data_ptr(), _CODE[x.dtype], rows, cols, q.data_ptr(), e.data_ptr(), _current(dev)))
+    return q, e
+
+
+def dequant_i8x16(q, e, *, out_dtype=None, out=None, stream=None):
+    """The values of such a checkpoint (moe_dequant_i8x16), exact in out_dtype
+    torch.bfloat16 (default) and torch.float32."""
+    rows, cols, dev = _matrix("q", q)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return dequant_i8x16(q, e, out_dtype=out_dtype, out=out)
+    out_dtype = _out_dtype("out", out, out_dtype, torch.bfloat16)
+    if out_dtype not in _FLOATS:
+        raise TypeError(f"dequant_i8x16: out {out_dtype}")
+    _pair(dev, "q", (q, e), rows, cols)
+    _tensor(dev, "out", out, (rows, cols), (out_dtype,))
+    if out is None:
+        out = _empty(q, (rows, cols), out_dtype)
+    L = _lib or lib()
+    _check(L.moe_dequant_i8x16(q.data_ptr(), e.data_ptr(), rows, cols, out.data_ptr(), _CODE[out_dtype], _current(dev)))
+    return out
+
+
+def ffn(x, bank: Experts, *, want_gu: bool = False, gu_dtype=None, y_dtype=None, out=None, gu=None, ws=None, stream=None):
     """The dense gated FFN block (moe_ffn) with a bf16 bank of n = 1.  Returns
-    y [T][H], or (y, gu) with want_gu: gu fp32 [T][2 I], what ffn_backward needs."""
+    y [T][H], or (y, gu) with want_gu: what ffn_backward needs, fp32 [T][2 I], or
+    with gu_dtype torch.int8 an 8-bit checkpoint, the pair (codes [T][2 I], exponents
+    [T][2 ceil(I / 16)])."""
     T, H, dev = _matrix("x", x)
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
-            return ffn(x, bank, want_gu=want_gu, y_dtype=y_dtype, out=out, gu=gu, ws=ws)
+            return ffn(x, bank, want_gu=want_gu, gu_dtype=gu_dtype, y_dtype=y_dtype, out=out, gu=gu, ws=ws)
     st, I = _dense_bank(bank, H, dev)
     y_dtype = _out_dtype("out", out, y_dtype, torch.bfloat16)
     if y_dtype not in _FLOATS:
         raise TypeError(f"ffn: y {y_dtype}")
     _tensor(dev, "x", x, (T, H), (torch.bfloat16,))
     _tensor(dev, "out", out, (T, H), _FLOATS)
-    _tensor(dev, "gu", gu, (T, 2 * I), (torch.float32,))
+    gu = _to_save(dev, x, gu, want_gu, gu_dtype, T, I)
+    gp, g_dt, ge = _saved(dev, gu, T, I)
     if out is None:
         out = _empty(x, (T, H), y_dtype)
-    if gu is None and want_gu:
-        gu = _empty(x, (T, 2 * I), torch.float32)
     L = _lib or lib()
-    wp, wn, ws = _scratch(ws, L.moe_ffn_workspace_size(T, H, I), x)
-    _check(L.moe_ffn(x.data_ptr(), BF16, T, ctypes.byref(st), out.data_ptr(), _CODE[out.dtype], _ptr(gu), wp, wn,
-                     _current(dev)))
+    if g_dt == I8:
+        wp, wn, ws = _scratch(ws, L.moe_ffn_ckpt_workspace_size(T, H, I), x)
+        _check(L.moe_ffn_ckpt(x.data_ptr(), BF16, T, ctypes.byref(st), out.data_ptr(), _CODE[out.dtype], gp, ge, wp, wn,
+                              _current(dev)))
+    else:
+        wp, wn, ws = _scratch(ws, L.moe_ffn_workspace_size(T, H, I), x)
+        _check(L.moe_ffn(x.data_ptr(), BF16, T, ctypes.byref(st), out.data_ptr(), _CODE[out.dtype], gp, wp, wn,
+                         _current(dev)))
     return (out, gu) if want_gu else out
 
 
-def ffn_backward(dy, x, bank: Experts, gu=None, *, need=("dx", "dw_gate", "dw_up", "dw_down"), ws=None, stream=None):
+_GRADS = ("dx", "dw_gate", "dw_up", "dw_down")
+
+
+def _grads(need, dy, bank):
+    """The gradients to write: those wanted, like dy and the weights."""
+    if not set(need) <= set(_GRADS):
+        raise ValueError(f"need: {need}")
+    likes = (dy, bank.w_gate, bank.w_up, bank.w_down)
+    return tuple(torch.empty_like(t) if k in need else None for k, t in zip(_GRADS, likes))
+
+
+def _kept_x(device: int, name, x, rows, H):
+    """(pointer, dtype code, pointer of the exponents) of a bf16 matrix or its 8-bit checkpoint."""
+    if isinstance(x, tuple):
+        _pair(device, name, x, rows, H)
+        return x[0].data_ptr(), I8, x[1].data_ptr()
+    _tensor(device, name, x, (rows, H), (torch.bfloat16,))
+    return x.data_ptr(), BF16, None
+
+
+def ffn_backward(dy, x, bank: Experts, gu=None, *, need=_GRADS, ws=None, stream=None):
     """Gradients of ffn (moe_ffn_backward): (dx [T][H], dw_gate, dw_up [1][I][H],
     dw_down [1][H][I]), None for those not in `need`.  gu: what ffn returned
-    (None: computed again)."""
-    T, H, dev = _matrix("x", x)
+    (None: computed again).  x may be its 8-bit checkpoint, the pair that
+    quant_i8x16 returned."""
+    T, H, dev = _matrix("dy", dy)
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
             return ffn_backward(dy, x, bank, gu, need=need, ws=ws)
     st, I = _dense_bank(bank, H, dev)
-    bf = (torch.bfloat16,)
-    _tensor(dev, "x", x, (T, H), bf)
-    _tensor(dev, "dy", dy, (T, H), bf)
-    _tensor(dev, "gu", gu, (T, 2 * I), (torch.float32,))
-    names = ("dx", "dw_gate", "dw_up", "dw_down")
-    if not set(need) <= set(names):
-        raise ValueError(f"need: {need}")
-    likes = (x, bank.w_gate, bank.w_up, bank.w_down)
-    o = tuple(torch.empty_like(t) if k in need else None for k, t in zip(names, likes))
+    _tensor(dev, "dy", dy, (T, H), (torch.bfloat16,))
+    xp, x_dt, xe = _kept_x(dev, "x", x, T, H)
+    gp, g_dt, ge = _saved(dev, gu, T, I)
+    o = _grads(need, dy, bank)
     L = _lib or lib()
-    wp, wn, ws = _scratch(ws, L.moe_ffn_backward_workspace_size(T, H, I, int(gu is not None)), x)
-    _check(L.moe_ffn_backward(dy.data_ptr(), x.data_ptr(), BF16, T, ctypes.byref(st), _ptr(gu), *map(_ptr, o), wp, wn,
-                              _current(dev)))
+    if x_dt == I8 or g_dt == I8:
+        wp, wn, ws = _scratch(ws, L.moe_ffn_ckpt_backward_workspace_size(T, H, I, int(gu is not None), x_dt), dy)
+        _check(L.moe_ffn_ckpt_backward(dy.data_ptr(), xp, x_dt, xe, T, ctypes.byref(st), gp, g_dt, ge, *map(_ptr, o), wp, wn,
+                                       _current(dev)))
+    else:
+        wp, wn, ws = _scratch(ws, L.moe_ffn_backward_workspace_size(T, H, I, int(gu is not None)), dy)
+        _check(L.moe_ffn_backward(dy.data_ptr(), xp, BF16, T, ctypes.byref(st), gp, *map(_ptr, o), wp, wn, _current(dev)))
     return o
 
 
@@ -685,3 +807,187 @@ def linear_i8(q, q_scale, w, w_scale, bias=None, *, out_dtype=None, out=None, ws
     _check(L.moe_linear_i8(q.data_ptr(), q_scale.data_ptr(), T, K, w.data_ptr(), w_scale.data_ptr(), _ptr(bias), N,
                            out.data_ptr(), _CODE[out_dtype], wp, wn, _current(dev)))
     return out
+
+
+# ---------------------------------------------------------------- training step of the layer
+
+def _experts_bank(bank: Experts, H: int, device):
+    bf = (torch.bfloat16,)
+    wg, wu, wd = bank.w_gate, bank.w_up, bank.w_down
+    if wg.dim() != 3 or bank.dt not in (None, BF16):
+        raise ValueError("bank: bf16 weights [n][I][H] and [n][H][I]")
+    n, I, _ = wg.shape
+    if n > _MOST or I > _MOST:
+        raise ValueError(f"bank: n={n} or I={I} is above {_MOST}")
+    _tensor(device, "w_gate", wg, (n, I, H), bf)
+    _tensor(device, "w_up", wu, (n, I, H), bf)
+    _tensor(device, "w_down", wd, (n, H, I), bf)
+    return ExpertsT(n, H, I, BF16, wg.data_ptr(), wu.data_ptr(), wd.data_ptr()), n, I
+
+
+def experts_ffn(xs, offsets, bank: Experts, *, want_gu: bool = False, gu_dtype=None, y_dtype=None, out=None, gu=None,
+                ws=None, stream=None):
+    """The gated FFN of the bank's n bf16 experts on rows sorted by expert
+    (moe_experts_ffn): rows [offsets[e], offsets[e + 1]) of xs [R][H] with expert e.
+    Returns y [R][H] (rows of no expert are not written), or (y, gu) with
+    want_gu: what experts_ffn_backward needs, fp32 [R][2 I], or with gu_dtype torch.int8
+    an 8-bit checkpoint, the pair (codes [R][2 I], exponents [R][2 ceil(I / 16)])."""
+    R, H, dev = _matrix("xs", xs)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return experts_ffn(xs, offsets, bank, want_gu=want_gu, gu_dtype=gu_dtype, y_dtype=y_dtype, out=out, gu=gu, ws=ws)
+    st, n, I = _experts_bank(bank, H, dev)
+    y_dtype = _out_dtype("out", out, y_dtype, torch.bfloat16)
+    if y_dtype not in _FLOATS:
+        raise TypeError(f"experts_ffn: y {y_dtype}")
+    _tensor(dev, "xs", xs, (R, H), (torch.bfloat16,))
+    _tensor(dev, "offsets", offsets, (n + 1,), (torch.int32,))
+    _tensor(dev, "out", out, (R, H), _FLOATS)
+    gu = _to_save(dev, xs, gu, want_gu, gu_dtype, R, I)
+    gp, g_dt, ge = _saved(dev, gu, R, I)
+    if out is None:
+        out = _empty(xs, (R, H), y_dtype)
+    L = _lib or lib()
+    wp, wn, ws = _scratch(ws, L.moe_experts_ffn_workspace_size(R, n, H, I), xs)
+    _check(L.moe_experts_ffn(xs.data_ptr(), BF16, offsets.data_ptr(), R, ctypes.byref(st), out.data_ptr(), _CODE[out.dtype],
+                             gp, g_dt, ge, wp, wn, _current(dev)))
+    return (out, gu) if want_gu else out
+
+
+def experts_ffn_backward(dy, xs, offsets, bank: Experts, gu=None, *, need=_GRADS, ws=None, stream=None):
+    """Gradients of experts_ffn (moe_experts_ffn_backward): (dx [R][H], dw_gate,
+    dw_up [n][I][H], dw_down [n][H][I]), None for those not in `need`; zeros for an
+    expert without rows.  gu: what experts_ffn returned (None: computed again).  xs
+    may be its 8-bit checkpoint, the pair that quant_i8x16 returned."""
+    R, H, dev = _matrix("dy", dy)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return experts_ffn_backward(dy, xs, offsets, bank, gu, need=need, ws=ws)
+    st, n, I = _experts_bank(bank, H, dev)
+    _tensor(dev, "dy", dy, (R, H), (torch.bfloat16,))
+    _tensor(dev, "offsets", offsets, (n + 1,), (torch.int32,))
+    xp, x_dt, xe = _kept_x(dev, "xs", xs, R, H)
+    gp, g_dt, ge = _saved(dev, gu, R, I)
+    o = _grads(need, dy, bank)
+    L = _lib or lib()
+    wp, wn, ws = _scratch(ws, L.moe_experts_ffn_backward_workspace_size(R, n, H, I, int(gu is not None), x_dt), dy)
+    _check(L.moe_experts_ffn_backward(dy.data_ptr(), xp, x_dt, xe, offsets.data_ptr(), R, ctypes.byref(st), gp, g_dt, ge,
+                                      *map(_ptr, o), wp, wn, _current(dev)))
+    return o
+
+
+def _slots(name, dest, k, device):
+    """Tokens of dest ([T * k] or [T][k] int32)."""
+    if k < 1 or k > _MOST or dest.numel() % k:
+        raise ValueError(f"{name}: dest of {dest.numel()} values with k={k}")
+    T = dest.numel() // k
+    _tensor(device, "dest", dest, (T, k) if dest.dim() == 2 else (T * k,), (torch.int32,))
+    return T
+
+
+def dispatch(x, dest, k: int, *, R=None, out=None, stream=None):
+    """Rows of the tokens sorted by expert (moe_dispatch): xs[dest[t * k + j]] = x[t].
+    x: [T][H] fp32 or bf16, or its 8-bit checkpoint, the pair that quant_i8x16
+    returned (xs is then bf16).  dest: as permute returned it; values outside [0, R)
+    are skipped.  R: rows of xs (default T * k); rows that dest does not name are not
+    written."""
+    q, e = x if isinstance(x, tuple) else (x, None)
+    T, H, dev = _matrix("x", q)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return dispatch(x, dest, k, R=R, out=out)
+    if _slots("dispatch", dest, k, dev) != T:
+        raise ValueError(f"dispatch: dest of {dest.numel()} values with T={T}, k={k}")
+    if e is None:
+        _tensor(dev, "x", q, (T, H), _FLOATS)
+        code, dtype = _CODE[q.dtype], q.dtype
+    else:
+        _pair(dev, "x", x, T, H)
+        code, dtype = I8, torch.bfloat16
+    R = (T * k if out is None else out.shape[0]) if R is None else R
+    if not 0 <= R <= _MOST:
+        raise ValueError(f"dispatch: R={R}")
+    _tensor(dev, "out", out, (R, H), (dtype,))
+    if out is None:
+        out = _empty(q, (R, H), dtype)
+    L = _lib or lib()
+    _check(L.moe_dispatch(q.data_ptr(), code, _ptr(e), T, H, dest.data_ptr(), k, R, out.data_ptr(), _current(dev)))
+    return out
+
+
+def dispatch_backward(dxs, dest, k: int, *, add=None, out_dtype=None, out=None, stream=None):
+    """Gradient of dispatch (moe_dispatch_backward): dx[t] = add[t] + sum_j dxs[dest[t * k + j]].
+    out_dtype: default dxs's.  out may be add itself."""
+    R, H, dev = _matrix("dxs", dxs)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return dispatch_backward(dxs, dest, k, add=add, out_dtype=out_dtype, out=out)
+    T = _slots("dispatch_backward", dest, k, dev)
+    out_dtype = _out_dtype("out", out, out_dtype, dxs.dtype)
+    if out_dtype not in _FLOATS:
+        raise TypeError(f"dispatch_backward: dx {out_dtype}")
+    _tensor(dev, "dxs", dxs, (R, H), _FLOATS)
+    _tensor(dev, "add", add, (T, H), _FLOATS)
+    _tensor(dev, "out", out, (T, H), (out_dtype,))
+    if out is None:
+        out = _empty(dxs, (T, H), out_dtype)
+    L = _lib or lib()
+    _check(L.moe_dispatch_backward(dxs.data_ptr(), _CODE[dxs.dtype], R, dest.data_ptr(), T, k, H, _ptr(add),
+                                   F32 if add is None else _CODE[add.dtype], out.data_ptr(), _CODE[out_dtype], _current(dev)))
+    return out
+
+
+def combine_backward(dout, y_perm, dest, topk_w, *, y_scale=None, R=None, dy_dtype=None, need=("dy", "dw"), dy=None,
+                     stream=None):
+    """Gradients of combine (moe_combine_backward) for the output gradient dout [T][H]:
+    (dy [R][H], dw [T][k] fp32), None for those not in `need`; that of y_sh is dout
+    itself.  y_perm, y_scale: what combine read (y_perm may be None without dw).  R: rows of
+    dy (default y_perm's, or T * k); rows that dest does not name are not written.
+    dy_dtype: default dout's."""
+    T, H, dev = _matrix("dout", dout)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return combine_backward(dout, y_perm, dest, topk_w, y_scale=y_scale, R=R, dy_dtype=dy_dtype, need=need, dy=dy)
+    if not set(need) <= {"dy", "dw"}:
+        raise ValueError(f"need: {need}")
+    if topk_w.dim() != 2:
+        raise ValueError(f"topk_w has shape {tuple(topk_w.shape)}, expected [T][k]")
+    k = topk_w.shape[1]
+    f32 = (torch.float32,)
+    _tensor(dev, "topk_w", topk_w, (T, k), f32)
+    if _slots("combine_backward", dest, k, dev) != T:
+        raise ValueError(f"combine_backward: dest of {dest.numel()} values with T={T}, k={k}")
+    if R is None:
+        R = y_perm.shape[0] if y_perm is not None else dy.shape[0] if dy is not None else T * k
+    if not 0 <= R <= _MOST:
+        raise ValueError(f"combine_backward: R={R}")
+    y_dt = F32
+    want_dw = "dw" in need
+    if y_perm is not None:
+        fp8 = _is_fp8(y_perm.dtype)
+        _tensor(dev, "y_perm", y_perm, (R, H), (y_perm.dtype,) if fp8 else _FLOATS)
+        if fp8 != (y_scale is not None):
+            raise ValueError("combine_backward: y_scale goes with e4m3 y_perm")
+        _tensor(dev, "y_scale", y_scale, (R, H // 128), f32)
+        y_dt = E4M3 if fp8 else _CODE[y_perm.dtype]
+    elif want_dw:
+        raise ValueError("combine_backward: dw without y_perm")
+    dy_dtype = _out_dtype("dy", dy, dy_dtype, dout.dtype)
+    if dy_dtype not in _FLOATS:
+        raise TypeError(f"combine_backward: dy {dy_dtype}")
+    _tensor(dev, "dout", dout, (T, H), _FLOATS)
+    _tensor(dev, "dy", dy, (R, H), (dy_dtype,))
+    if "dy" not in need:
+        dy = None
+    elif dy is None:
+        dy = _empty(dout, (R, H), dy_dtype)
+    dw = _empty(topk_w, (T, k), torch.float32) if want_dw else None
+    L = _lib or lib()
+    _check(L.moe_combine_backward(dout.data_ptr(), _CODE[dout.dtype], _ptr(y_perm), y_dt, _ptr(y_scale), R, dest.data_ptr(),
+                                  topk_w.data_ptr(), T, k, H, _ptr(dy), _CODE[dy_dtype], _ptr(dw), _current(dev)))
+    return dy, dw

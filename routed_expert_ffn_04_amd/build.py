@@ -17,7 +17,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["route.hip", "permute.hip", "quant.hip", "combine.hip", "gffn.hip", "gffn_tile.hip",
            "gffn_stream.hip", "gffn_mid.hip", "gffn_big.hip", "gffn_mx.hip", "gffn_mxbig.hip", "noalloc.hip", "api.cpp",
-           "ffn.hip", "norm.hip", "norm_grad.hip", "linear_i8.hip", "dense_api.cpp"]
+           "ffn.hip", "norm.hip", "norm_grad.hip", "linear_i8.hip", "dense_api.cpp",
+           "experts.hip", "dispatch.hip", "ckpt.hip", "train_api.cpp"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

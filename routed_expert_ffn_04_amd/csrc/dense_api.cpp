@@ -7,50 +7,13 @@
 
 #include <cmath>
 
+#include "api_check.h"
 #include "dense.h"
 #include "internal.h"
 
 namespace {
 
-using moe::set_error;
-
-template <class... A>
-moe_status_t fail(moe_status_t st, const char* fmt, A... a) {
-    return (moe_status_t)set_error(st, fmt, a...);
-}
-
-moe_status_t done(hipError_t e, const char* what) {
-    if (e != hipSuccess) return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-    return (moe_status_t)set_error(MOE_OK, "%s", "");
-}
-
-bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
-bool is_float(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
-unsigned size_of(int dt) { return dt == MOE_F32 ? 4 : 2; }
-
-constexpr int kMaxFfn = 1 << 21;    // a tile's 256 rows of 2 I bf16 stay below 2^31 bytes
-constexpr int kMaxRows = 1 << 30;   // rows and tiles are counted in 32 bits
-
-// The bank of the dense block: n = 1, bf16, H and I multiples of 8.
-moe_status_t check_dense(const moe_experts_t* b, const char* name) {
-    if (!b) return fail(MOE_ERR_INVALID, "%s: null bank", name);
-    if (b->n != 1) return fail(MOE_ERR_INVALID, "%s: n = %d, expected 1", name, b->n);
-    if (b->dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: weight dtype %d", name, b->dt);
-    if (b->H <= 0 || b->I <= 0) return fail(MOE_ERR_INVALID, "%s: H=%d I=%d", name, b->H, b->I);
-    if (b->H % 8 || b->I % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d I=%d must be multiples of 8", name, b->H, b->I);
-    if (b->H > kMaxFfn || b->I > kMaxFfn)
-        return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d I=%d > %d", name, b->H, b->I, kMaxFfn);
-    if (!b->w_gate || !b->w_up || !b->w_down) return fail(MOE_ERR_INVALID, "%s: null weight pointer", name);
-    if (!aligned(b->w_gate, 16) || !aligned(b->w_up, 16) || !aligned(b->w_down, 16))
-        return fail(MOE_ERR_INVALID, "%s: weights must be 16-byte aligned", name);
-    return MOE_OK;
-}
-
-bool dense_sizes(int T, int H, int I) {
-    return T >= 0 && T <= kMaxRows && H > 0 && I > 0 && H % 8 == 0 && I % 8 == 0 && H <= kMaxFfn && I <= kMaxFfn;
-}
-
-size_t or_zero(size_t bytes) { return bytes == moe::kUnfit ? 0 : bytes; }
+using namespace moe::api;
 
 constexpr int kMaxNormH = 16384;
 constexpr int kMaxI8K = 131071;   // 128 * 128 * K stays below 2^31

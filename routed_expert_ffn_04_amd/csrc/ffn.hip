@@ -46,10 +46,11 @@ struct Forward {
     Plan gateup, down;
     size_t h, part, total;   // workspace
 };
-Plan gateup_plan(int T, int H, int I) { return plan_tiles(T, 2L * I, H, kKE, true); }
-Forward forward(int T, int H, int I) {
+Plan gateup_plan(int T, int H, int I, bool tiles) { return plan_tiles(T, 2L * I, H, kKE, !tiles); }
+// tiles: not the kernel for a few rows, whose waves hold eight gate columns, half of an i8x16 block
+Forward forward(int T, int H, int I, bool tiles) {
     Forward f;
-    f.gateup = gateup_plan(T, H, I);
+    f.gateup = gateup_plan(T, H, I, tiles);
     f.down = plan_tiles(T, H, I, kKE, true);
     f.h = 0;
     f.part = align256((size_t)T * I * 2);
@@ -63,11 +64,11 @@ int turn_of(int I) { return (I + kKE - 1) / kKE * kKE; }
 
 struct Backward {
     Plan gateup, dh, dx, dwgu, dw1, dwd;   // dw1: one of the gate and up gradients alone
-    size_t gu, dgu, h, part, total;
+    size_t gu, dgu, h, x, part, total;
 };
-Backward backward(int T, int H, int I, bool has_gu) {
+Backward backward(int T, int H, int I, bool has_gu, bool x_i8) {
     Backward w;
-    w.gateup = gateup_plan(T, H, I);
+    w.gateup = gateup_plan(T, H, I, false);
     w.dh = plan_tiles(T, I, H, kKE, false);
     w.dx = plan_tiles(T, H, turn_of(I) + I, kKE, false);
     w.dwgu = plan_tiles(2L * I, H, T, kKE, false);
@@ -80,6 +81,8 @@ Backward backward(int T, int H, int I, bool has_gu) {
     o += align256((size_t)T * I * 4);
     w.h = o;
     o += align256((size_t)T * I * 2);
+    w.x = o;
+    o += x_i8 ? align256((size_t)T * H * 2) : 0;
     w.part = o;
     size_t most = max2(part_bytes(w.dh, T, I), part_bytes(w.dx, T, H));
     most = max2(most, max2(part_bytes(w.dwgu, 2L * I, H), part_bytes(w.dw1, I, H)));
@@ -98,6 +101,17 @@ hipError_t gateup(const FfnProblem& p, const Plan& plan, void* h, float* gu, flo
     G.out = h;
     G.out2 = gu;
     return run<kBf16, kRow, kRow, kEpiGateUp>(G, plan, part, s);
+}
+
+// The same, g and u kept as i8x16 blocks.
+hipError_t gateup8(const FfnProblem& p, const Plan& plan, void* h, float* part, hipStream_t s) {
+    Args G = base(p.T, p.I, p.H);
+    G.A = rows(p.x, p.H, p.T);
+    G.B = rows(p.wg, p.H, p.I, p.wu);
+    G.out = h;
+    G.q = p.gu8;
+    G.qe = p.gu8_e;
+    return run<kBf16, kRow, kRow, kEpiGateUp8>(G, plan, part, s);
 }
 
 // The last products of the backward pass, which do not depend on each other:
@@ -167,26 +181,28 @@ hipError_t launch_products(Product* todo, int n, float* part, hipStream_t s) {
     return e;
 }
 
-// A matrix of zeros (the weight gradients of no tokens): M and N are multiples of 8.
 __global__ __launch_bounds__(256) void zero_kernel(uint4* out, size_t n) {
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) out[i] = uint4{0, 0, 0, 0};
-}
-hipError_t zero_rows(void* out, int M, int N, hipStream_t s) {
-    const size_t n = (size_t)M * N / 8;
-    zero_kernel<<<dim3((unsigned)std::min((n + 255) / 256, (size_t)4096)), dim3(256), 0, s>>>((uint4*)out, n);
-    return hipGetLastError();
 }
 
 }  // namespace
 
-size_t ffn_ws_bytes(int T, int H, int I) { return T > 0 ? forward(T, H, I).total : 0; }
-size_t ffn_backward_ws_bytes(int T, int H, int I, int has_gu) { return T > 0 ? backward(T, H, I, has_gu != 0).total : 0; }
+hipError_t launch_zero_bf16(void* out, size_t values, hipStream_t s) {
+    const size_t n = values / 8;
+    zero_kernel<<<dim3((unsigned)std::min((n + 255) / 256, (size_t)4096)), dim3(256), 0, s>>>((uint4*)out, n);
+    return hipGetLastError();
+}
+
+size_t ffn_ws_bytes(int T, int H, int I, int gu8) { return T > 0 ? forward(T, H, I, gu8 != 0).total : 0; }
+size_t ffn_backward_ws_bytes(int T, int H, int I, int has_gu, int x_i8) {
+    return T > 0 ? backward(T, H, I, has_gu != 0, x_i8 != 0).total : 0;
+}
 
 hipError_t launch_ffn(const FfnProblem& p, void* ws, hipStream_t s) {
-    const Forward w = forward(p.T, p.H, p.I);
+    const Forward w = forward(p.T, p.H, p.I, p.gu8 != nullptr);
     uint8_t* b = (uint8_t*)ws;
     float* part = (float*)(b + w.part);
-    hipError_t e = gateup(p, w.gateup, b + w.h, p.gu, part, s);
+    hipError_t e = p.gu8 ? gateup8(p, w.gateup, b + w.h, part, s) : gateup(p, w.gateup, b + w.h, p.gu, part, s);
     if (e != hipSuccess) return e;
     Args G = base(p.T, p.H, p.I);
     G.A = rows(b + w.h, p.I, p.T);
@@ -196,22 +212,30 @@ hipError_t launch_ffn(const FfnProblem& p, void* ws, hipStream_t s) {
     return run<kBf16, kRow, kRow, kEpiOut>(G, w.down, part, s);
 }
 
-hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
+hipError_t launch_ffn_backward(const FfnProblem& q, void* ws, hipStream_t s) {
+    FfnProblem p = q;
     hipError_t e = hipSuccess;
     if (p.T == 0) {
-        if (p.dwg) e = zero_rows(p.dwg, p.I, p.H, s);
-        if (e == hipSuccess && p.dwu) e = zero_rows(p.dwu, p.I, p.H, s);
-        if (e == hipSuccess && p.dwd) e = zero_rows(p.dwd, p.H, p.I, s);
+        const size_t n = (size_t)p.I * p.H;
+        if (p.dwg) e = launch_zero_bf16(p.dwg, n, s);
+        if (e == hipSuccess && p.dwu) e = launch_zero_bf16(p.dwu, n, s);
+        if (e == hipSuccess && p.dwd) e = launch_zero_bf16(p.dwd, n, s);
         return e;
     }
     const int T = p.T, H = p.H, I = p.I;
-    const Backward w = backward(T, H, I, p.gu_in != nullptr);
+    const bool has_gu = p.gu_in || p.gu8;
+    const Backward w = backward(T, H, I, has_gu, p.x_e != nullptr);
     uint8_t* b = (uint8_t*)ws;
     float* part = (float*)(b + w.part);
     uint8_t* dgu = b + w.dgu;
     uint8_t* h = b + w.h;
     const float* gu = p.gu_in;
-    if (!gu) {
+    if (p.x_e && (!has_gu || p.dwg || p.dwu)) {
+        e = launch_dequant_i8x16((const int8_t*)p.x, p.x_e, T, H, b + w.x, 0, s);
+        if (e != hipSuccess) return e;
+        p.x = b + w.x;
+    }
+    if (!has_gu) {
         gu = (const float*)(b + w.gu);
         e = gateup(p, w.gateup, h, (float*)(b + w.gu), part, s);
         if (e != hipSuccess) return e;
@@ -221,9 +245,11 @@ hipError_t launch_ffn_backward(const FfnProblem& p, void* ws, hipStream_t s) {
         G.A = rows(p.dy, H, T);
         G.B = cols(p.wd, I, I);
         G.gu = gu;
+        G.q = p.gu8;
+        G.qe = p.gu8_e;
         G.out = dgu;
         G.out2 = h;
-        e = run<kBf16, kRow, kCol, kEpiGrad>(G, w.dh, part, s);
+        e = p.gu8 ? run<kBf16, kRow, kCol, kEpiGrad8>(G, w.dh, part, s) : run<kBf16, kRow, kCol, kEpiGrad>(G, w.dh, part, s);
     }
     if (e != hipSuccess) return e;
     // the products that are wanted: dx, the gate and up gradients (both at once, or

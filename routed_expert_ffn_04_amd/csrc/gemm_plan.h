@@ -17,11 +17,12 @@ inline size_t part_bytes(const Plan& p, long M, long cols) { return p.splits > 1
 // thread takes eight consecutive columns of one row.
 template <int EPI>
 __global__ __launch_bounds__(256) void reduce_kernel(Args G, const float* __restrict__ part, int splits) {
-    const int groups = (G.N + 7) / 8;
+    // kEpiGateUp8: whole blocks of 16 columns, whose halves meet in neighbouring lanes
+    const int groups = EPI == kEpiGateUp8 ? 2 * i8x16_blocks(G.N) : (G.N + 7) / 8;
     const long at = (long)blockIdx.x * 256 + threadIdx.x;
     if (at >= (long)G.M * groups) return;
     const int m = (int)(at / groups), n = (int)(at % groups) * 8;
-    constexpr bool GU = EPI == kEpiGateUp;
+    constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
     const size_t cols = GU ? 2 * (size_t)G.N : (size_t)G.N;
     const size_t plane = (size_t)G.M * cols;
     const float* p = part + (size_t)m * cols + n;
@@ -58,13 +59,17 @@ __global__ __launch_bounds__(256) void reduce_kernel(Args G, const float* __rest
     };
     float v[8];
     total(p, v);
-    if constexpr (EPI == kEpiGateUp) {
+    if constexpr (GU) {
         float u[8], h[8];
         total(p + G.N, u);
+        if constexpr (EPI == kEpiGateUp8) {
+            store_gu8(G, m, n, v, u);
+            if (n >= G.N) return;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = silu_mul(v[e], u[e]);
         *(uint4*)((uint16_t*)G.out + (size_t)m * G.N + n) = pack8(h);
-        if (G.out2) {
+        if (EPI == kEpiGateUp && G.out2) {
             float* o = (float*)G.out2 + (size_t)m * cols + n;
             *(float4*)o = make_float4(v[0], v[1], v[2], v[3]);
             *(float4*)(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -72,11 +77,18 @@ __global__ __launch_bounds__(256) void reduce_kernel(Args G, const float* __rest
             *(float4*)o = make_float4(u[0], u[1], u[2], u[3]);
             *(float4*)(o + 4) = make_float4(u[4], u[5], u[6], u[7]);
         }
-    } else if constexpr (EPI == kEpiGrad) {
+    } else if constexpr (EPI == kEpiGrad || EPI == kEpiGrad8) {
         float g[8], u[8], dg[8], du[8], h[8];
-        const float* gp = G.gu + (size_t)m * (2 * (size_t)G.N) + n;
-        load(gp, g);
-        load(gp + G.N, u);
+        if constexpr (EPI == kEpiGrad8) {
+            const size_t nb = (size_t)i8x16_blocks(G.N), at8 = (size_t)m * (2 * (size_t)G.N) + n;
+            const uint8_t* e = G.qe + (size_t)m * (2 * nb) + n / kI8Block;
+            i8x16_values(*(const uint2*)(G.q + at8), e[0], g);
+            i8x16_values(*(const uint2*)(G.q + at8 + G.N), e[nb], u);
+        } else {
+            const float* gp = G.gu + (size_t)m * (2 * (size_t)G.N) + n;
+            load(gp, g);
+            load(gp + G.N, u);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) swiglu_grad(g[e], u[e], v[e], dg[e], du[e], h[e]);
         uint16_t* d = (uint16_t*)G.out + (size_t)m * (2 * (size_t)G.N) + n;
@@ -102,7 +114,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(Args G, const float* __rest
 
 template <int EPI>
 hipError_t launch_reduce(const Args& G, const float* part, int splits, hipStream_t s) {
-    const long threads = (long)G.M * ((G.N + 7) / 8);
+    const long threads = (long)G.M * (EPI == kEpiGateUp8 ? 2 * i8x16_blocks(G.N) : (G.N + 7) / 8);
     const long blocks = (threads + 255) / 256;
     if (blocks == 0) return hipSuccess;
     if (!grid_fits(blocks, 256)) return hipErrorInvalidValue;
@@ -128,10 +140,10 @@ hipError_t launch_tiling(const Args& G, const Plan& p, hipStream_t s) {
 // into `part` and a second launch that joins them.
 template <int E, int LA, int LB, int EPI>
 hipError_t run(Args G, const Plan& p, float* part, hipStream_t s) {
-    constexpr bool GU = EPI == kEpiGateUp;
+    constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
     G.splits = p.splits;
     G.kspan = p.kspan;
-    if constexpr (LA == kRow && LB == kRow) {
+    if constexpr (LA == kRow && LB == kRow && EPI != kEpiGateUp8) {
         if (p.few) return launch_few<E, EPI>(G, s);
     }
     Args P = G;

@@ -45,6 +45,7 @@
 #pragma once
 #include "common.h"
 #include "gffn_common.h"
+#include "i8x16.h"
 #include "tile_plan.h"
 
 namespace moe {
@@ -65,6 +66,8 @@ enum Epi {
     kEpiGrad = 2,      // acc = dh; with the saved g, u: dg, du (bf16 [M][2 N]) and h (bf16 [M][N])
     kEpiPart = 3,      // 32-bit accumulators of one k-split, [split][M][N] (gate/up: [split][M][2 I])
     kEpiI8 = 4,        // acc * x_scale[m] * w_scale[n] + bias[n], bf16 or fp32
+    kEpiGateUp8 = 5,   // kEpiGateUp with g and u as blocks of 16 columns (i8x16.h): codes in q, exponents in qe
+    kEpiGrad8 = 6,     // kEpiGrad with g and u from such blocks
 };
 
 constexpr uint32_t kFar = 1u << 31;   // past every byte of a tile: 256 rows of at most 2^23 bytes
@@ -89,6 +92,8 @@ struct Args {
     int msplit;
     int out_f32;
     const float* gu;     // kEpiGrad: saved pre-activations [M][2 N]
+    int8_t* q;           // kEpiGateUp8 (written), kEpiGrad8 (read): codes [M][2 N]
+    uint8_t* qe;         // and exponents [M][2 ceil(N / 16)]
     const float* xs; const float* ws; const float* bias;   // kEpiI8
 };
 
@@ -189,6 +194,30 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float& d
     h = a * u;
 }
 
+// The gate and up columns n .. n + 7 of row m as i8x16 blocks: the lane and its
+// neighbour (lane ^ 1: the columns before or after) hold the two halves of a block.
+// Called by both, also past the end (values there count as zeros, nothing is stored).
+__device__ __forceinline__ void store_gu8(const Args& G, int m, int n, const float (&g)[8], const float (&u)[8]) {
+    const bool in = n < G.N;
+    float gv[8], uv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        gv[e] = in ? g[e] : 0.0f;
+        uv[e] = in ? u[e] : 0.0f;
+    }
+    const uint32_t ge = i8x16_exponent(i8x16_pair_max(gv)), ue = i8x16_exponent(i8x16_pair_max(uv));
+    if (m >= G.M || !in) return;
+    const size_t nb = (size_t)i8x16_blocks(G.N);
+    int8_t* q = G.q + (size_t)m * (2 * (size_t)G.N) + n;
+    *(uint2*)q = i8x16_codes(gv, ge);
+    *(uint2*)(q + G.N) = i8x16_codes(uv, ue);
+    if (n % kI8Block == 0) {
+        uint8_t* e = G.qe + (size_t)m * (2 * nb) + n / kI8Block;
+        e[0] = (uint8_t)ge;
+        e[nb] = (uint8_t)ue;
+    }
+}
+
 // Eight consecutive outputs (m, n .. n + 7) of a kEpiOut / kEpiI8 / kEpiPart matrix.
 __device__ __forceinline__ void store8(const Args& G, uint8_t* row, int n, const float (&v)[8], bool f32) {
     if (G.vec && n + 8 <= G.N) {
@@ -213,6 +242,14 @@ __device__ __forceinline__ void store8(const Args& G, uint8_t* row, int n, const
 // each die with an L2 of its own: every die takes one contiguous run of tiles,
 // ordered in bands of 8 m-tiles with n outermost, so the 32 tiles that a die
 // works on together form a block of about 8 x 4 and share their operands in L2.
+// Tile t of the bands:
+__device__ __forceinline__ void band_of(int t, int mt, int nt, int& tm, int& tn) {
+    const int band = t / (8 * nt);
+    const int rows = min(8, mt - band * 8);
+    t -= band * 8 * nt;
+    tn = t / rows;
+    tm = band * 8 + t % rows;
+}
 __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& tm, int& tn, int& split) {
     const int x = b % kXcds, j = b / kXcds;
     const int base = total / kXcds, extra = total % kXcds;
@@ -220,20 +257,16 @@ __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& t
     const int per = mt * nt;
     split = t / per;
     t -= split * per;
-    const int band = t / (8 * nt);
-    const int rows = min(8, mt - band * 8);
-    t -= band * 8 * nt;
-    tn = t / rows;
-    tm = band * 8 + t % rows;
+    band_of(t, mt, nt, tm, tn);
 }
 
 // Launch shape of the tiles: LDS, and waves per SIMD by it.
 constexpr int tile_lds(int edge, int ring) { return ring * edge * kStage; }
 constexpr int tile_waves(int edge, int ring) { return edge == 256 ? 2 : 163840 / tile_lds(edge, ring); }   // per SIMD
 
-// Workgroup `block` of the `blocks` that share out the tiles and splits of G.
+// Tile (tm, tn) of the k-split `split` of G.
 template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
-__device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
+__device__ __forceinline__ void tile_at(const Args& G, int tm, int tn, int split) {
     constexpr int kThreads = tile_threads(BM);
     constexpr int EB = E == kI8 ? 1 : 2;
     constexpr int KE = kStage / EB;                            // k elements per stage
@@ -251,8 +284,6 @@ __device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
     const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int wm = wave / WN, wn = wave % WN;
 
-    int tm, tn, split;
-    tile_of(block, G.mt, G.nt, blocks, tm, tn, split);
     const int m0 = tm * BM, n0 = tn * kTileN;
     const int k0 = split * G.kspan;
     const int kn = min(G.K - k0, G.kspan);                     // k elements of this split
@@ -533,6 +564,20 @@ __device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
         if (mb >= G.M) break;
         // the saved pre-activations of the 32 rows, read while the accumulators pass through LDS
         float4 gv[kPass][2], uv[kPass][2];
+        uint2 gq[kPass], uq[kPass];
+        uint32_t ge[kPass], ue[kPass];
+        if constexpr (EPI == kEpiGrad8) {
+            const size_t nb = (size_t)i8x16_blocks(G.N);
+#pragma unroll
+            for (int p = 0; p < kPass; ++p) {
+                const size_t m = (size_t)min(mb + p * RP + lane / RL, G.M - 1);
+                const int n = min(nl, G.N - 8);
+                gq[p] = *(const uint2*)(G.q + m * (2 * (size_t)G.N) + n);
+                uq[p] = *(const uint2*)(G.q + m * (2 * (size_t)G.N) + G.N + n);
+                ge[p] = G.qe[m * (2 * nb) + n / kI8Block];
+                ue[p] = G.qe[m * (2 * nb) + nb + n / kI8Block];
+            }
+        }
         if constexpr (EPI == kEpiGrad) {
 #pragma unroll
             for (int p = 0; p < kPass; ++p) {
@@ -565,6 +610,7 @@ __device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
                 float g[8], u[8], h[8];
                 words(row, c, g);
                 words(row, WC / 2 + c, u);
+                if constexpr (EPI == kEpiGateUp8) store_gu8(G, m, n, g, u);
                 if (m < G.M && n < G.N) {
                     if constexpr (EPI == kEpiPart) {
                         float* o = (float*)G.out + ((size_t)split * G.M + m) * (2 * (size_t)G.N) + n;
@@ -577,7 +623,7 @@ __device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) h[e] = silu_mul(g[e], u[e]);
                         *(uint4*)((uint16_t*)G.out + (size_t)m * G.N + n) = pack8(h);
-                        if (G.out2) {
+                        if (EPI == kEpiGateUp && G.out2) {
                             float* o = (float*)G.out2 + (size_t)m * (2 * (size_t)G.N) + n;
                             *(float4*)o = make_float4(g[0], g[1], g[2], g[3]);
                             *(float4*)(o + 4) = make_float4(g[4], g[5], g[6], g[7]);
@@ -596,11 +642,16 @@ __device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
                 float v[8];
                 words(row, c, v);
                 if (m < G.M && n < G.N) {
-                    if constexpr (EPI == kEpiGrad) {
-                        const float4 ga = gv[p][0], gb = gv[p][1], ua = uv[p][0], ub = uv[p][1];
-                        const float g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
-                        const float u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
-                        float dg[8], du[8], h[8];
+                    if constexpr (EPI == kEpiGrad || EPI == kEpiGrad8) {
+                        float g[8], u[8], dg[8], du[8], h[8];
+                        if constexpr (EPI == kEpiGrad8) {
+                            i8x16_values(gq[p], ge[p], g);
+                            i8x16_values(uq[p], ue[p], u);
+                        } else {
+                            const float4 ga = gv[p][0], gb = gv[p][1], ua = uv[p][0], ub = uv[p][1];
+                            g[0] = ga.x; g[1] = ga.y; g[2] = ga.z; g[3] = ga.w; g[4] = gb.x; g[5] = gb.y; g[6] = gb.z; g[7] = gb.w;
+                            u[0] = ua.x; u[1] = ua.y; u[2] = ua.z; u[3] = ua.w; u[4] = ub.x; u[5] = ub.y; u[6] = ub.z; u[7] = ub.w;
+                        }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) swiglu_grad(g[e], u[e], v[e], dg[e], du[e], h[e]);
                         uint16_t* d = (uint16_t*)G.out + (size_t)m * (2 * (size_t)G.N) + n;
@@ -626,6 +677,14 @@ __device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
             }
         }
     }
+}
+
+// Workgroup `block` of the `blocks` that share out the tiles and splits of G.
+template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
+__device__ __forceinline__ void tile(const Args& G, int block, int blocks) {
+    int tm, tn, split;
+    tile_of(block, G.mt, G.nt, blocks, tm, tn, split);
+    tile_at<E, LA, LB, EPI, GU, BM, BN, R>(G, tm, tn, split);
 }
 
 template <int E, int LA, int LB, int EPI, bool GU, int BM, int BN, int R>
