@@ -10,8 +10,10 @@
 // expert and tile by a prefix sum over the offsets, which its first wave-wide loads
 // bring: no list is made beforehand, and nothing about the rows has to reach the host.
 #include <algorithm>
+#include <cstdlib>
 
 #include "gemm_plan.h"
+#include "gemm_stream.h"
 
 namespace moe {
 using namespace gemm;
@@ -29,8 +31,6 @@ struct Grouped {
     int n, R;              // experts; rows there are
     int nt;                // kRows: column tiles; kSum: tiles of an expert
 };
-
-__device__ __forceinline__ int rows_before(const int32_t* offsets, int e, int R) { return min(max(offsets[e], 0), R); }
 
 // Position in the order of `total` tiles, of which every die takes one contiguous
 // run, of workgroup `block`; -1 past them.
@@ -108,6 +108,18 @@ __device__ __forceinline__ Args rows_of(const Grouped& P, const Place& at) {
     return G;
 }
 
+// Workgroups of weight gradients of `nt` tiles an expert.  The dies share out every
+// expert's tiles, so that none has the long experts for itself.
+__host__ __device__ __forceinline__ int die_share(int nt) { return (nt + kXcds - 1) / kXcds; }
+__device__ __forceinline__ bool find_sum(int nt, int block, int& e, int& t) {
+    const int per = die_share(nt);
+    e = block / kXcds / per;
+    const int x = (block + e) % kXcds, j = block / kXcds % per;   // the dies with a tile more take turns
+    const int base = nt / kXcds, extra = nt % kXcds;
+    t = x * base + min(x, extra) + j;
+    return j < base + (x < extra ? 1 : 0);
+}
+
 // Weight gradient of expert e, its tile t.
 __device__ __forceinline__ Args sum_of(const Grouped& P, int e, int t, int& tm, int& tn) {
     Args G = P.G;
@@ -147,9 +159,9 @@ __global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per
     const Grouped& P = Q.P[i];
     int tm, tn;
     if (Q.sum[i]) {
-        const int t = in_die_order(b - Q.first[i], P.n * P.nt);
-        if (t < 0) return;
-        const Args G = sum_of(P, t / P.nt, t % P.nt, tm, tn);
+        int e, t;
+        if (!find_sum(P.nt, b - Q.first[i], e, t)) return;
+        const Args G = sum_of(P, e, t, tm, tn);
         tile_at<kBf16, kCol, kCol, kEpiOut, false, EDGE, EDGE, 5>(G, tm, tn, 0);
     } else {
         Place at;
@@ -159,6 +171,8 @@ __global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per
         tile_at<kBf16, kRow, kCol, kEpiOut, false, EDGE, EDGE, 5>(G, tm, tn, 0);
     }
 }
+
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void stream_kernel(Stream S) { stream(S); }
 
 // ---------------------------------------------------------------- host
 
@@ -274,7 +288,7 @@ int together_edge(const Products& Q, int m, int R, int n) {
             const double mt = Q.sum[i] ? (G.M + edge - 1) / edge : (each + edge - 1) / edge;
             const double span = ((Q.sum[i] ? each : G.K) + kKE - 1) / kKE;
             const double tiles = (Q.sum[i] ? n : used) * mt * nt;
-            all += Q.sum[i] ? tiles : rows_grid(R, n, edge, (int)nt);
+            all += Q.sum[i] ? tiles + (double)n * kXcds : rows_grid(R, n, edge, (int)nt);
             work += tiles * (span * t.stage + t.tile) / 256;
             longest = std::max(longest, span);
         }
@@ -298,8 +312,7 @@ hipError_t launch_products(Products Q, int m, hipStream_t s) {
             P.G.mt = (P.G.M + EDGE - 1) / EDGE;
             P.G.nt = (P.G.N + EDGE - 1) / EDGE;
             P.nt = P.G.mt * P.G.nt;
-            total += (long)P.n * P.nt;
-            total = (total + kXcds - 1) / kXcds * kXcds;   // the next product begins on the first die
+            total += (long)P.n * die_share(P.nt) * kXcds;
         } else {
             P.nt = (P.G.N + EDGE - 1) / EDGE;
             total += rows_grid(P.R, P.n, EDGE, P.nt);
@@ -311,6 +324,37 @@ hipError_t launch_products(Products Q, int m, hipStream_t s) {
     static DeviceCache ready;
     if (!allow_lds(ready, k, tile_lds(EDGE, 5))) return hipErrorInvalidValue;
     k<<<dim3((unsigned)total), dim3(tile_threads(EDGE)), tile_lds(EDGE, 5), s>>>(Q);
+    return hipGetLastError();
+}
+
+hipError_t launch_stream(const Products& Q, int m, hipStream_t s) {
+    Stream S{};
+    S.offsets = Q.P[0].offsets;
+    S.n = Q.P[0].n;
+    S.R = Q.P[0].R;
+    long total = 0;
+    for (int i = 0; i < m; ++i) {
+        const Grouped& P = Q.P[i];
+        const Args& G = P.G;
+        SumProduct& D = S.P[i];
+        D.A = G.A.p; D.B = G.B.p;
+        D.lda = (uint32_t)G.A.ld; D.ldb = (uint32_t)G.B.ld;
+        D.M = G.out2 ? G.msplit : G.M; D.N = G.N;
+        D.half = (D.M + kStreamM - 1) / kStreamM;
+        D.mt = G.out2 ? 2 * D.half : D.half;
+        D.nt = (D.N + kStreamN - 1) / kStreamN;
+        D.skip = (uint32_t)G.msplit * 2;
+        D.out = (uint8_t*)G.out; D.out2 = (uint8_t*)G.out2;
+        D.step = P.wstep;
+        D.per = die_share(D.mt * D.nt);
+        total += (long)S.n * D.per;
+        if (i == 0) S.first = (int)total;
+    }
+    S.total = (int)total;
+    const int grid = std::max(device_cu_count() / kXcds, 1) * kXcds;
+    static DeviceCache ready;
+    if (!allow_lds(ready, stream_kernel, kStreamLds)) return hipErrorInvalidValue;
+    stream_kernel<<<dim3(grid), dim3(512), kStreamLds, s>>>(S);
     return hipGetLastError();
 }
 
@@ -337,7 +381,7 @@ bool fits(int R, int n, int H, int I, bool grads) {
     if (!rows_edge(R, n, I, H)) return false;
     // the largest tiles take the fewest workgroups
     const auto tiles = [](long v) { return (v + 255) / 256; };
-    const double all = (double)rows_grid(R, n, 256, (int)tiles(H)) + (double)n * (tiles(2L * I) + tiles(I)) * tiles(H) + 3 * kXcds;
+    const double all = (double)rows_grid(R, n, 256, (int)tiles(H)) + (double)n * ((tiles(2L * I) + tiles(I)) * tiles(H) + 2 * kXcds);
     return all < 4e9 && grid_fits((long)all, tile_threads(256));
 }
 
@@ -434,7 +478,18 @@ hipError_t launch_experts_backward(const ExpertsProblem& p, void* ws, hipStream_
     }
     if (p.dwd) weight(rows(p.dy, H, H), rows(h, I, I), H, I, p.dwd, nullptr, H);
     if (m == 0) return hipSuccess;
-    switch (together_edge(Q, m, R, p.n)) {
+    if (getenv("MOE_STREAM")) {
+        int first = 0;
+        if (!Q.sum[0]) {
+            e = launch_rows<kCol, kEpiOut>(Q.P[0], s);
+            first = 1;
+        }
+        Products Z{};
+        for (int i = first; i < m; ++i) Z.P[i - first] = Q.P[i];
+        if (e == hipSuccess && m > first) e = launch_stream(Z, m - first, s);
+        return e;
+    }
+    switch (getenv("MOE_EDGE") ? atoi(getenv("MOE_EDGE")) : together_edge(Q, m, R, p.n)) {
         case 64: return launch_products<64>(Q, m, s);
         case 128: return launch_products<128>(Q, m, s);
         case 256: return launch_products<256>(Q, m, s);
