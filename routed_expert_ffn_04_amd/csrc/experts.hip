@@ -10,7 +10,6 @@
 // expert and tile by a prefix sum over the offsets, which its first wave-wide loads
 // bring: no list is made beforehand, and nothing about the rows has to reach the host.
 #include <algorithm>
-#include <cstdlib>
 
 #include "gemm_plan.h"
 #include "gemm_stream.h"
@@ -327,14 +326,25 @@ hipError_t launch_products(Products Q, int m, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_stream(const Products& Q, int m, hipStream_t s) {
+// The weight gradients as a stream of 256 x 256 tiles: where these give every CU one.
+// (With fewer, smaller tiles in one launch with dx.)
+long stream_tiles(const Grouped* P, int m) {
+    long tiles = 0;
+    for (int i = 0; i < m; ++i) {
+        const Args& G = P[i].G;
+        tiles += (long)P[i].n * ((G.M + kStreamM - 1) / kStreamM) * ((G.N + kStreamN - 1) / kStreamN);
+    }
+    return tiles;
+}
+
+hipError_t launch_stream(const Grouped* todo, int m, hipStream_t s) {
     Stream S{};
-    S.offsets = Q.P[0].offsets;
-    S.n = Q.P[0].n;
-    S.R = Q.P[0].R;
+    S.offsets = todo[0].offsets;
+    S.n = todo[0].n;
+    S.R = todo[0].R;
     long total = 0;
     for (int i = 0; i < m; ++i) {
-        const Grouped& P = Q.P[i];
+        const Grouped& P = todo[i];
         const Args& G = P.G;
         SumProduct& D = S.P[i];
         D.A = G.A.p; D.B = G.B.p;
@@ -348,6 +358,7 @@ hipError_t launch_stream(const Products& Q, int m, hipStream_t s) {
         D.step = P.wstep;
         D.per = die_share(D.mt * D.nt);
         total += (long)S.n * D.per;
+        if (total > 0x7fffffffL) return hipErrorInvalidValue;
         if (i == 0) S.first = (int)total;
     }
     S.total = (int)total;
@@ -478,18 +489,12 @@ hipError_t launch_experts_backward(const ExpertsProblem& p, void* ws, hipStream_
     }
     if (p.dwd) weight(rows(p.dy, H, H), rows(h, I, I), H, I, p.dwd, nullptr, H);
     if (m == 0) return hipSuccess;
-    if (getenv("MOE_STREAM")) {
-        int first = 0;
-        if (!Q.sum[0]) {
-            e = launch_rows<kCol, kEpiOut>(Q.P[0], s);
-            first = 1;
-        }
-        Products Z{};
-        for (int i = first; i < m; ++i) Z.P[i - first] = Q.P[i];
-        if (e == hipSuccess && m > first) e = launch_stream(Z, m - first, s);
-        return e;
+    const int sums = p.dx ? 1 : 0;   // the weight gradients follow
+    if (m > sums && stream_tiles(&Q.P[sums], m - sums) >= device_cu_count()) {
+        if (p.dx) e = launch_rows<kCol, kEpiOut>(Q.P[0], s);
+        return e == hipSuccess ? launch_stream(&Q.P[sums], m - sums, s) : e;
     }
-    switch (getenv("MOE_EDGE") ? atoi(getenv("MOE_EDGE")) : together_edge(Q, m, R, p.n)) {
+    switch (together_edge(Q, m, R, p.n)) {
         case 64: return launch_products<64>(Q, m, s);
         case 128: return launch_products<128>(Q, m, s);
         case 256: return launch_products<256>(Q, m, s);

@@ -6,20 +6,19 @@
 // first and the last of these (256 x 256 outputs, 512 rows: 22 us, 12 of them
 // products; the outputs of all CUs at once take 6 us to HBM).  Here a workgroup takes
 // its tiles one after the other and its ring never drains: the loads of the next tile's first
-// stages go out while the last ones of this tile multiply.  Two workgroups a CU
-// with nothing in common but the CU fill each other's gaps.
+// stages go out while the last ones of this tile multiply.
 //
-// Tile.  256 x 128 outputs, 4 waves (2 x 2) of 128 x 64 (12 LDS reads for 32
-// products), stages of 32 rows (24 KiB), a ring of three, 72 KiB.  Rows of k are met
-// as they are stored, in pieces of 512 and 256 bytes, so short stages cost nothing
-// in the loads.
+// Tile.  256 x 256 outputs, 8 waves (2 x 4) of 128 x 64, stages of 32 rows (32 KiB), a
+// ring of four, and 4 KiB a wave for what leaves: all of LDS.  Rows of k are met as
+// they are stored, in pieces of 512 bytes, so short stages cost nothing in the loads.
+// (256 x 128 outputs and two workgroups a CU: more of the rows are read again from
+// HBM, 4.0 ms against 3.3 for 2048 rows an expert; 128 x 128: 1.4 to 1.6 times as long.)
 //
-// The accumulators leave between two parts of a stage, straight from registers: a lane
-// has four consecutive n of a row m; two 16-column blocks side by side, exchanged
-// between neighbouring rows of lanes (v_permlane16_swap), give it eight, and a store
-// 64-byte pieces of 16 rows.  Memory operations of a wave retire in the order of their
-// issue, and a stage's loads go out before the stores of the same turn, so the
-// stores of a tile have three stages to reach L2 before anything waits for them.
+// The accumulators leave between two parts of a stage: 16 rows at a time through LDS,
+// so that a store writes whole lines.  (64-byte pieces of 16 rows straight from registers
+// take the address unit 3.9 us a tile, lines 1.2.)  Memory operations of a wave
+// retire in the order of their issue, and a stage's loads go out before the stores of the same
+// turn, so the stores of a tile have three stages to reach L2 before anything waits.
 //
 // Each die takes an eighth of every expert's tiles (it would have the long experts for
 // itself otherwise), and its workgroups tiles next to each other.
