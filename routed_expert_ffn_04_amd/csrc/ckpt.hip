@@ -5,7 +5,7 @@
 #include "dense.h"
 #include "gffn_common.h"
 #include "i8x16.h"
-#include "row8.h"
+#include "row_io.h"
 
 namespace moe {
 
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void quant_kernel(const void* __restrict__ x, 
                                                     int8_t* __restrict__ q, uint8_t* __restrict__ e8) {
     const At a = place(rows, cols);
     float v[8] = {};
-    if (a.valid) load_row8<F32>(x, (size_t)a.row * cols + a.c, v);
+    if (a.valid) load_row<F32, 8>(x, (size_t)a.row * cols + a.c, v);
     const uint32_t E = i8x16_exponent(i8x16_pair_max(v));
     if (!a.valid) return;
     *(uint2*)(q + (size_t)a.row * cols + a.c) = i8x16_codes(v, E);
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__
     float v[8];
     i8x16_values(*(const uint2*)(q + (size_t)a.row * cols + a.c),
                  e8[(size_t)a.row * i8x16_blocks(cols) + a.c / kI8Block], v);
-    store_row8<F32>(out, (size_t)a.row * cols + a.c, v);
+    store_row<F32, 8>(out, (size_t)a.row * cols + a.c, v);
 }
 
 bool grid_of(long rows, int cols, dim3& grid) {

@@ -7,145 +7,178 @@
 // Memory-bound, no arithmetic to speak of.  Each runs over the tokens, so a token's row
 // is read once from HBM and every sorted row once (read or written): a kernel
 // that ran over the sorted rows instead would read the tokens' rows k times.
+//
+// Sorted rows are met once, and there are many more of them than the caches hold, so
+// they go past the caches' usual order (NT) where a row is whole lines: dispatch of 16384
+// tokens to 8 of 7168 columns in bf16 437 -> 355 us (5.9 TB/s), its gradient 420 -> 376.  Rows
+// of other lengths keep the usual one, which joins the pieces of a line (2056 columns:
+// 45 us, against 63).  Row numbers that are the same in a whole wave are read
+// through the scalar cache: the gradient took 532 us with vector loads of them.
 #include "dense.h"
 #include "gffn_common.h"
 #include "i8x16.h"
-#include "row8.h"
+#include "row_io.h"
 
 namespace moe {
 
 namespace {
 
-// ---- dispatch: a lane takes 16 bytes of a token's row (of the row as it is written) and stores them k times.
-// A workgroup takes 256 pieces of one token, or several tokens with shorter rows.
+// Pieces of a token's row: 16 bytes of what is written or summed.  Long rows (LONG): a
+// workgroup takes U * 256 pieces of one token, so that the token and with it its rows' numbers
+// are uniform.  Short ones: one piece a lane, several tokens a workgroup.
+template <bool LONG, int U>
 struct Piece {
-    long t;
-    int c;
-    bool valid;
-};
-__device__ __forceinline__ Piece piece_of(int T, int pieces, int slabs, int per) {
-    Piece p;
-    if (per == 1) {
-        const uint32_t b = blockIdx.x;
-        const uint32_t t = b / (uint32_t)slabs;
-        p.t = t;
-        p.c = (int)(b - t * slabs) * 256 + (int)threadIdx.x;
-        p.valid = p.c < pieces;
-    } else {
-        const int r = (int)threadIdx.x / pieces;
-        p.t = (long)blockIdx.x * per + r;
-        p.c = (int)threadIdx.x - r * pieces;
-        p.valid = r < per && p.t < T;
+    int t, c;
+    __device__ __forceinline__ Piece(int pieces, int slabs, int per) {
+        if constexpr (LONG) {
+            t = (int)(blockIdx.x / (uint32_t)slabs);
+            c = (int)(blockIdx.x - (uint32_t)t * slabs) * (U * 256) + (int)threadIdx.x;
+        } else {
+            const int r = (int)threadIdx.x / pieces;
+            t = r < per ? (int)(blockIdx.x * per + r) : 0x7fffffff;
+            c = (int)threadIdx.x - r * pieces;
+        }
     }
-    return p;
-}
+};
 
-enum { kCopy = 0, kFromI8 = 1 };
-
-template <int KIND>
+// ---- dispatch: a token's piece is read once and stored k times
+template <bool FROM_I8, bool LONG, int U, bool NT>
 __global__ __launch_bounds__(256) void dispatch_kernel(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xe,
                                                        int T, int pieces, int slabs, int per,
                                                        const int32_t* __restrict__ dest, int k, int R,
-                                                       uint4* __restrict__ xs) {
-    const Piece p = piece_of(T, pieces, slabs, per);
-    if (!p.valid) return;
-    uint4 v;
-    if constexpr (KIND == kFromI8) {
-        const int blocks = (pieces + 1) / 2;
-        float f[8];
-        i8x16_values(*(const uint2*)(x + ((size_t)p.t * pieces + p.c) * 8), xe[(size_t)p.t * blocks + p.c / 2], f);
-        v = make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
-                       f32x2_to_bf16x2(f[6], f[7]));
-    } else {
-        v = ((const uint4*)x)[(size_t)p.t * pieces + p.c];
+                                                       i32x4* __restrict__ xs) {
+    const Piece<LONG, U> p(pieces, slabs, per);
+    if (p.t >= T) return;
+    i32x4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = p.c + u * 256;
+        if (c >= pieces) continue;
+        if constexpr (FROM_I8) {
+            float f[8];
+            i8x16_values(*(const uint2*)(x + ((size_t)p.t * pieces + c) * 8), xe[(size_t)p.t * ((pieces + 1) / 2) + c / 2], f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[u][e] = (int)f32x2_to_bf16x2(f[2 * e], f[2 * e + 1]);
+        } else {
+            v[u] = ((const i32x4*)x)[(size_t)p.t * pieces + c];
+        }
     }
     const int32_t* d = dest + (size_t)p.t * k;
     for (int j = 0; j < k; ++j) {
         const int r = d[j];
-        if ((unsigned)r < (unsigned)R) xs[(size_t)r * pieces + p.c] = v;
+        if ((unsigned)r >= (unsigned)R) continue;
+        i32x4* row = xs + (size_t)r * pieces;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (p.c + u * 256 < pieces) put<NT>(row + p.c + u * 256, v[u]);
     }
 }
 
-// ---- gradient of dispatch: a lane takes eight columns of a token, the rows of up to eight experts in flight
+// ---- gradient of dispatch: the rows of up to eight experts in flight
 constexpr int kRows = 8;
 
-template <bool F32, bool ADD_F32, bool OUT_F32>
-__global__ __launch_bounds__(256) void gather_kernel(const void* __restrict__ dxs, const void* __restrict__ add, int T,
+template <bool F32, bool ADD_F32, bool OUT_F32, bool LONG, bool NT>
+__global__ __launch_bounds__(256) void gather_kernel(const void* __restrict__ dxs, const void* add, int T,
                                                      int pieces, int slabs, int per, const int32_t* __restrict__ dest,
-                                                     int k, int R, void* __restrict__ dx) {
-    const Piece p = piece_of(T, pieces, slabs, per);
-    if (!p.valid) return;
-    const size_t at = ((size_t)p.t * pieces + p.c) * 8;
-    float sum[8] = {};
-    if (add) load_row8<ADD_F32>(add, at, sum);
+                                                     int k, int R, void* dx) {   // dx may be add
+    constexpr int C = F32 ? 4 : 8;
+    const Piece<LONG, 1> p(pieces, slabs, per);
+    if (p.t >= T || p.c >= pieces) return;
+    const size_t at = ((size_t)p.t * pieces + p.c) * C;
+    float sum[C] = {};
+    if (add) load_row<ADD_F32, C>(add, at, sum);
     const int32_t* d = dest + (size_t)p.t * k;
     for (int j0 = 0; j0 < k; j0 += kRows) {
-        float v[kRows][8];
+        Raw<F32, C> v[kRows];
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
             const int r = j0 + j < k ? d[j0 + j] : -1;
-            if ((unsigned)r < (unsigned)R) {
-                load_row8<F32>(dxs, ((size_t)r * pieces + p.c) * 8, v[j]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
-            }
+            v[j] = Raw<F32, C>{};
+            if ((unsigned)r < (unsigned)R) v[j].template load<NT>(dxs, ((size_t)r * pieces + p.c) * C);
         }
 #pragma unroll
-        for (int j = 0; j < kRows; ++j)
+        for (int j = 0; j < kRows; ++j) {
+            float f[C];
+            v[j].values(f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += v[j][e];
+            for (int e = 0; e < C; ++e) sum[e] += f[e];
+        }
     }
-    store_row8<OUT_F32>(dx, at, sum);
+    store_row<OUT_F32, C>(dx, at, sum);
 }
 
-// ---- gradients of combine: a wave takes one assignment, so the sum over its row stays in the wave
+// ---- gradients of combine: a wave takes one assignment, so the sum over its row stays in
+// the wave; the waves of a workgroup share their tokens' rows in the caches
 enum { kYNone = 0, kYF32 = 1, kYBf16 = 2, kYE4m3 = 3 };
+constexpr int kGradWaves = 8, kAhead = 4;   // pieces of 64 lanes whose loads go out together
 
-template <int Y, bool D_F32, bool DY_F32>
-__global__ __launch_bounds__(256) void combine_grad_kernel(const void* __restrict__ dout, const void* __restrict__ y,
-                                                           const float* __restrict__ y_scale,
-                                                           const int32_t* __restrict__ dest, const float* __restrict__ w,
-                                                           long n, int k, int H, int R, void* __restrict__ dy,
-                                                           float* __restrict__ dw) {
+template <int Y, bool D_F32, bool DY_F32, bool NT>
+__global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
+    const void* __restrict__ dout, const void* __restrict__ y, const float* __restrict__ y_scale,
+    const int32_t* __restrict__ dest, const float* __restrict__ w, long n, int k, int H, int R, void* __restrict__ dy,
+    float* __restrict__ dw) {
+    constexpr int C = D_F32 || DY_F32 || Y == kYF32 ? 4 : 8;   // 16 bytes a lane of the wider ones
     const int lane = threadIdx.x % kWave;
-    const long f = (long)blockIdx.x * 4 + threadIdx.x / kWave;
+    const long f = (long)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (f >= n) return;
     const long t = f / k;
     const int r = dest[f];
-    const bool here = (unsigned)r < (unsigned)R;
     float sum = 0.0f;
-    if (here) {
+    if ((unsigned)r < (unsigned)R) {
         const float wf = w[f];
         const size_t from = (size_t)t * H, to = (size_t)r * H;
-        for (int c = lane * 8; c < H; c += kWave * 8) {
-            float d[8];
-            load_row8<D_F32>(dout, from + c, d);
-            if constexpr (Y != kYNone) {
-                float v[8];
+        for (int c0 = lane * C; c0 < H; c0 += kAhead * kWave * C) {
+            Raw<D_F32, C> d[kAhead];
+            Raw<Y == kYF32, C> v[kAhead];   // e4m3: the first word or two of it
+            float scale[kAhead];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                const int c = c0 + a * kWave * C;
+                if (c >= H) break;
+                d[a].load(dout, from + c);
                 if constexpr (Y == kYE4m3) {
-                    const uint2 q = *(const uint2*)((const uint8_t*)y + to + c);
-                    const float sc = y_scale[(size_t)r * (H / 128) + c / 128];
-                    const uint32_t word[2] = {q.x, q.y};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)word[i], false);
-                        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)word[i], true);
-                        v[4 * i] = lo[0] * sc;
-                        v[4 * i + 1] = lo[1] * sc;
-                        v[4 * i + 2] = hi[0] * sc;
-                        v[4 * i + 3] = hi[1] * sc;
+                    const uint8_t* q = (const uint8_t*)y + to + c;
+                    if constexpr (C == 8) {
+                        const uint2 two = *(const uint2*)q;
+                        v[a].w[0][0] = (int)two.x;
+                        v[a].w[0][1] = (int)two.y;
+                    } else {
+                        v[a].w[0][0] = *(const int*)q;
                     }
-                } else {
-                    load_row8<Y == kYF32>(y, to + c, v);
+                    scale[a] = y_scale[(size_t)r * (H / 128) + c / 128];
+                } else if constexpr (Y != kYNone) {
+                    v[a].template load<NT>(y, to + c);
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(d[e], v[e], sum);
             }
-            if (dy) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] *= wf;
-                store_row8<DY_F32>(dy, to + c, d);
+            for (int a = 0; a < kAhead; ++a) {
+                const int c = c0 + a * kWave * C;
+                if (c >= H) break;
+                float g[C];
+                d[a].values(g);
+                if constexpr (Y != kYNone) {
+                    float b[C];
+                    if constexpr (Y == kYE4m3) {
+#pragma unroll
+                        for (int i = 0; i < C / 4; ++i) {
+                            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(v[a].w[0][i], false);
+                            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(v[a].w[0][i], true);
+                            b[4 * i] = lo[0] * scale[a];
+                            b[4 * i + 1] = lo[1] * scale[a];
+                            b[4 * i + 2] = hi[0] * scale[a];
+                            b[4 * i + 3] = hi[1] * scale[a];
+                        }
+                    } else {
+                        v[a].values(b);
+                    }
+#pragma unroll
+                    for (int e = 0; e < C; ++e) sum = __builtin_fmaf(g[e], b[e], sum);
+                }
+                if (dy) {
+#pragma unroll
+                    for (int e = 0; e < C; ++e) g[e] *= wf;
+                    store_row<DY_F32, C, NT>(dy, to + c, g);
+                }
             }
         }
     }
@@ -156,65 +189,96 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const void* __restric
     }
 }
 
-// Launch shape of the kernels over the tokens' pieces of 16 bytes (or eight columns).
+// Launch shape of the kernels over the tokens' pieces.
 struct Shape {
     int slabs, per;
+    bool rows;      // LONG
     long blocks;
 };
-Shape shape_of(int T, int pieces) {
+Shape shape_of(int T, int pieces, int u) {
     Shape s;
-    s.per = pieces >= 256 ? 1 : 256 / pieces;
-    s.slabs = (pieces + 255) / 256;
-    s.blocks = s.per == 1 ? (long)T * s.slabs : ((long)T + s.per - 1) / s.per;
+    s.rows = pieces > 128;   // up to 128 pieces two tokens and more fit a workgroup
+    s.per = s.rows ? 1 : 256 / pieces;
+    s.slabs = (pieces + u * 256 - 1) / (u * 256);
+    s.blocks = s.rows ? (long)T * s.slabs : ((long)T + s.per - 1) / s.per;
     return s;
 }
-bool fits(long blocks) { return blocks <= 0xffffffffL / 256; }
+bool fits(long blocks, int threads) { return blocks <= 0xffffffffL / threads; }
+
+// Whether the rows of a matrix are whole lines.
+bool whole_lines(const void* p, size_t row_bytes) { return ((uintptr_t)p | row_bytes) % 128 == 0; }
+
+constexpr int kU = 2;   // 512 pieces a workgroup: 355 us against 388 with 256 and 364 with 1024 (see above)
 
 }  // namespace
 
-bool dispatch_fits(int T, int H, int k) { return fits(shape_of(T, H / 4).blocks) && fits(((long)T * k + 3) / 4); }
+bool dispatch_fits(int T, int H, int k) {
+    return fits(shape_of(T, H / 4, 1).blocks, 256) && fits(((long)T * k + kGradWaves - 1) / kGradWaves, kGradWaves * 64);
+}
 
 hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t s) {
     const int pieces = p.x_f32 ? p.H / 4 : p.H / 8;
-    const Shape g = shape_of(p.T, pieces);
-    if (!fits(g.blocks)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)g.blocks), block(256);
+    const Shape g = shape_of(p.T, pieces, kU);
+    if (!fits(g.blocks, 256)) return hipErrorInvalidValue;
     const auto run = [&](auto* kernel) {
-        kernel<<<grid, block, 0, s>>>((const uint8_t*)p.x, p.xe, p.T, pieces, g.slabs, g.per, p.dest, p.k, p.R, (uint4*)p.xs);
+        kernel<<<dim3((unsigned)g.blocks), dim3(256), 0, s>>>((const uint8_t*)p.x, p.xe, p.T, pieces, g.slabs, g.per, p.dest,
+                                                             p.k, p.R, (i32x4*)p.xs);
         return hipGetLastError();
     };
-    return p.xe ? run(dispatch_kernel<kFromI8>) : run(dispatch_kernel<kCopy>);
-}
-
-hipError_t launch_dispatch_backward(const DispatchProblem& p, hipStream_t s) {
-    const int pieces = p.H / 8;
-    const Shape g = shape_of(p.T, pieces);
-    if (!fits(g.blocks)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)g.blocks), block(256);
-    const auto run = [&](auto* kernel) {
-        kernel<<<grid, block, 0, s>>>(p.dxs, p.add, p.T, pieces, g.slabs, g.per, p.dest, p.k, p.R, p.dx);
-        return hipGetLastError();
-    };
-    if (p.dxs_f32) {
-        if (p.add_f32) return p.dx_f32 ? run(gather_kernel<true, true, true>) : run(gather_kernel<true, true, false>);
-        return p.dx_f32 ? run(gather_kernel<true, false, true>) : run(gather_kernel<true, false, false>);
-    }
-    if (p.add_f32) return p.dx_f32 ? run(gather_kernel<false, true, true>) : run(gather_kernel<false, true, false>);
-    return p.dx_f32 ? run(gather_kernel<false, false, true>) : run(gather_kernel<false, false, false>);
+    if (!g.rows) return p.xe ? run(dispatch_kernel<true, false, 1, false>) : run(dispatch_kernel<false, false, 1, false>);
+    if (whole_lines(p.xs, (size_t)pieces * 16))
+        return p.xe ? run(dispatch_kernel<true, true, kU, true>) : run(dispatch_kernel<false, true, kU, true>);
+    return p.xe ? run(dispatch_kernel<true, true, kU, false>) : run(dispatch_kernel<false, true, kU, false>);
 }
 
 namespace {
 
-template <int Y>
-hipError_t combine_grad(const CombineGradProblem& p, hipStream_t s) {
-    const long n = (long)p.T * p.k, blocks = (n + 3) / 4;
-    if (!fits(blocks)) return hipErrorInvalidValue;
+template <bool F32, bool ADD_F32, bool OUT_F32>
+hipError_t gather(const DispatchProblem& p, hipStream_t s) {
+    const int pieces = p.H / (F32 ? 4 : 8);
+    const Shape g = shape_of(p.T, pieces, 1);
+    if (!fits(g.blocks, 256)) return hipErrorInvalidValue;
     const auto run = [&](auto* kernel) {
-        kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(p.dout, p.y, p.y_scale, p.dest, p.w, n, p.k, p.H, p.R, p.dy, p.dw);
+        kernel<<<dim3((unsigned)g.blocks), dim3(256), 0, s>>>(p.dxs, p.add, p.T, pieces, g.slabs, g.per, p.dest, p.k, p.R, p.dx);
         return hipGetLastError();
     };
-    if (p.dout_f32) return p.dy_f32 ? run(combine_grad_kernel<Y, true, true>) : run(combine_grad_kernel<Y, true, false>);
-    return p.dy_f32 ? run(combine_grad_kernel<Y, false, true>) : run(combine_grad_kernel<Y, false, false>);
+    if (!g.rows) return run(gather_kernel<F32, ADD_F32, OUT_F32, false, false>);
+    if (whole_lines(p.dxs, (size_t)pieces * 16)) return run(gather_kernel<F32, ADD_F32, OUT_F32, true, true>);
+    return run(gather_kernel<F32, ADD_F32, OUT_F32, true, false>);
+}
+
+}  // namespace
+
+hipError_t launch_dispatch_backward(const DispatchProblem& p, hipStream_t s) {
+    if (p.dxs_f32) {
+        if (p.add_f32) return p.dx_f32 ? gather<true, true, true>(p, s) : gather<true, true, false>(p, s);
+        return p.dx_f32 ? gather<true, false, true>(p, s) : gather<true, false, false>(p, s);
+    }
+    if (p.add_f32) return p.dx_f32 ? gather<false, true, true>(p, s) : gather<false, true, false>(p, s);
+    return p.dx_f32 ? gather<false, false, true>(p, s) : gather<false, false, false>(p, s);
+}
+
+namespace {
+
+template <int Y, bool D_F32, bool DY_F32>
+hipError_t combine_grad(const CombineGradProblem& p, hipStream_t s) {
+    const long n = (long)p.T * p.k, blocks = (n + kGradWaves - 1) / kGradWaves;
+    if (!fits(blocks, kGradWaves * 64)) return hipErrorInvalidValue;
+    const auto run = [&](auto* kernel) {
+        kernel<<<dim3((unsigned)blocks), dim3(kGradWaves * 64), 0, s>>>(p.dout, p.y, p.y_scale, p.dest, p.w, n, p.k, p.H, p.R,
+                                                                       p.dy, p.dw);
+        return hipGetLastError();
+    };
+    if ((!p.dy || whole_lines(p.dy, (size_t)p.H * (DY_F32 ? 4 : 2))) &&
+        (Y == kYNone || Y == kYE4m3 || whole_lines(p.y, (size_t)p.H * (Y == kYF32 ? 4 : 2))))
+        return run(combine_grad_kernel<Y, D_F32, DY_F32, true>);
+    return run(combine_grad_kernel<Y, D_F32, DY_F32, false>);
+}
+
+template <int Y>
+hipError_t combine_grad(const CombineGradProblem& p, hipStream_t s) {
+    if (p.dout_f32) return p.dy_f32 ? combine_grad<Y, true, true>(p, s) : combine_grad<Y, true, false>(p, s);
+    return p.dy_f32 ? combine_grad<Y, false, true>(p, s) : combine_grad<Y, false, false>(p, s);
 }
 
 }  // namespace
