@@ -11,6 +11,7 @@
 // bring: no list is made beforehand, and nothing about the rows has to reach the host.
 #include <algorithm>
 
+#include "gemm_half.h"
 #include "gemm_plan.h"
 #include "gemm_stream.h"
 
@@ -141,6 +142,12 @@ __global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per
     const Args G = rows_of<EPI>(P, at);
     int tm, tn;
     band_of(at.t, (at.m + EDGE - 1) / EDGE, P.nt, tm, tn);
+    if constexpr (EDGE == 256) {
+        if (at.m - tm * EDGE <= EDGE / 2) {
+            half_tile<LB, EPI, GU>(G, tm * EDGE, tn);
+            return;
+        }
+    }
     tile_at<kBf16, kRow, LB, EPI, GU, EDGE, EDGE, 5>(G, tm, tn, 0);
 }
 

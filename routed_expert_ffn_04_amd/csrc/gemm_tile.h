@@ -260,6 +260,156 @@ __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& t
     band_of(t, mt, nt, tm, tn);
 }
 
+// Epilogue of a wave whose part of the product begins at row mw and column nw.  Every wave has
+// left the ring, which becomes the scratch.
+template <int E, int EPI, bool GU, int IB, int JB>
+__device__ __forceinline__ void finish(const Args& G, const typename Acc<E>::type (&acc)[IB][JB], uint8_t* smem, int wave,
+                                       int lane, int mw, int nw, int split) {
+    // acc[i][j][v]: m = 16 i + l % 16, n = 16 j + 4 (l / 16) + v of the wave's part.  32 rows at a time pass through the wave's own piece of LDS
+    // (rows padded by 16 bytes, free of bank conflicts both ways), so that global
+    // accesses are whole row pieces.
+    constexpr int WC = JB * 16;                          // MFMA columns of a wave
+    constexpr int RS = WC * 4 + 16;
+    constexpr int RL = (GU ? WC / 2 : WC) / 8;           // lanes a row, eight outputs each
+    constexpr int RP = 64 / RL, kPass = 32 / RP;         // rows a pass
+    uint8_t* piece = smem + wave * 32 * RS;
+    // A lane's eight columns are the same in every pass: their scales are read once.
+    const int nl = nw + (lane % RL) * 8;
+    float wsv[8], bv[8], xsv[IB / 2][kPass];
+    if constexpr (EPI == kEpiI8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int ne = min(nl + e, G.N - 1);
+            wsv[e] = G.ws[ne];
+            bv[e] = G.bias ? G.bias[ne] : 0.0f;
+        }
+#pragma unroll
+        for (int ib = 0; ib < IB / 2; ++ib)
+#pragma unroll
+            for (int p = 0; p < kPass; ++p)
+                xsv[ib][p] = G.xs[min(mw + ib * 32 + p * RP + lane / RL, G.M - 1)];
+    }
+#pragma unroll
+    for (int ib = 0; ib < IB / 2; ++ib) {
+        const int mb = mw + ib * 32;
+        if (mb >= G.M) break;
+        // the saved pre-activations of the 32 rows, read while the accumulators pass through LDS
+        float4 gv[kPass][2], uv[kPass][2];
+        uint2 gq[kPass], uq[kPass];
+        uint32_t ge[kPass], ue[kPass];
+        if constexpr (EPI == kEpiGrad8) {
+            const size_t nb = (size_t)i8x16_blocks(G.N);
+#pragma unroll
+            for (int p = 0; p < kPass; ++p) {
+                const size_t m = (size_t)min(mb + p * RP + lane / RL, G.M - 1);
+                const int n = min(nl, G.N - 8);
+                gq[p] = *(const uint2*)(G.q + m * (2 * (size_t)G.N) + n);
+                uq[p] = *(const uint2*)(G.q + m * (2 * (size_t)G.N) + G.N + n);
+                ge[p] = G.qe[m * (2 * nb) + n / kI8Block];
+                ue[p] = G.qe[m * (2 * nb) + nb + n / kI8Block];
+            }
+        }
+        if constexpr (EPI == kEpiGrad) {
+#pragma unroll
+            for (int p = 0; p < kPass; ++p) {
+                const size_t at = (size_t)min(mb + p * RP + lane / RL, G.M - 1) * (2 * (size_t)G.N) + min(nl, G.N - 8);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    gv[p][e] = *(const float4*)(G.gu + at + 4 * e);
+                    uv[p][e] = *(const float4*)(G.gu + at + G.N + 4 * e);
+                }
+            }
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < JB; ++j)
+                *(typename Acc<E>::type*)(piece + (i * 16 + lane % 16) * RS + (16 * j + 4 * (lane / 16)) * 4) = acc[ib * 2 + i][j];
+        wave_sync();
+        auto words = [&](int row, int n, float(&v)[8]) {
+            const float4 lo = *(const float4*)(piece + row * RS + n * 4);
+            const float4 hi = *(const float4*)(piece + row * RS + n * 4 + 16);
+            v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w; v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        };
+        if constexpr (GU) {
+            // WC / 2 gate columns, then as many up columns
+#pragma unroll
+            for (int p = 0; p < kPass; ++p) {
+                const int row = p * RP + lane / RL, c = (lane % RL) * 8;
+                const int m = mb + row, n = nw + c;
+                float g[8], u[8], h[8];
+                words(row, c, g);
+                words(row, WC / 2 + c, u);
+                if constexpr (EPI == kEpiGateUp8) store_gu8(G, m, n, g, u);
+                if (m < G.M && n < G.N) {
+                    if constexpr (EPI == kEpiPart) {
+                        float* o = (float*)G.out + ((size_t)split * G.M + m) * (2 * (size_t)G.N) + n;
+                        *(float4*)o = make_float4(g[0], g[1], g[2], g[3]);
+                        *(float4*)(o + 4) = make_float4(g[4], g[5], g[6], g[7]);
+                        o += G.N;
+                        *(float4*)o = make_float4(u[0], u[1], u[2], u[3]);
+                        *(float4*)(o + 4) = make_float4(u[4], u[5], u[6], u[7]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[e] = silu_mul(g[e], u[e]);
+                        *(uint4*)((uint16_t*)G.out + (size_t)m * G.N + n) = pack8(h);
+                        if (EPI == kEpiGateUp && G.out2) {
+                            float* o = (float*)G.out2 + (size_t)m * (2 * (size_t)G.N) + n;
+                            *(float4*)o = make_float4(g[0], g[1], g[2], g[3]);
+                            *(float4*)(o + 4) = make_float4(g[4], g[5], g[6], g[7]);
+                            o += G.N;
+                            *(float4*)o = make_float4(u[0], u[1], u[2], u[3]);
+                            *(float4*)(o + 4) = make_float4(u[4], u[5], u[6], u[7]);
+                        }
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < kPass; ++p) {
+                const int row = p * RP + lane / RL, c = (lane % RL) * 8;
+                const int m = mb + row, n = nw + c;
+                float v[8];
+                words(row, c, v);
+                if (m < G.M && n < G.N) {
+                    if constexpr (EPI == kEpiGrad || EPI == kEpiGrad8) {
+                        float g[8], u[8], dg[8], du[8], h[8];
+                        if constexpr (EPI == kEpiGrad8) {
+                            i8x16_values(gq[p], ge[p], g);
+                            i8x16_values(uq[p], ue[p], u);
+                        } else {
+                            const float4 ga = gv[p][0], gb = gv[p][1], ua = uv[p][0], ub = uv[p][1];
+                            g[0] = ga.x; g[1] = ga.y; g[2] = ga.z; g[3] = ga.w; g[4] = gb.x; g[5] = gb.y; g[6] = gb.z; g[7] = gb.w;
+                            u[0] = ua.x; u[1] = ua.y; u[2] = ua.z; u[3] = ua.w; u[4] = ub.x; u[5] = ub.y; u[6] = ub.z; u[7] = ub.w;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) swiglu_grad(g[e], u[e], v[e], dg[e], du[e], h[e]);
+                        uint16_t* d = (uint16_t*)G.out + (size_t)m * (2 * (size_t)G.N) + n;
+                        *(uint4*)d = pack8(dg);
+                        *(uint4*)(d + G.N) = pack8(du);
+                        *(uint4*)((uint16_t*)G.out2 + (size_t)m * G.N + n) = pack8(h);
+                    } else if constexpr (EPI == kEpiPart) {
+                        store8(G, (uint8_t*)((float*)G.out + ((size_t)split * G.M + m) * G.N), n, v, true);
+                    } else if constexpr (EPI == kEpiI8) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            v[e] = (float)__float_as_int(v[e]) * (xsv[ib][p] * wsv[e]);
+                            if (G.bias) v[e] += bv[e];
+                        }
+                        store8(G, (uint8_t*)G.out + (size_t)m * G.N * (G.out_f32 ? 4 : 2), n, v, G.out_f32);
+                    } else {
+                        const size_t row_bytes = (size_t)G.N * (G.out_f32 ? 4 : 2);
+                        uint8_t* o = m < G.msplit ? (uint8_t*)G.out + (size_t)m * row_bytes
+                                                  : (uint8_t*)G.out2 + (size_t)(m - G.msplit) * row_bytes;
+                        store8(G, o, n, v, G.out_f32);
+                    }
+                }
+            }
+        }
+    }
+}
+
 // Launch shape of the tiles: LDS, and waves per SIMD by it.
 constexpr int tile_lds(int edge, int ring) { return ring * edge * kStage; }
 constexpr int tile_waves(int edge, int ring) { return edge == 256 ? 2 : 163840 / tile_lds(edge, ring); }   // per SIMD
@@ -532,151 +682,7 @@ __device__ __forceinline__ void tile_at(const Args& G, int tm, int tn, int split
     // the prefetched (zero) stages land before the ring becomes the epilogue's scratch
     barrier_vm<0>();
 
-    // ---- epilogue.  acc[i][j][v]: m = 16 i + l % 16, n = 16 j + 4 (l / 16) + v of
-    // the wave's part.  32 rows at a time pass through the wave's own piece of LDS
-    // (rows padded by 16 bytes, free of bank conflicts both ways), so that global
-    // accesses are whole row pieces.
-    constexpr int WC = JB * 16;                          // MFMA columns of a wave
-    constexpr int RS = WC * 4 + 16;
-    constexpr int RL = (GU ? WC / 2 : WC) / 8;           // lanes a row, eight outputs each
-    constexpr int RP = 64 / RL, kPass = 32 / RP;         // rows a pass
-    uint8_t* piece = smem + wave * 32 * RS;
-    const int nw = n0 + wn * (GU ? WC / 2 : WC);
-    // A lane's eight columns are the same in every pass: their scales are read once.
-    const int nl = nw + (lane % RL) * 8;
-    float wsv[8], bv[8], xsv[IB / 2][kPass];
-    if constexpr (EPI == kEpiI8) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int ne = min(nl + e, G.N - 1);
-            wsv[e] = G.ws[ne];
-            bv[e] = G.bias ? G.bias[ne] : 0.0f;
-        }
-#pragma unroll
-        for (int ib = 0; ib < IB / 2; ++ib)
-#pragma unroll
-            for (int p = 0; p < kPass; ++p)
-                xsv[ib][p] = G.xs[min(m0 + wm * IB * 16 + ib * 32 + p * RP + lane / RL, G.M - 1)];
-    }
-#pragma unroll
-    for (int ib = 0; ib < IB / 2; ++ib) {
-        const int mb = m0 + wm * IB * 16 + ib * 32;
-        if (mb >= G.M) break;
-        // the saved pre-activations of the 32 rows, read while the accumulators pass through LDS
-        float4 gv[kPass][2], uv[kPass][2];
-        uint2 gq[kPass], uq[kPass];
-        uint32_t ge[kPass], ue[kPass];
-        if constexpr (EPI == kEpiGrad8) {
-            const size_t nb = (size_t)i8x16_blocks(G.N);
-#pragma unroll
-            for (int p = 0; p < kPass; ++p) {
-                const size_t m = (size_t)min(mb + p * RP + lane / RL, G.M - 1);
-                const int n = min(nl, G.N - 8);
-                gq[p] = *(const uint2*)(G.q + m * (2 * (size_t)G.N) + n);
-                uq[p] = *(const uint2*)(G.q + m * (2 * (size_t)G.N) + G.N + n);
-                ge[p] = G.qe[m * (2 * nb) + n / kI8Block];
-                ue[p] = G.qe[m * (2 * nb) + nb + n / kI8Block];
-            }
-        }
-        if constexpr (EPI == kEpiGrad) {
-#pragma unroll
-            for (int p = 0; p < kPass; ++p) {
-                const size_t at = (size_t)min(mb + p * RP + lane / RL, G.M - 1) * (2 * (size_t)G.N) + min(nl, G.N - 8);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    gv[p][e] = *(const float4*)(G.gu + at + 4 * e);
-                    uv[p][e] = *(const float4*)(G.gu + at + G.N + 4 * e);
-                }
-            }
-        }
-        wave_sync();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < JB; ++j)
-                *(typename Acc<E>::type*)(piece + (i * 16 + lane % 16) * RS + (16 * j + 4 * (lane / 16)) * 4) = acc[ib * 2 + i][j];
-        wave_sync();
-        auto words = [&](int row, int n, float(&v)[8]) {
-            const float4 lo = *(const float4*)(piece + row * RS + n * 4);
-            const float4 hi = *(const float4*)(piece + row * RS + n * 4 + 16);
-            v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w; v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
-        };
-        if constexpr (GU) {
-            // WC / 2 gate columns, then as many up columns
-#pragma unroll
-            for (int p = 0; p < kPass; ++p) {
-                const int row = p * RP + lane / RL, c = (lane % RL) * 8;
-                const int m = mb + row, n = nw + c;
-                float g[8], u[8], h[8];
-                words(row, c, g);
-                words(row, WC / 2 + c, u);
-                if constexpr (EPI == kEpiGateUp8) store_gu8(G, m, n, g, u);
-                if (m < G.M && n < G.N) {
-                    if constexpr (EPI == kEpiPart) {
-                        float* o = (float*)G.out + ((size_t)split * G.M + m) * (2 * (size_t)G.N) + n;
-                        *(float4*)o = make_float4(g[0], g[1], g[2], g[3]);
-                        *(float4*)(o + 4) = make_float4(g[4], g[5], g[6], g[7]);
-                        o += G.N;
-                        *(float4*)o = make_float4(u[0], u[1], u[2], u[3]);
-                        *(float4*)(o + 4) = make_float4(u[4], u[5], u[6], u[7]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) h[e] = silu_mul(g[e], u[e]);
-                        *(uint4*)((uint16_t*)G.out + (size_t)m * G.N + n) = pack8(h);
-                        if (EPI == kEpiGateUp && G.out2) {
-                            float* o = (float*)G.out2 + (size_t)m * (2 * (size_t)G.N) + n;
-                            *(float4*)o = make_float4(g[0], g[1], g[2], g[3]);
-                            *(float4*)(o + 4) = make_float4(g[4], g[5], g[6], g[7]);
-                            o += G.N;
-                            *(float4*)o = make_float4(u[0], u[1], u[2], u[3]);
-                            *(float4*)(o + 4) = make_float4(u[4], u[5], u[6], u[7]);
-                        }
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int p = 0; p < kPass; ++p) {
-                const int row = p * RP + lane / RL, c = (lane % RL) * 8;
-                const int m = mb + row, n = nw + c;
-                float v[8];
-                words(row, c, v);
-                if (m < G.M && n < G.N) {
-                    if constexpr (EPI == kEpiGrad || EPI == kEpiGrad8) {
-                        float g[8], u[8], dg[8], du[8], h[8];
-                        if constexpr (EPI == kEpiGrad8) {
-                            i8x16_values(gq[p], ge[p], g);
-                            i8x16_values(uq[p], ue[p], u);
-                        } else {
-                            const float4 ga = gv[p][0], gb = gv[p][1], ua = uv[p][0], ub = uv[p][1];
-                            g[0] = ga.x; g[1] = ga.y; g[2] = ga.z; g[3] = ga.w; g[4] = gb.x; g[5] = gb.y; g[6] = gb.z; g[7] = gb.w;
-                            u[0] = ua.x; u[1] = ua.y; u[2] = ua.z; u[3] = ua.w; u[4] = ub.x; u[5] = ub.y; u[6] = ub.z; u[7] = ub.w;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) swiglu_grad(g[e], u[e], v[e], dg[e], du[e], h[e]);
-                        uint16_t* d = (uint16_t*)G.out + (size_t)m * (2 * (size_t)G.N) + n;
-                        *(uint4*)d = pack8(dg);
-                        *(uint4*)(d + G.N) = pack8(du);
-                        *(uint4*)((uint16_t*)G.out2 + (size_t)m * G.N + n) = pack8(h);
-                    } else if constexpr (EPI == kEpiPart) {
-                        store8(G, (uint8_t*)((float*)G.out + ((size_t)split * G.M + m) * G.N), n, v, true);
-                    } else if constexpr (EPI == kEpiI8) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            v[e] = (float)__float_as_int(v[e]) * (xsv[ib][p] * wsv[e]);
-                            if (G.bias) v[e] += bv[e];
-                        }
-                        store8(G, (uint8_t*)G.out + (size_t)m * G.N * (G.out_f32 ? 4 : 2), n, v, G.out_f32);
-                    } else {
-                        const size_t row_bytes = (size_t)G.N * (G.out_f32 ? 4 : 2);
-                        uint8_t* o = m < G.msplit ? (uint8_t*)G.out + (size_t)m * row_bytes
-                                                  : (uint8_t*)G.out2 + (size_t)(m - G.msplit) * row_bytes;
-                        store8(G, o, n, v, G.out_f32);
-                    }
-                }
-            }
-        }
-    }
+    finish<E, EPI, GU, IB, JB>(G, acc, smem, wave, lane, m0 + wm * IB * 16, n0 + wn * (GU ? JB * 8 : JB * 16), split);
 }
 
 // Workgroup `block` of the `blocks` that share out the tiles and splits of G.
