@@ -133,8 +133,8 @@ __device__ __forceinline__ Args sum_of(const Grouped& P, int e, int t, int& tm, 
     return G;
 }
 
-template <int LB, int EPI, int EDGE>
-__global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per_eu(tile_waves(EDGE, 5)))) void rows_kernel(
+template <int LB, int EPI, int EDGE, int R>
+__global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per_eu(tile_waves(EDGE, R)))) void rows_kernel(
     Grouped P) {
     constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
     Place at;
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per
             return;
         }
     }
-    tile_at<kBf16, kRow, LB, EPI, GU, EDGE, EDGE, 5>(G, tm, tn, 0);
+    tile_at<kBf16, kRow, LB, EPI, GU, EDGE, EDGE, R>(G, tm, tn, 0);
 }
 
 // The last products of the backward pass, which do not depend on each other: one launch.
@@ -157,8 +157,8 @@ struct Products {
     int first[4];   // first workgroup of each
     int sum[3];     // a weight gradient, else dx
 };
-template <int EDGE>
-__global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per_eu(tile_waves(EDGE, 5)))) void products_kernel(
+template <int EDGE, int R>
+__global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per_eu(tile_waves(EDGE, R)))) void products_kernel(
     Products Q) {
     const int b = blockIdx.x;
     const int i = (b >= Q.first[1]) + (b >= Q.first[2]);
@@ -168,13 +168,13 @@ __global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per
         int e, t;
         if (!find_sum(P.nt, b - Q.first[i], e, t)) return;
         const Args G = sum_of(P, e, t, tm, tn);
-        tile_at<kBf16, kCol, kCol, kEpiOut, false, EDGE, EDGE, 5>(G, tm, tn, 0);
+        tile_at<kBf16, kCol, kCol, kEpiOut, false, EDGE, EDGE, R>(G, tm, tn, 0);
     } else {
         Place at;
         if (!find_rows(P, EDGE, b - Q.first[i], at)) return;
         const Args G = rows_of<kEpiOut>(P, at);
         band_of(at.t, (at.m + EDGE - 1) / EDGE, P.nt, tm, tn);
-        tile_at<kBf16, kRow, kCol, kEpiOut, false, EDGE, EDGE, 5>(G, tm, tn, 0);
+        tile_at<kBf16, kRow, kCol, kEpiOut, false, EDGE, EDGE, R>(G, tm, tn, 0);
     }
 }
 
@@ -206,16 +206,20 @@ long row_tiles(int R, int n, int edge) { return (long)R / edge + std::min(R, n);
 // share the tiles that there are evenly).
 long rows_grid(int R, int n, int edge, int nt) { return (row_tiles(R, n, edge) * nt + kXcds - 1) / kXcds * kXcds; }
 
-// Tile edge of a product over the experts' rows, by the time estimated for rows
-// spread evenly.
+// Row tiles of rows spread evenly, which is what times are estimated for.
+long even_tiles(int R, int n, int edge) {
+    const int used = std::min(R, n), each = (R + used - 1) / used;
+    return (long)used * ((each + edge - 1) / edge);
+}
+
+// Tile edge of a product over the experts' rows, by the estimated time.
 int rows_edge(int R, int n, long cols, int K) {
     int best = 0;
     double least = 0;
-    const int used = std::min(R, n), each = (R + used - 1) / used;
     for (int edge = 64; edge <= 256; edge *= 2) {
         const long nt = (cols + edge - 1) / edge;
         if (nt > 0x7fffffffL / 2 || !grid_fits(rows_grid(R, n, edge, (int)nt), tile_threads(edge))) continue;
-        const double us = tiling_us(edge, (long)used * ((each + edge - 1) / edge) * nt, (K + kKE - 1) / kKE);
+        const double us = tiling_us(edge, even_tiles(R, n, edge) * nt, (K + kKE - 1) / kKE);
         if (least == 0 || us < least) {
             least = us;
             best = edge;
@@ -224,26 +228,35 @@ int rows_edge(int R, int n, long cols, int K) {
     return best;
 }
 
+template <int LB, int EPI, int EDGE, int R>
+hipError_t launch_rows_ring(const Grouped& P, long grid, hipStream_t s) {
+    auto* k = rows_kernel<LB, EPI, EDGE, R>;
+    static DeviceCache ready;
+    if (!allow_lds(ready, k, tile_lds(EDGE, R))) return hipErrorInvalidValue;
+    k<<<dim3((unsigned)grid), dim3(tile_threads(EDGE)), tile_lds(EDGE, R), s>>>(P);
+    return hipGetLastError();
+}
+
+// The longer ring where there are no more tiles than it lets run at once (launch_tiling).
 template <int LB, int EPI, int EDGE>
-hipError_t launch_rows_edge(Grouped P, hipStream_t s) {
+hipError_t launch_rows_edge(Grouped P, long used, hipStream_t s) {
     constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
     P.nt = (P.G.N + (GU ? EDGE / 2 : EDGE) - 1) / (GU ? EDGE / 2 : EDGE);
     const long grid = rows_grid(P.R, P.n, EDGE, P.nt);
     if (!grid_fits(grid, tile_threads(EDGE))) return hipErrorInvalidValue;
-    auto* k = rows_kernel<LB, EPI, EDGE>;
-    static DeviceCache ready;
-    if (!allow_lds(ready, k, tile_lds(EDGE, 5))) return hipErrorInvalidValue;
-    k<<<dim3((unsigned)grid), dim3(tile_threads(EDGE)), tile_lds(EDGE, 5), s>>>(P);
-    return hipGetLastError();
+    if constexpr (EDGE < 256) {
+        if (used * P.nt <= (EDGE == 64 ? 512 : 256)) return launch_rows_ring<LB, EPI, EDGE, 10>(P, grid, s);
+    }
+    return launch_rows_ring<LB, EPI, EDGE, 5>(P, grid, s);
 }
 
 template <int LB, int EPI>
 hipError_t launch_rows(const Grouped& P, hipStream_t s) {
     constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
     switch (rows_edge(P.R, P.n, GU ? 2L * P.G.N : P.G.N, P.G.K)) {
-        case 64: return launch_rows_edge<LB, EPI, 64>(P, s);
-        case 128: return launch_rows_edge<LB, EPI, 128>(P, s);
-        case 256: return launch_rows_edge<LB, EPI, 256>(P, s);
+        case 64: return launch_rows_edge<LB, EPI, 64>(P, even_tiles(P.R, P.n, 64), s);
+        case 128: return launch_rows_edge<LB, EPI, 128>(P, even_tiles(P.R, P.n, 128), s);
+        case 256: return launch_rows_edge<LB, EPI, 256>(P, even_tiles(P.R, P.n, 256), s);
         default: return hipErrorInvalidValue;
     }
 }
@@ -308,9 +321,18 @@ int together_edge(const Products& Q, int m, int R, int n) {
     return best;
 }
 
+template <int EDGE, int R>
+hipError_t launch_products_ring(const Products& Q, long total, hipStream_t s) {
+    auto* k = products_kernel<EDGE, R>;
+    static DeviceCache ready;
+    if (!allow_lds(ready, k, tile_lds(EDGE, R))) return hipErrorInvalidValue;
+    k<<<dim3((unsigned)total), dim3(tile_threads(EDGE)), tile_lds(EDGE, R), s>>>(Q);
+    return hipGetLastError();
+}
+
 template <int EDGE>
 hipError_t launch_products(Products Q, int m, hipStream_t s) {
-    long total = 0;
+    long total = 0, used = 0;
     for (int i = 0; i < m; ++i) {
         Grouped& P = Q.P[i];
         Q.first[i] = (int)total;
@@ -319,18 +341,19 @@ hipError_t launch_products(Products Q, int m, hipStream_t s) {
             P.G.nt = (P.G.N + EDGE - 1) / EDGE;
             P.nt = P.G.mt * P.G.nt;
             total += (long)P.n * die_share(P.nt) * kXcds;
+            used += (long)P.n * P.nt;
         } else {
             P.nt = (P.G.N + EDGE - 1) / EDGE;
             total += rows_grid(P.R, P.n, EDGE, P.nt);
+            used += even_tiles(P.R, P.n, EDGE) * P.nt;
         }
         if (!grid_fits(total, tile_threads(EDGE))) return hipErrorInvalidValue;
     }
     for (int i = m; i < 4; ++i) Q.first[i] = (int)total;
-    auto* k = products_kernel<EDGE>;
-    static DeviceCache ready;
-    if (!allow_lds(ready, k, tile_lds(EDGE, 5))) return hipErrorInvalidValue;
-    k<<<dim3((unsigned)total), dim3(tile_threads(EDGE)), tile_lds(EDGE, 5), s>>>(Q);
-    return hipGetLastError();
+    if constexpr (EDGE < 256) {
+        if (used <= (EDGE == 64 ? 512 : 256)) return launch_products_ring<EDGE, 10>(Q, total, s);
+    }
+    return launch_products_ring<EDGE, 5>(Q, total, s);
 }
 
 // The weight gradients as a stream of 256 x 256 tiles: where these give every CU one.
