@@ -819,9 +819,14 @@ def _experts_bank(bank: Experts, H: int, device):
     n, I, _ = wg.shape
     if n > _MOST or I > _MOST:
         raise ValueError(f"bank: n={n} or I={I} is above {_MOST}")
-    _tensor(device, "w_gate", wg, (n, I, H), bf)
-    _tensor(device, "w_up", wu, (n, I, H), bf)
-    _tensor(device, "w_down", wd, (n, H, I), bf)
+    shape = (n, I, H)
+    if not (wg.shape == shape and wu.shape == shape and wd.shape == (n, H, I)
+            and wg.dtype is bf[0] and wu.dtype is bf[0] and wd.dtype is bf[0]
+            and wg.get_device() == device and wu.get_device() == device and wd.get_device() == device
+            and wg.is_contiguous() and wu.is_contiguous() and wd.is_contiguous()):
+        _tensor(device, "w_gate", wg, shape, bf)   # which one it is
+        _tensor(device, "w_up", wu, shape, bf)
+        _tensor(device, "w_down", wd, (n, H, I), bf)
     return ExpertsT(n, H, I, BF16, wg.data_ptr(), wu.data_ptr(), wd.data_ptr()), n, I
 
 
@@ -880,10 +885,12 @@ def experts_ffn_backward(dy, xs, offsets, bank: Experts, gu=None, *, need=_GRADS
 
 def _slots(name, dest, k, device):
     """Tokens of dest ([T * k] or [T][k] int32)."""
-    if k < 1 or k > _MOST or dest.numel() % k:
-        raise ValueError(f"{name}: dest of {dest.numel()} values with k={k}")
-    T = dest.numel() // k
-    _tensor(device, "dest", dest, (T, k) if dest.dim() == 2 else (T * k,), (torch.int32,))
+    n = dest.numel()
+    if k < 1 or k > _MOST or n % k:
+        raise ValueError(f"{name}: dest of {n} values with k={k}")
+    T = n // k
+    if dest.dim() != 1 or dest.dtype is not torch.int32 or dest.get_device() != device or not dest.is_contiguous():
+        _tensor(device, "dest", dest, (T, k) if dest.dim() == 2 else (n,), (torch.int32,))
     return T
 
 
