@@ -11,6 +11,7 @@
 // bring: no list is made beforehand, and nothing about the rows has to reach the host.
 #include <algorithm>
 
+#include "experts_plan.h"
 #include "gemm_half.h"
 #include "gemm_plan.h"
 #include "gemm_stream.h"
@@ -21,6 +22,7 @@ using namespace gemm;
 namespace {
 
 constexpr int kKE = kStage / 2;
+static_assert(kDies == kXcds && kStreamEdge == kStreamM && kStreamEdge == kStreamN, "what the plans count with");
 
 // One product for all experts: G as for expert 0 from row 0 on, and the steps
 // from expert to expert.
@@ -110,7 +112,6 @@ __device__ __forceinline__ Args rows_of(const Grouped& P, const Place& at) {
 
 // Workgroups of weight gradients of `nt` tiles an expert.  The dies share out every
 // expert's tiles, so that none has the long experts for itself.
-__host__ __device__ __forceinline__ int die_share(int nt) { return (nt + kXcds - 1) / kXcds; }
 __device__ __forceinline__ bool find_sum(int nt, int block, int& e, int& t) {
     const int per = die_share(nt);
     e = block / kXcds / per;
@@ -198,36 +199,6 @@ Grouped base(const ExpertsProblem& p, int N, int K) {
     return P;
 }
 
-// Row tiles that the experts' rows can fill: one more than they fill together, for every expert
-// that has rows.
-long row_tiles(int R, int n, int edge) { return (long)R / edge + std::min(R, n); }
-
-// Workgroups of a product over the experts' rows (a multiple of the dies, which
-// share the tiles that there are evenly).
-long rows_grid(int R, int n, int edge, int nt) { return (row_tiles(R, n, edge) * nt + kXcds - 1) / kXcds * kXcds; }
-
-// Row tiles of rows spread evenly, which is what times are estimated for.
-long even_tiles(int R, int n, int edge) {
-    const int used = std::min(R, n), each = (R + used - 1) / used;
-    return (long)used * ((each + edge - 1) / edge);
-}
-
-// Tile edge of a product over the experts' rows, by the estimated time.
-int rows_edge(int R, int n, long cols, int K) {
-    int best = 0;
-    double least = 0;
-    for (int edge = 64; edge <= 256; edge *= 2) {
-        const long nt = (cols + edge - 1) / edge;
-        if (nt > 0x7fffffffL / 2 || !grid_fits(rows_grid(R, n, edge, (int)nt), tile_threads(edge))) continue;
-        const double us = tiling_us(edge, even_tiles(R, n, edge) * nt, (K + kKE - 1) / kKE);
-        if (least == 0 || us < least) {
-            least = us;
-            best = edge;
-        }
-    }
-    return best;
-}
-
 template <int LB, int EPI, int EDGE, int R>
 hipError_t launch_rows_ring(const Grouped& P, long grid, hipStream_t s) {
     auto* k = rows_kernel<LB, EPI, EDGE, R>;
@@ -237,15 +208,14 @@ hipError_t launch_rows_ring(const Grouped& P, long grid, hipStream_t s) {
     return hipGetLastError();
 }
 
-// The longer ring where there are no more tiles than it lets run at once (launch_tiling).
 template <int LB, int EPI, int EDGE>
-hipError_t launch_rows_edge(Grouped P, long used, hipStream_t s) {
+hipError_t launch_rows_edge(Grouped P, hipStream_t s) {
     constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
     P.nt = (P.G.N + (GU ? EDGE / 2 : EDGE) - 1) / (GU ? EDGE / 2 : EDGE);
     const long grid = rows_grid(P.R, P.n, EDGE, P.nt);
     if (!grid_fits(grid, tile_threads(EDGE))) return hipErrorInvalidValue;
     if constexpr (EDGE < 256) {
-        if (used * P.nt <= (EDGE == 64 ? 512 : 256)) return launch_rows_ring<LB, EPI, EDGE, 10>(P, grid, s);
+        if (ring_of(EDGE, even_tiles(P.R, P.n, EDGE) * P.nt) == 10) return launch_rows_ring<LB, EPI, EDGE, 10>(P, grid, s);
     }
     return launch_rows_ring<LB, EPI, EDGE, 5>(P, grid, s);
 }
@@ -253,10 +223,10 @@ hipError_t launch_rows_edge(Grouped P, long used, hipStream_t s) {
 template <int LB, int EPI>
 hipError_t launch_rows(const Grouped& P, hipStream_t s) {
     constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
-    switch (rows_edge(P.R, P.n, GU ? 2L * P.G.N : P.G.N, P.G.K)) {
-        case 64: return launch_rows_edge<LB, EPI, 64>(P, even_tiles(P.R, P.n, 64), s);
-        case 128: return launch_rows_edge<LB, EPI, 128>(P, even_tiles(P.R, P.n, 128), s);
-        case 256: return launch_rows_edge<LB, EPI, 256>(P, even_tiles(P.R, P.n, 256), s);
+    switch (rows_edge(P.R, P.n, GU ? 2L * P.G.N : P.G.N, P.G.K, kKE)) {
+        case 64: return launch_rows_edge<LB, EPI, 64>(P, s);
+        case 128: return launch_rows_edge<LB, EPI, 128>(P, s);
+        case 256: return launch_rows_edge<LB, EPI, 256>(P, s);
         default: return hipErrorInvalidValue;
     }
 }
@@ -291,36 +261,6 @@ Backward backward(int R, int H, int I, bool has_gu, bool x_i8) {
     return w;
 }
 
-int together_edge(const Products& Q, int m, int R, int n) {
-    int best = 0;
-    double least = 0;
-    const int used = std::min(R, n), each = (R + used - 1) / used;
-    struct { double stage, tile, end, alone; } t;
-    for (int edge = 64; edge <= 256; edge *= 2) {
-        if (edge == 256) t = {1.7, 4.6, 0.41, 1.25};
-        else if (edge == 128) t = {0.48, 0.8, 0.39, 0.6};
-        else t = {0.2, 0, 0.44, 0.19};
-        double work = 0, longest = 0, all = 0;
-        for (int i = 0; i < m; ++i) {
-            const Args& G = Q.P[i].G;
-            const double nt = (G.N + edge - 1) / edge;
-            const double mt = Q.sum[i] ? (G.M + edge - 1) / edge : (each + edge - 1) / edge;
-            const double span = ((Q.sum[i] ? each : G.K) + kKE - 1) / kKE;
-            const double tiles = (Q.sum[i] ? n : used) * mt * nt;
-            all += Q.sum[i] ? tiles + (double)n * kXcds : rows_grid(R, n, edge, (int)nt);
-            work += tiles * (span * t.stage + t.tile) / 256;
-            longest = std::max(longest, span);
-        }
-        if (!grid_fits((long)all, tile_threads(edge))) continue;
-        const double us = std::max(longest * t.alone + 5, work + longest * t.end) + 2;
-        if (best == 0 || us < least) {
-            least = us;
-            best = edge;
-        }
-    }
-    return best;
-}
-
 template <int EDGE, int R>
 hipError_t launch_products_ring(const Products& Q, long total, hipStream_t s) {
     auto* k = products_kernel<EDGE, R>;
@@ -331,40 +271,23 @@ hipError_t launch_products_ring(const Products& Q, long total, hipStream_t s) {
 }
 
 template <int EDGE>
-hipError_t launch_products(Products Q, int m, hipStream_t s) {
-    long total = 0, used = 0;
+hipError_t launch_products(Products Q, const GroupSize* sizes, int m, hipStream_t s) {
+    long total = 0, tiles = 0;
     for (int i = 0; i < m; ++i) {
         Grouped& P = Q.P[i];
         Q.first[i] = (int)total;
-        if (Q.sum[i]) {
-            P.G.mt = (P.G.M + EDGE - 1) / EDGE;
-            P.G.nt = (P.G.N + EDGE - 1) / EDGE;
-            P.nt = P.G.mt * P.G.nt;
-            total += (long)P.n * die_share(P.nt) * kXcds;
-            used += (long)P.n * P.nt;
-        } else {
-            P.nt = (P.G.N + EDGE - 1) / EDGE;
-            total += rows_grid(P.R, P.n, EDGE, P.nt);
-            used += even_tiles(P.R, P.n, EDGE) * P.nt;
-        }
+        P.G.mt = (sizes[i].M + EDGE - 1) / EDGE;
+        P.G.nt = (sizes[i].N + EDGE - 1) / EDGE;
+        P.nt = Q.sum[i] ? P.G.mt * P.G.nt : P.G.nt;
+        total += group_grid(sizes[i], P.R, P.n, EDGE);
+        tiles += group_tiles(sizes[i], P.R, P.n, EDGE);
         if (!grid_fits(total, tile_threads(EDGE))) return hipErrorInvalidValue;
     }
     for (int i = m; i < 4; ++i) Q.first[i] = (int)total;
     if constexpr (EDGE < 256) {
-        if (used <= (EDGE == 64 ? 512 : 256)) return launch_products_ring<EDGE, 10>(Q, total, s);
+        if (ring_of(EDGE, tiles) == 10) return launch_products_ring<EDGE, 10>(Q, total, s);
     }
     return launch_products_ring<EDGE, 5>(Q, total, s);
-}
-
-// The weight gradients as a stream of 256 x 256 tiles: where these give every CU one.
-// (With fewer, smaller tiles in one launch with dx.)
-long stream_tiles(const Grouped* P, int m) {
-    long tiles = 0;
-    for (int i = 0; i < m; ++i) {
-        const Args& G = P[i].G;
-        tiles += (long)P[i].n * ((G.M + kStreamM - 1) / kStreamM) * ((G.N + kStreamN - 1) / kStreamN);
-    }
-    return tiles;
 }
 
 hipError_t launch_stream(const Grouped* todo, int m, hipStream_t s) {
@@ -417,13 +340,10 @@ hipError_t gateup(const ExpertsProblem& p, const void* x, void* h, float* gu, bo
 // Whether every product has a tiling whose grid holds it.
 bool fits(int R, int n, int H, int I, bool grads) {
     if (R == 0) return true;
-    if (!rows_edge(R, n, 2L * I, H)) return false;
-    if (!grads) return rows_edge(R, n, H, I) != 0;
-    if (!rows_edge(R, n, I, H)) return false;
-    // the largest tiles take the fewest workgroups
-    const auto tiles = [](long v) { return (v + 255) / 256; };
-    const double all = (double)rows_grid(R, n, 256, (int)tiles(H)) + (double)n * ((tiles(2L * I) + tiles(I)) * tiles(H) + 2 * kXcds);
-    return all < 4e9 && grid_fits((long)all, tile_threads(256));
+    if (!rows_edge(R, n, 2L * I, H, kKE)) return false;
+    if (!grads) return rows_edge(R, n, H, I, kKE) != 0;
+    const GroupSize all[3] = {{0, H, turn_of(I) + I, false}, {2 * I, H, 0, true}, {H, I, 0, true}};
+    return rows_edge(R, n, I, H, kKE) && rows_edge(R, n, H, turn_of(I) + I, kKE) && group_edge(all, 3, R, n, kKE);
 }
 
 }  // namespace
@@ -489,6 +409,7 @@ hipError_t launch_experts_backward(const ExpertsProblem& p, void* ws, hipStream_
         if (e != hipSuccess) return e;
     }
     Products Q{};
+    GroupSize sizes[3];
     int m = 0;
     if (p.dx) {
         Grouped P = base(p, H, turn_of(I) + I);
@@ -498,6 +419,7 @@ hipError_t launch_experts_backward(const ExpertsProblem& p, void* ws, hipStream_
         P.G.B = rows(p.wg, H, H, p.wu);
         P.wstep = one * 2;
         P.G.out = p.dx;
+        sizes[m] = {0, P.G.N, P.G.K, false};
         Q.P[m++] = P;
     }
     const auto weight = [&](const Operand& A, const Operand& B, int M, int N, void* out, void* out2, int msplit) {
@@ -510,6 +432,7 @@ hipError_t launch_experts_backward(const ExpertsProblem& p, void* ws, hipStream_
         P.G.out2 = out2;
         P.G.msplit = msplit;
         Q.sum[m] = 1;
+        sizes[m] = {M, N, 0, true};
         Q.P[m++] = P;
     };
     if (p.dwg || p.dwu) {
@@ -519,15 +442,16 @@ hipError_t launch_experts_backward(const ExpertsProblem& p, void* ws, hipStream_
     }
     if (p.dwd) weight(rows(p.dy, H, H), rows(h, I, I), H, I, p.dwd, nullptr, H);
     if (m == 0) return hipSuccess;
+    if (m == 1 && p.dx) return launch_rows<kCol, kEpiOut>(Q.P[0], s);
     const int sums = p.dx ? 1 : 0;   // the weight gradients follow
-    if (m > sums && stream_tiles(&Q.P[sums], m - sums) >= device_cu_count()) {
+    if (stream_tiles(sizes, m, p.n) >= device_cu_count()) {
         if (p.dx) e = launch_rows<kCol, kEpiOut>(Q.P[0], s);
         return e == hipSuccess ? launch_stream(&Q.P[sums], m - sums, s) : e;
     }
-    switch (together_edge(Q, m, R, p.n)) {
-        case 64: return launch_products<64>(Q, m, s);
-        case 128: return launch_products<128>(Q, m, s);
-        case 256: return launch_products<256>(Q, m, s);
+    switch (group_edge(sizes, m, R, p.n, kKE)) {
+        case 64: return launch_products<64>(Q, sizes, m, s);
+        case 128: return launch_products<128>(Q, sizes, m, s);
+        case 256: return launch_products<256>(Q, sizes, m, s);
         default: return hipErrorInvalidValue;
     }
 }

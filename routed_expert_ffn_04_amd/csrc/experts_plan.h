@@ -1,0 +1,100 @@
+// Tiles and grids of the experts' products, from their sizes alone (plain C++, no
+// device code).  How the rows are spread over the experts is not known to the host: a
+// grid has room for any spread, times are estimated for an even one.
+#pragma once
+#include "tile_plan.h"
+
+namespace moe {
+namespace gemm {
+
+constexpr int kDies = 8;
+constexpr int kStreamEdge = 256;   // tiles of the streamed weight gradients
+
+// Most of an expert's `tiles` that a die takes.
+constexpr int die_share(int tiles) { return (tiles + kDies - 1) / kDies; }
+
+// Row tiles that the experts' rows can fill: one more than they fill together, for
+// every expert that has rows; and those of an even spread.
+inline long row_tiles(int R, int n, int edge) { return (long)R / edge + std::min(R, n); }
+inline int even_rows(int R, int n) { return (R + std::min(R, n) - 1) / std::min(R, n); }
+inline long even_tiles(int R, int n, int edge) { return (long)std::min(R, n) * ((even_rows(R, n) + edge - 1) / edge); }
+
+// Workgroups of a product over the experts' rows: a multiple of the dies, which share
+// the tiles that there are evenly.
+inline long rows_grid(int R, int n, int edge, long nt) { return (row_tiles(R, n, edge) * nt + kDies - 1) / kDies * kDies; }
+
+// Tile edge of a product over the experts' rows, by the estimated time; 0: no grid
+// holds it.  cols: MFMA columns (gate/up: both matrices').
+inline int rows_edge(int R, int n, long cols, int K, int stage_elems) {
+    int best = 0;
+    double least = 0;
+    for (int edge = 64; edge <= 256; edge *= 2) {
+        const long nt = (cols + edge - 1) / edge;
+        if (!grid_fits(rows_grid(R, n, edge, nt), tile_threads(edge))) continue;
+        const double us = tiling_us(edge, even_tiles(R, n, edge) * nt, (K + stage_elems - 1) / stage_elems);
+        if (best == 0 || us < least) {
+            least = us;
+            best = edge;
+        }
+    }
+    return best;
+}
+
+// Half-stages in the ring of tiles: ten where there are no more of them than then run at once.
+inline int ring_of(int edge, long tiles) { return (edge == 64 && tiles <= 512) || (edge == 128 && tiles <= 256) ? 10 : 5; }
+
+// The products of the backward pass that do not depend on each other: dx, over the
+// rows, and weight gradients (sum), for every expert.
+struct GroupSize {
+    int M, N, K;   // dx: N, K; a gradient: M, N
+    bool sum;
+};
+
+// The weight gradients go as a stream of 256 x 256 tiles where these give every CU
+// one: with fewer (up to 256 of them were tried), smaller tiles in one launch with dx are faster.
+inline long stream_tiles(const GroupSize* p, int m, int n) {
+    long tiles = 0;
+    for (int i = 0; i < m; ++i)
+        if (p[i].sum) tiles += (long)n * ((p[i].M + kStreamEdge - 1) / kStreamEdge) * ((p[i].N + kStreamEdge - 1) / kStreamEdge);
+    return tiles;
+}
+
+// Workgroups of one of them in a launch together, and how many of these have a tile with rows spread evenly.
+inline long group_grid(const GroupSize& p, int R, int n, int edge) {
+    const long nt = (p.N + edge - 1) / edge, mt = (p.M + edge - 1) / edge;
+    return p.sum ? (long)n * ((mt * nt + kDies - 1) / kDies * kDies) : rows_grid(R, n, edge, nt);
+}
+inline long group_tiles(const GroupSize& p, int R, int n, int edge) {
+    const long nt = (p.N + edge - 1) / edge, mt = (p.M + edge - 1) / edge;
+    return p.sum ? n * mt * nt : even_tiles(R, n, edge) * nt;
+}
+
+// Tile edge of a launch together (times as in plan_together); 0: no grid holds it.
+inline int group_edge(const GroupSize* p, int m, int R, int n, int stage_elems) {
+    struct { double stage, tile, end, alone; } t;
+    int best = 0;
+    double least = 0;
+    for (int edge = 64; edge <= 256; edge *= 2) {
+        if (edge == 256) t = {1.7, 4.6, 0.41, 1.25};
+        else if (edge == 128) t = {0.48, 0.8, 0.39, 0.6};
+        else t = {0.2, 0, 0.44, 0.19};
+        double work = 0, longest = 0;
+        long all = 0;
+        for (int i = 0; i < m; ++i) {
+            const double span = ((p[i].sum ? even_rows(R, n) : p[i].K) + stage_elems - 1) / stage_elems;
+            all += group_grid(p[i], R, n, edge);
+            work += group_tiles(p[i], R, n, edge) * (span * t.stage + t.tile) / 256;
+            longest = std::max(longest, span);
+        }
+        if (!grid_fits(all, tile_threads(edge))) continue;
+        const double us = std::max(longest * t.alone + 5, work + longest * t.end) + 2;
+        if (best == 0 || us < least) {
+            least = us;
+            best = edge;
+        }
+    }
+    return best;
+}
+
+}  // namespace gemm
+}  // namespace moe

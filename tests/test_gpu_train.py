@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import routed_expert_ffn_04_amd as moe
+from experts_plan_cases import EXPERTS as TILINGS, spread
 from test_gpu_dense import BF, F32, HALF, I8, gamma, outbuf, rand, within
 
 pytestmark = pytest.mark.gpu
@@ -365,6 +366,94 @@ def test_experts_backward(sizes, H, I):
     _, pair = moe.experts_ffn(c.x, c.offsets, c.bank, want_gu=True, gu_dtype=I8)
     xp = moe.quant_i8x16(c.x)
     c.check_backward(moe.experts_ffn_backward(c.dy, xp, c.offsets, c.bank, pair), pair, xp)
+
+
+@pytest.mark.parametrize("R,n,H,I", sorted({sizes for _, _, sizes in TILINGS}))
+def test_experts_in_every_tiling(R, n, H, I):
+    """Sizes that reach every tiling of every product, both kinds of checkpoints."""
+    c = Experts(spread(R, n), H, I, 2)
+    y, gu = moe.experts_ffn(c.x, c.offsets, c.bank, want_gu=True)
+    c.check_forward(y, gu, False)
+    c.check_backward(moe.experts_ffn_backward(c.dy, c.x, c.offsets, c.bank, gu))
+    c.check_backward(moe.experts_ffn_backward(c.dy, c.x, c.offsets, c.bank, gu, need=("dx",)))
+    y8, pair = moe.experts_ffn(c.x, c.offsets, c.bank, want_gu=True, gu_dtype=I8)
+    assert torch.equal(y8, y)
+    c.check_forward(y, pair, True)
+    c.check_backward(moe.experts_ffn_backward(c.dy, c.x, c.offsets, c.bank, pair), pair)
+
+
+def test_experts_many():
+    """As many experts as there may be, most of them without rows."""
+    sizes = [(3 * e) % 7 if e % 5 == 0 else 0 for e in range(1024)]
+    c = Experts(sizes, 24, 40, 7)
+    y, gu = moe.experts_ffn(c.x, c.offsets, c.bank, want_gu=True)
+    c.check_forward(y, gu, False)
+    c.check_backward(moe.experts_ffn_backward(c.dy, c.x, c.offsets, c.bank, gu))
+
+
+def test_experts_offsets_past_the_rows():
+    """Offsets that are not what they should be are cut to the rows there are: nothing outside is written."""
+    c = Experts([40, 50, 30], 264, 136, 8)
+    for bad in ([0, 40, 1000, 2 ** 31 - 1], [-5, 130, 20, 90], [2 ** 31 - 1, 0, 0, 0]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        y, guard = outbuf((c.R, c.H), BF)
+        gu, guard_gu = outbuf((c.R, 2 * c.I), F32)
+        moe.experts_ffn(c.x, off, c.bank, want_gu=True, out=y, gu=gu)
+        moe.experts_ffn_backward(c.dy, c.x, off, c.bank, gu)
+        guard()
+        guard_gu()
+
+
+def test_experts_of_more_elements_than_an_int32_counts():
+    """Rows before the experts' own, zeros here, push those past 2^31 elements of the saved g and u."""
+    H, I, sizes = 72, 1032, [70, 0, 300, 33]
+    n = sum(sizes)
+    before = (1 << 31) // (2 * I) + 1000
+    c = Experts(sizes, H, I, 9)
+    off = c.offsets + before
+    x, dy = (torch.zeros(before + n, H, dtype=BF, device="cuda") for _ in range(2))
+    x[before:], dy[before:] = c.x, c.dy
+    assert before * 2 * I > 1 << 31
+    y, gu = moe.experts_ffn(x, off, c.bank, want_gu=True)
+    c.check_forward(y[before:], gu[before:], False)
+    dx, *dw = moe.experts_ffn_backward(dy, x, off, c.bank, gu)
+    c.check_backward([dx[before:], *dw])
+    del gu, y, dx
+    y, pair = moe.experts_ffn(x, off, c.bank, want_gu=True, gu_dtype=I8)
+    held = tuple(t[before:] for t in pair)
+    c.check_forward(y[before:], held, True)
+    kept = moe.quant_i8x16(x)
+    dx, *dw = moe.experts_ffn_backward(dy, kept, off, c.bank, pair)
+    c.check_backward([dx[before:], *dw], held, tuple(t[before:] for t in kept))
+
+
+def test_rows_of_more_elements_than_an_int32_counts():
+    """The last of the sorted rows lie past 2^31 elements."""
+    T, k, H = 150100, 2, 7168
+    assert T * k * H > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(T, H, dtype=BF, device="cuda").normal_(generator=g)
+    dest = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32)
+    some = torch.cat([torch.arange(5), torch.arange(T - 5, T)]).cuda()
+    at = dest.view(T, k)[some].long()
+    xs = moe.dispatch(x, dest, k)
+    assert torch.equal(xs[at], x[some].unsqueeze(1).expand(-1, k, -1))
+    last = torch.tensor([T * k - 1], device="cuda")
+    assert torch.equal(xs[last], x[(dest == T * k - 1).nonzero()[0] // k])
+    dx = moe.dispatch_backward(xs, dest, k)
+    assert torch.equal(dx[some], (2 * x[some].float()).to(BF))
+    w = torch.rand(T, k, generator=g, device="cuda")
+    dy, dw = moe.combine_backward(x, xs, dest, w)
+    ref = w[some].double().unsqueeze(2) * x[some].double().unsqueeze(1)
+    within(dy[at], ref, (HALF[BF] + 2.0 ** -24) * 1.01 * ref.abs(), "dy")
+    sq = x[some].double().square().sum(1, keepdim=True).expand(-1, k)
+    within(dw[some], sq, gamma(H) * sq, "dw")
+    del xs, dx, dy
+    big = torch.empty(T * k, H, dtype=BF, device="cuda").normal_(generator=g)
+    q, e = moe.quant_i8x16(big)
+    rq, re = exact_pair(big[-7:])
+    assert torch.equal(q[-7:], rq) and torch.equal(e[-7:], re)
+    assert torch.equal(moe.dequant_i8x16(q, e)[-7:].double(), values((q[-7:], e[-7:])))
 
 
 def test_experts_agree_with_dense():
