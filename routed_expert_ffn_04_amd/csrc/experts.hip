@@ -32,6 +32,7 @@ struct Grouped {
     const int32_t* offsets;
     int n, R;              // experts; rows there are
     int nt;                // kRows: column tiles; kSum: tiles of an expert
+    int cus;               // kRows, 256-row tiles: CUs of a die
 };
 
 // Position in the order of `total` tiles, of which every die takes one contiguous
@@ -44,10 +45,15 @@ __device__ __forceinline__ int in_die_order(int block, int total) {
 
 // Workgroup `block`'s among all experts' row tiles: the expert, the tile within it and
 // the expert's rows; false past the last one.  Every wave does this by itself.
+//
+// cuts (256-row tiles): where a die's tiles leave up to half of its CUs without work in
+// their last round, the tiles of that round are cut into halves of 128 rows, which
+// take 0.6 of a tile's time each (half_tile).
 struct Place {
     int e, t, first, m;
+    int half;   // 0: the whole tile, 1: its upper, 2: its lower half
 };
-__device__ __forceinline__ bool find_rows(const Grouped& P, int edge, int block, Place& at) {
+__device__ __forceinline__ bool find_rows(const Grouped& P, int edge, int block, bool cuts, Place& at) {
     const int lane = threadIdx.x % kWave;
     auto tiles = [&](int e) {
         if (e >= P.n) return 0;
@@ -64,6 +70,15 @@ __device__ __forceinline__ bool find_rows(const Grouped& P, int edge, int block,
     };
     int total = 0;
     for (int e0 = 0; e0 < P.n; e0 += kWave) total += __builtin_amdgcn_readlane(scan(tiles(e0 + lane)), kWave - 1);
+    at.half = 0;
+    if (cuts) {
+        const int x = block % kXcds, j = block / kXcds;
+        const int mine = total / kXcds + (x < total % kXcds ? 1 : 0), last = mine % P.cus, whole = mine - last;
+        if (2 * last <= P.cus && last <= kMostCuts && j >= whole) {
+            at.half = 1 + (j - whole) % 2;
+            block = (whole + (j - whole) / 2) * kXcds + x;
+        }
+    }
     int t = in_die_order(block, total);
     if (t < 0) return false;
     for (int e0 = 0; e0 < P.n; e0 += kWave) {
@@ -139,13 +154,15 @@ __global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per
     Grouped P) {
     constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
     Place at;
-    if (!find_rows(P, EDGE, blockIdx.x, at)) return;
+    if (!find_rows(P, EDGE, blockIdx.x, EDGE == 256, at)) return;
     const Args G = rows_of<EPI>(P, at);
     int tm, tn;
     band_of(at.t, (at.m + EDGE - 1) / EDGE, P.nt, tm, tn);
     if constexpr (EDGE == 256) {
-        if (at.m - tm * EDGE <= EDGE / 2) {
-            half_tile<LB, EPI, GU>(G, tm * EDGE, tn);
+        const int m0 = tm * EDGE + (at.half == 2 ? EDGE / 2 : 0);
+        if (m0 >= at.m) return;
+        if (at.half || at.m - m0 <= EDGE / 2) {
+            half_tile<LB, EPI, GU>(G, m0, tn);
             return;
         }
     }
@@ -172,7 +189,7 @@ __global__ __launch_bounds__(tile_threads(EDGE)) __attribute__((amdgpu_waves_per
         tile_at<kBf16, kCol, kCol, kEpiOut, false, EDGE, EDGE, R>(G, tm, tn, 0);
     } else {
         Place at;
-        if (!find_rows(P, EDGE, b - Q.first[i], at)) return;
+        if (!find_rows(P, EDGE, b - Q.first[i], false, at)) return;
         const Args G = rows_of<kEpiOut>(P, at);
         band_of(at.t, (at.m + EDGE - 1) / EDGE, P.nt, tm, tn);
         tile_at<kBf16, kRow, kCol, kEpiOut, false, EDGE, EDGE, R>(G, tm, tn, 0);
@@ -212,6 +229,7 @@ template <int LB, int EPI, int EDGE>
 hipError_t launch_rows_edge(Grouped P, hipStream_t s) {
     constexpr bool GU = EPI == kEpiGateUp || EPI == kEpiGateUp8;
     P.nt = (P.G.N + (GU ? EDGE / 2 : EDGE) - 1) / (GU ? EDGE / 2 : EDGE);
+    P.cus = std::max(device_cu_count() / kXcds, 1);
     const long grid = rows_grid(P.R, P.n, EDGE, P.nt);
     if (!grid_fits(grid, tile_threads(EDGE))) return hipErrorInvalidValue;
     if constexpr (EDGE < 256) {

@@ -20,8 +20,12 @@ inline int even_rows(int R, int n) { return (R + std::min(R, n) - 1) / std::min(
 inline long even_tiles(int R, int n, int edge) { return (long)std::min(R, n) * ((even_rows(R, n) + edge - 1) / edge); }
 
 // Workgroups of a product over the experts' rows: a multiple of the dies, which share
-// the tiles that there are evenly.
-inline long rows_grid(int R, int n, int edge, long nt) { return (row_tiles(R, n, edge) * nt + kDies - 1) / kDies * kDies; }
+// the tiles that there are evenly, and of 256-row tiles so many more for the second
+// halves of those that are cut (find_rows).
+constexpr int kMostCuts = 16;   // of a die
+inline long rows_grid(int R, int n, int edge, long nt) {
+    return (row_tiles(R, n, edge) * nt + kDies - 1) / kDies * kDies + (edge == 256 ? kDies * kMostCuts : 0);
+}
 
 // Tile edge of a product over the experts' rows, by the estimated time; 0: no grid
 // holds it.  cols: MFMA columns (gate/up: both matrices').
