@@ -27,15 +27,35 @@ inline long rows_grid(int R, int n, int edge, long nt) {
     return (row_tiles(R, n, edge) * nt + kDies - 1) / kDies * kDies + (edge == 256 ? kDies * kMostCuts : 0);
 }
 
-// Tile edge of a product over the experts' rows, by the estimated time; 0: no grid
-// holds it.  cols: MFMA columns (gate/up: both matrices').
+// Estimated time, in us, of a product over the experts' rows by tiles of an edge, for
+// rows spread around an even share: fitted to 80 banks and row counts (4 to 128 experts
+// of 1024 x 512 to 7168 x 2048, 12 to 1200 rows each, shares that differ by a factor of
+// two to three).  Taking the edge with the least of these loses 1.1 % against the best of
+// the three (tiling_us of an even spread: 4.9 %).  The last tile of an expert counts for a part of one, of
+// 256-row tiles as half a one's 0.6 where few rows fill no more.
+inline double rows_us(int edge, int R, int n, long nt, int span) {
+    const double experts = std::min(R, n), rows = R / experts;
+    if (edge == 256) {
+        const double tiles = experts * std::max(rows / 256 + 0.14, 0.6) * nt / 256, full = std::min(1.0, tiles);
+        return std::max(rows < 110 ? 0.6 : 1.0, tiles + 0.12) * (span * (0.91 + 0.12 * full * full) + 10.7);
+    }
+    if (edge == 128) {
+        const double tiles = experts * std::max(rows / 128 + 0.55, 1.0) * nt / 512;
+        return tiles <= 1 ? span * (0.49 + 0.51 * tiles) + 5 : tiles * (span * 0.88 + 6) + 1;
+    }
+    const double tiles = experts * std::max(rows / 64 + 0.42, 1.0) * nt / 256;
+    return std::max(1.0, tiles + 0.14) * (span * 0.19 + 0.47) + 3;
+}
+
+// Tile edge of such a product, by the estimated time; 0: no grid holds it.  cols: MFMA
+// columns (gate/up: both matrices').
 inline int rows_edge(int R, int n, long cols, int K, int stage_elems) {
     int best = 0;
     double least = 0;
     for (int edge = 64; edge <= 256; edge *= 2) {
         const long nt = (cols + edge - 1) / edge;
         if (!grid_fits(rows_grid(R, n, edge, nt), tile_threads(edge))) continue;
-        const double us = tiling_us(edge, even_tiles(R, n, edge) * nt, (K + stage_elems - 1) / stage_elems);
+        const double us = rows_us(edge, R, n, nt, (K + stage_elems - 1) / stage_elems);
         if (best == 0 || us < least) {
             least = us;
             best = edge;

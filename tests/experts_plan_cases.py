@@ -8,17 +8,19 @@ stage.  That the library plans what is written here is checked without a GPU, so
 change of the plans that leaves a tiling untested shows."""
 
 EXPERTS = [
-    ("gateup", "64r10", (1, 1, 8, 8)), ("gateup", "64r5", (40, 40, 8, 400)), ("gateup", "128r10", (355, 5, 200, 2512)),
-    ("gateup", "128r5", (25, 13, 1928, 1904)), ("gateup", "256r5", (1600, 8, 152, 3120)),
-    ("down", "64r10", (7, 2, 24, 40)), ("down", "64r5", (31, 31, 1224, 8)), ("down", "128r10", (1396, 17, 1456, 208)),
-    ("down", "128r5", (95, 35, 1384, 1824)), ("down", "256r5", (4609, 23, 2248, 136)),
-    ("dh", "64r10", (7, 2, 24, 40)), ("dh", "64r5", (49, 46, 8, 720)), ("dh", "128r10", (772, 12, 264, 2304)),
-    ("dh", "128r5", (1220, 19, 8, 2136)), ("dh", "256r5", (3609, 18, 136, 2840)),
-    ("dx", "64r10", (7, 2, 24, 40)), ("dx", "64r5", (31, 31, 1224, 8)), ("dx", "128r10", (959, 14, 1776, 96)),
-    ("dx", "128r5", (20, 14, 3512, 1456)), ("dx", "256r5", (10524, 54, 872, 72)),
-    ("grads", "64r10", (7, 2, 24, 40)), ("grads", "64r5", (49, 46, 8, 208)), ("grads", "128r10", (534, 1, 2048, 400)),
-    ("grads", "128r5", (266, 4, 2544, 328)), ("grads", "256r5", (1464, 3, 2712, 200)), ("grads", "stream", (68, 58, 8, 296)),
-    ("grads", "stream", (4609, 23, 2248, 136)),
+    ("gateup", "64r10", (1, 1, 8, 8)), ("gateup", "64r5", (40, 40, 8, 400)),
+    ("gateup", "256r5", (1600, 8, 152, 3120)), ("gateup", "128r10", (32362, 51, 8, 40)),
+    ("gateup", "128r5", (1053, 22, 8, 1392)), ("gateup", "256r5", (93, 69, 1680, 368)),
+    ("down", "64r10", (7, 2, 24, 40)), ("down", "64r5", (31, 31, 1224, 8)), ("down", "256r5", (4609, 23, 2248, 136)),
+    ("down", "128r10", (3028, 24, 1160, 8)), ("down", "128r5", (32881, 53, 72, 8)),
+    ("down", "256r5", (19, 19, 2768, 1896)), ("dh", "64r10", (7, 2, 24, 40)), ("dh", "64r5", (49, 46, 8, 720)),
+    ("dh", "256r5", (3609, 18, 136, 2840)), ("dh", "128r10", (31682, 64, 24, 80)),
+    ("dh", "128r5", (2892, 62, 8, 968)), ("dh", "256r5", (49, 41, 1784, 1240)), ("dx", "64r10", (7, 2, 24, 40)),
+    ("dx", "64r5", (31, 31, 1224, 8)), ("dx", "256r5", (10524, 54, 872, 72)), ("dx", "128r10", (3028, 24, 1160, 8)),
+    ("dx", "128r5", (32881, 53, 72, 8)), ("dx", "256r5", (69, 42, 1224, 1088)), ("grads", "64r10", (7, 2, 24, 40)),
+    ("grads", "64r5", (49, 46, 8, 208)), ("grads", "128r10", (534, 1, 2048, 400)),
+    ("grads", "128r5", (266, 4, 2544, 328)), ("grads", "256r5", (1464, 3, 2712, 200)),
+    ("grads", "stream", (68, 58, 8, 296)),
 ]
 
 
