@@ -400,14 +400,16 @@ moe_status_t moe_dequant_i8x16(const int8_t* q, const uint8_t* e8, int32_t rows,
  * (another GPU's experts), which are skipped; no row may be named twice.  Rows
  * that are not named stay as they are.  x: [T][H] MOE_F32, MOE_BF16, or MOE_I8: codes of
  * moe_quant_i8x16 with the exponents x_e8 [T][ceil(H / 16)] (NULL otherwise).  xs: [R][H] of x's type,
- * MOE_BF16 for MOE_I8.  H a positive multiple of 8; rows 16-byte aligned (codes 8); T, R and T * k at most 2^30. */
+ * MOE_BF16 for MOE_I8.  H a positive multiple of 8; rows 16-byte aligned (codes 8); T, H, R and T * k at most 2^30
+ * (here and in the two calls below).  xs may not overlap another tensor. */
 moe_status_t moe_dispatch(const void* x, int32_t x_dt, const uint8_t* x_e8, int32_t T, int32_t H, const int32_t* dest,
                           int32_t k, int32_t R, void* xs, void* stream);
 
 /* Gradient of moe_dispatch: dx[t] = add[t] + sum_j dxs[dest[t * k + j]], fp32, in this order
  * (assignments without a row here add nothing).  dxs: [R][H], add: [T][H] or NULL (0;
  * the gradient of x from elsewhere, e.g. the shared expert), dx: [T][H], which may be add itself
- * if their types agree; each MOE_F32 or MOE_BF16, 16-byte aligned, H a positive multiple of 8. */
+ * if their types agree, and may not overlap another tensor otherwise; each MOE_F32 or MOE_BF16, 16-byte
+ * aligned, H a positive multiple of 8. */
 moe_status_t moe_dispatch_backward(const void* dxs, int32_t dxs_dt, int32_t R, const int32_t* dest, int32_t T,
                                    int32_t k, int32_t H, const void* add, int32_t add_dt, void* dx, int32_t dx_dt,
                                    void* stream);
@@ -417,8 +419,8 @@ moe_status_t moe_dispatch_backward(const void* dxs, int32_t dxs_dt, int32_t R, c
  * (the gradient of y_sh is dout itself).  y: what moe_combine read, [R][H] MOE_F32, MOE_BF16 or
  * MOE_E4M3 with y_scale; may be NULL without dw.  dy: [R][H] MOE_F32 or MOE_BF16, rows that
  * dest does not name stay as they are; dw: [T][k] fp32, 0 for assignments without a row
- * here.  Either may be NULL.  Sums are fp32.  H a positive multiple of 8 (128 with MOE_E4M3 y); rows
- * 16-byte aligned (codes 8). */
+ * here.  Either may be NULL; neither may overlap another tensor.  Sums are fp32.  H a positive multiple of 8
+ * (128 with MOE_E4M3 y); rows 16-byte aligned (codes 8). */
 moe_status_t moe_combine_backward(const void* dout, int32_t dout_dt, const void* y, int32_t y_dt, const float* y_scale,
                                   int32_t R, const int32_t* dest, const float* topk_w, int32_t T, int32_t k, int32_t H,
                                   void* dy, int32_t dy_dt, float* dw, void* stream);

@@ -94,3 +94,12 @@ def test_spread(product, tiling, sizes):
     R, n, _, _ = sizes
     rows = spread(R, n)
     assert sum(rows) == R and len(rows) == n and (n == 1 or 0 in rows)
+
+
+def test_rows_longer_than_their_columns_count_are_refused():
+    """Columns are counted in 32 bits, a few thousand past the row's end."""
+    L, wide = moe.lib(), (1 << 31) - 8
+    assert L.moe_dispatch(P, moe.BF16, None, 1, wide, P, 1, 1, P, None) == moe.MOE_ERR_UNSUPPORTED
+    assert L.moe_dispatch_backward(P, moe.BF16, 1, P, 1, 1, wide, None, 0, P, moe.BF16, None) == moe.MOE_ERR_UNSUPPORTED
+    assert L.moe_combine_backward(P, moe.BF16, P, moe.BF16, None, 1, P, P, 1, 1, wide, P, moe.BF16, P,
+                                  None) == moe.MOE_ERR_UNSUPPORTED
