@@ -110,7 +110,10 @@ __global__ __launch_bounds__(256) void gather_kernel(const void* __restrict__ dx
 // ---- gradients of combine: a wave takes one assignment, so the sum over its row stays in
 // the wave; the waves of a workgroup share their tokens' rows in the caches
 enum { kYNone = 0, kYF32 = 1, kYBf16 = 2, kYE4m3 = 3 };
-constexpr int kGradWaves = 8, kAhead = 4;   // pieces of 64 lanes whose loads go out together
+// kAhead pieces of 64 lanes have their loads out together.  Eight of them and four waves a
+// workgroup, against four and eight: 30018 fp32 rows of 2056 110.7 us against 114.5 (4.8 TB/s), e4m3 rows
+// 317 against 323, 128 tokens of 8 bf16 rows 9.0 against 10.1.
+constexpr int kGradWaves = 4, kAhead = 8;
 
 template <int Y, bool D_F32, bool DY_F32, bool NT>
 __global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
