@@ -505,6 +505,36 @@ def test_experts_no_rows():
     assert all(bool((d == 0).all()) for d in grads[1:])
 
 
+def test_experts_none_with_rows():
+    """Many experts, none with rows: streamed gradients of zeros, and nothing else written."""
+    c = Experts([0] * 64, 520, 512, after=300)
+    y, guard = outbuf((c.R, c.H), BF)
+    y, gu = moe.experts_ffn(c.x, c.offsets, c.bank, want_gu=True, out=y)
+    assert bool((y == 77).all())
+    grads = moe.experts_ffn_backward(c.dy, c.x, c.offsets, c.bank, gu)
+    assert all(bool((d == 0).all()) for d in grads[1:])
+    guard()
+
+
+def test_experts_part_of_a_bank():
+    """Offsets that begin inside a longer list (a part of the experts, on rows of all) and x kept in 8 bits alone."""
+    c = Experts([33, 70, 0, 130, 9], 264, 136, 11)
+    part = moe.Experts(c.wg[1:4], c.wu[1:4], c.wd[1:4])
+    a, b = int(c.ends[1]), int(c.ends[4])
+    whole, guard = outbuf((c.R, c.H), BF)
+    y, gu = moe.experts_ffn(c.x, c.offsets[1:5], part, want_gu=True, out=whole)
+    assert bool((y[:a] == 77).all()) and bool((y[b:] == 77).all())
+    all_y, all_gu = moe.experts_ffn(c.x, c.offsets, c.bank, want_gu=True)
+    assert torch.equal(y[a:b], all_y[a:b]) and torch.equal(gu[a:b], all_gu[a:b])
+    guard()
+    xp = moe.quant_i8x16(c.x)
+    dx, *dw = moe.experts_ffn_backward(c.dy, xp, c.offsets[1:5], part)
+    for e in (1, 2, 3):
+        lo, hi = c.ends[e], c.ends[e + 1]
+        r = Rows(values((xp[0][lo:hi], xp[1][lo:hi])), c.dy[lo:hi], c.wg[e], c.wu[e], c.wd[e])
+        check_grads(r, [dx] + dw, lo, hi, e - 1)
+
+
 # ---------------------------------------------------------------- the dense block with checkpoints
 
 DENSE = [(1, 8, 8), (1, 256, 512), (16, 1024, 520), (17, 264, 136), (64, 256, 512), (129, 136, 264), (257, 2056, 1336),
