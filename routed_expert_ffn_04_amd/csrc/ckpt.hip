@@ -1,7 +1,7 @@
 // Activation checkpoints in 8 bits (format: i8x16.h): moe_quant_i8x16 and
 // moe_dequant_i8x16.  Memory-bound: a lane takes eight consecutive columns of a
 // row (one 16-byte bf16 load, or two fp32 ones; one 8-byte access of the codes), two
-// neighbouring lanes a block.
+// neighbouring lanes a block.  16384 x 7168 from bf16 67 us (5.3 TB/s), back 65 (5.5).
 #include "dense.h"
 #include "gffn_common.h"
 #include "i8x16.h"

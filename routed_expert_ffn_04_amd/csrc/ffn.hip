@@ -1,4 +1,5 @@
-// Dense gated FFN block and its gradients in bf16 (moe_ffn, moe_ffn_backward).
+// Dense gated FFN block and its gradients in bf16 (moe_ffn, moe_ffn_backward; with
+// checkpoints in 8 bits: moe_ffn_ckpt, moe_ffn_ckpt_backward).
 //   g = x Wg^T, u = x Wu^T, h = silu(g) u, y = h Wd^T      (weights output-major)
 // One kernel forms both projections of the same columns side by side, applies
 // the activation and the product in its epilogue and writes h once.
@@ -15,6 +16,11 @@
 // the matrix cores take them; g and u are kept in fp32, because rounding them
 // as well would put a second error of the same size on dx and the gate and up
 // gradients.  All sums are fp32.
+//
+// Checkpoints in 8 bits (i8x16.h), where the caller asks for them: the gate/up epilogue
+// writes the codes of g and u instead of their fp32 values, and that of dh reads them.  x
+// is restored once for the weight gradients, whose tiles load straight into LDS: 16 us
+// for 4096 x 7168, of 950 for the block forward and back (7168 x 2048).
 #include <algorithm>
 #include <utility>
 
