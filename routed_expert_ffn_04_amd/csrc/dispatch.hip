@@ -23,6 +23,16 @@ namespace moe {
 
 namespace {
 
+// Workgroup's place where every die takes one contiguous run of the `blocks` there are, so that the
+// workgroups of a token share its row in one L2 (workgroups go to the dies in turn).  Tokens' pieces:
+// 16384 tokens to 8 rows of 7168, inputs in turn, 415 us against 428 (its gradient 375 either way).
+// Assignments, where rows are whole lines: e4m3 rows 311 against 318 us (fp32 rows of 2056 110.7
+// against 109.2, so not there).
+__device__ __forceinline__ uint32_t in_die_order(uint32_t block, uint32_t blocks) {
+    const uint32_t x = block % kXcds, base = blocks / kXcds, extra = blocks % kXcds;
+    return x * base + min(x, extra) + block / kXcds;
+}
+
 // Pieces of a token's row: 16 bytes of what is written or summed.  Long rows (LONG): a
 // workgroup takes U * 256 pieces of one token, so that the token and with it its rows' numbers
 // are uniform.  Short ones: one piece a lane, several tokens a workgroup.
@@ -31,8 +41,9 @@ struct Piece {
     int t, c;
     __device__ __forceinline__ Piece(int pieces, int slabs, int per) {
         if constexpr (LONG) {
-            t = (int)(blockIdx.x / (uint32_t)slabs);
-            c = (int)(blockIdx.x - (uint32_t)t * slabs) * (U * 256) + (int)threadIdx.x;
+            const uint32_t b = in_die_order(blockIdx.x, gridDim.x);
+            t = (int)(b / (uint32_t)slabs);
+            c = (int)(b - (uint32_t)t * slabs) * (U * 256) + (int)threadIdx.x;
         } else {
             const int r = (int)threadIdx.x / pieces;
             t = r < per ? (int)(blockIdx.x * per + r) : 0x7fffffff;
@@ -112,7 +123,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const void* __restrict__ dx
 enum { kYNone = 0, kYF32 = 1, kYBf16 = 2, kYE4m3 = 3 };
 // kAhead pieces of 64 lanes have their loads out together.  Eight of them and four waves a
 // workgroup, against four and eight: 30018 fp32 rows of 2056 110.7 us against 114.5 (4.8 TB/s), e4m3 rows
-// 317 against 323, 128 tokens of 8 bf16 rows 9.0 against 10.1.
+// 317 against 323 us, 128 tokens of 8 bf16 rows 9.0 against 10.1.
 constexpr int kGradWaves = 4, kAhead = 8;
 
 template <int Y, bool D_F32, bool DY_F32, bool NT>
@@ -122,7 +133,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
     float* __restrict__ dw) {
     constexpr int C = D_F32 || DY_F32 || Y == kYF32 ? 4 : 8;   // 16 bytes a lane of the wider ones
     const int lane = threadIdx.x % kWave;
-    const long f = (long)blockIdx.x * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const long f = (long)(NT ? in_die_order(blockIdx.x, gridDim.x) : blockIdx.x) * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (f >= n) return;
     const long t = f / k;
     const int r = dest[f];
