@@ -10,7 +10,8 @@
 //
 // Sorted rows are met once, and there are many more of them than the caches hold, so
 // they go past the caches' usual order (NT) where a row is whole lines: dispatch of 16384
-// tokens to 8 of 7168 columns in bf16 437 -> 355 us (5.9 TB/s), its gradient 420 -> 376.  Rows
+// tokens to 8 of 7168 columns in bf16 437 -> 355 us for the same tokens again, which the caches
+// hold (5.9 TB/s written and read; 415 for others every time, 5.1), its gradient 420 -> 376.  Rows
 // of other lengths keep the usual one, which joins the pieces of a line (2056 columns:
 // 45 us, against 63).  Row numbers that are the same in a whole wave are read
 // through the scalar cache: the gradient took 532 us with vector loads of them.
@@ -222,7 +223,7 @@ bool fits(long blocks, int threads) { return blocks <= 0xffffffffL / threads; }
 // Whether the rows of a matrix are whole lines.
 bool whole_lines(const void* p, size_t row_bytes) { return ((uintptr_t)p | row_bytes) % 128 == 0; }
 
-constexpr int kU = 2;   // 512 pieces a workgroup: 355 us against 388 with 256 and 364 with 1024 (see above)
+constexpr int kU = 2;   // 512 pieces a workgroup: 415 us against 424 with 256 and 417 with 1024 (see in_die_order)
 
 }  // namespace
 
