@@ -960,7 +960,8 @@ def combine_backward(dout, y_perm, dest, topk_w, *, y_scale=None, R=None, dy_dty
     if there is not None:
         with there:
             return combine_backward(dout, y_perm, dest, topk_w, y_scale=y_scale, R=R, dy_dtype=dy_dtype, need=need, dy=dy)
-    if not set(need) <= {"dy", "dw"}:
+    want_dy, want_dw = "dy" in need, "dw" in need
+    if want_dy + want_dw != len(need):
         raise ValueError(f"need: {need}")
     if topk_w.dim() != 2:
         raise ValueError(f"topk_w has shape {tuple(topk_w.shape)}, expected [T][k]")
@@ -974,9 +975,8 @@ def combine_backward(dout, y_perm, dest, topk_w, *, y_scale=None, R=None, dy_dty
     if not 0 <= R <= _MOST:
         raise ValueError(f"combine_backward: R={R}")
     y_dt = F32
-    want_dw = "dw" in need
     if y_perm is not None:
-        fp8 = _is_fp8(y_perm.dtype)
+        fp8 = y_perm.dtype not in _FLOATS and _is_fp8(y_perm.dtype)
         _tensor(dev, "y_perm", y_perm, (R, H), (y_perm.dtype,) if fp8 else _FLOATS)
         if fp8 != (y_scale is not None):
             raise ValueError("combine_backward: y_scale goes with e4m3 y_perm")
@@ -989,11 +989,11 @@ def combine_backward(dout, y_perm, dest, topk_w, *, y_scale=None, R=None, dy_dty
         raise TypeError(f"combine_backward: dy {dy_dtype}")
     _tensor(dev, "dout", dout, (T, H), _FLOATS)
     _tensor(dev, "dy", dy, (R, H), (dy_dtype,))
-    if "dy" not in need:
+    if not want_dy:
         dy = None
     elif dy is None:
         dy = _empty(dout, (R, H), dy_dtype)
-    dw = _empty(topk_w, (T, k), torch.float32) if want_dw else None
+    dw = torch.empty_like(topk_w) if want_dw else None
     L = _lib or lib()
     _check(L.moe_combine_backward(dout.data_ptr(), _CODE[dout.dtype], _ptr(y_perm), y_dt, _ptr(y_scale), R, dest.data_ptr(),
                                   topk_w.data_ptr(), T, k, H, _ptr(dy), _CODE[dy_dtype], _ptr(dw), _current(dev)))

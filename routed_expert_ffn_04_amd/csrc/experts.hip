@@ -93,6 +93,8 @@ __device__ __forceinline__ bool find_rows(const Grouped& P, int edge, int block,
             const int l = __builtin_ctzll(past);
             at.e = e0 + l;
             at.t = t - __builtin_amdgcn_readlane(upto - own, l);
+            // (offsets that do not ascend can name more tiles than 32 bits count)
+            if ((unsigned)at.t >= (unsigned)__builtin_amdgcn_readlane(own, l)) return false;
             at.first = __builtin_amdgcn_readfirstlane(rows_before(P.offsets, at.e, P.R));
             at.m = __builtin_amdgcn_readfirstlane(rows_before(P.offsets, at.e + 1, P.R)) - at.first;
             return true;
