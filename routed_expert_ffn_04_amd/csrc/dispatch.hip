@@ -120,29 +120,32 @@ __global__ __launch_bounds__(256) void gather_kernel(const void* __restrict__ dx
 }
 
 // ---- gradients of combine: a wave takes one assignment, so the sum over its row stays in
-// the wave; the waves of a workgroup share their tokens' rows in the caches
+// the wave; the waves of a workgroup share their tokens' rows in the caches.  S = 2: two
+// waves take one, where these are no more than the SIMDs and a wave would go over its row twice (device time,
+// rows of 7168 bf16, 128 / 512 / 1024 / 2048 of them: 3.9 / 4.9 / 7.0 / 14.2 us against 5.0 / 6.3 / 8.0 / 13.4).
 enum { kYNone = 0, kYF32 = 1, kYBf16 = 2, kYE4m3 = 3 };
 // kAhead pieces of 64 lanes have their loads out together.  Eight of them and four waves a
 // workgroup, against four and eight: 30018 fp32 rows of 2056 110.7 us against 114.5 (4.8 TB/s), e4m3 rows
 // 317 against 323 us, 128 tokens of 8 bf16 rows 9.0 against 10.1.
 constexpr int kGradWaves = 4, kAhead = 8;
 
-template <int Y, bool D_F32, bool DY_F32, bool NT>
+template <int Y, bool D_F32, bool DY_F32, bool NT, int S>
 __global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
     const void* __restrict__ dout, const void* __restrict__ y, const float* __restrict__ y_scale,
     const int32_t* __restrict__ dest, const float* __restrict__ w, long n, int k, int H, int R, void* __restrict__ dy,
     float* __restrict__ dw) {
     constexpr int C = D_F32 || DY_F32 || Y == kYF32 ? 4 : 8;   // 16 bytes a lane of the wider ones
     const int lane = threadIdx.x % kWave;
-    const long f = (long)(NT ? in_die_order(blockIdx.x, gridDim.x) : blockIdx.x) * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (f >= n) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const long f = (long)(NT ? in_die_order(blockIdx.x, gridDim.x) : blockIdx.x) * (kGradWaves / S) + wave / S;
+    if (S == 1 && f >= n) return;
     const long t = f / k;
-    const int r = dest[f];
+    const int r = f < n ? dest[f] : -1;
     float sum = 0.0f;
     if ((unsigned)r < (unsigned)R) {
         const float wf = w[f];
         const size_t from = (size_t)t * H, to = (size_t)r * H;
-        for (int c0 = lane * C; c0 < H; c0 += kAhead * kWave * C) {
+        for (int c0 = (wave % S * (kAhead * kWave) + lane) * C; c0 < H; c0 += S * kAhead * kWave * C) {
             Raw<D_F32, C> d[kAhead];
             Raw<Y == kYF32, C> v[kAhead];   // e4m3: the first word or two of it
             float scale[kAhead];
@@ -200,7 +203,17 @@ __global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
     if constexpr (Y != kYNone) {
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1) sum += __shfl_xor(sum, m, kWave);
-        if (lane == 0) dw[f] = sum;
+        if constexpr (S == 1) {
+            if (lane == 0) dw[f] = sum;
+        } else {
+            __shared__ float part[kGradWaves];
+            if (lane == 0) part[wave] = sum;
+            __syncthreads();
+            if (lane == 0 && wave % S == 0 && f < n) {
+                for (int i = 1; i < S; ++i) sum += part[wave + i];
+                dw[f] = sum;
+            }
+        }
     }
 }
 
@@ -277,17 +290,20 @@ namespace {
 
 template <int Y, bool D_F32, bool DY_F32>
 hipError_t combine_grad(const CombineGradProblem& p, hipStream_t s) {
-    const long n = (long)p.T * p.k, blocks = (n + kGradWaves - 1) / kGradWaves;
+    const long n = (long)p.T * p.k;
+    constexpr int C = D_F32 || DY_F32 || Y == kYF32 ? 4 : 8;   // as in the kernel
+    const int split = n <= 4L * device_cu_count() && p.H > kAhead * kWave * C ? 2 : 1;
+    const long blocks = (n * split + kGradWaves - 1) / kGradWaves;
     if (!fits(blocks, kGradWaves * 64)) return hipErrorInvalidValue;
     const auto run = [&](auto* kernel) {
         kernel<<<dim3((unsigned)blocks), dim3(kGradWaves * 64), 0, s>>>(p.dout, p.y, p.y_scale, p.dest, p.w, n, p.k, p.H, p.R,
                                                                        p.dy, p.dw);
         return hipGetLastError();
     };
-    if ((!p.dy || whole_lines(p.dy, (size_t)p.H * (DY_F32 ? 4 : 2))) &&
-        (Y == kYNone || Y == kYE4m3 || whole_lines(p.y, (size_t)p.H * (Y == kYF32 ? 4 : 2))))
-        return run(combine_grad_kernel<Y, D_F32, DY_F32, true>);
-    return run(combine_grad_kernel<Y, D_F32, DY_F32, false>);
+    const bool nt = (!p.dy || whole_lines(p.dy, (size_t)p.H * (DY_F32 ? 4 : 2))) &&
+                    (Y == kYNone || Y == kYE4m3 || whole_lines(p.y, (size_t)p.H * (Y == kYF32 ? 4 : 2)));
+    if (split == 2) return run(nt ? combine_grad_kernel<Y, D_F32, DY_F32, true, 2> : combine_grad_kernel<Y, D_F32, DY_F32, false, 2>);
+    return run(nt ? combine_grad_kernel<Y, D_F32, DY_F32, true, 1> : combine_grad_kernel<Y, D_F32, DY_F32, false, 1>);
 }
 
 template <int Y>

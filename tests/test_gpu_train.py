@@ -171,7 +171,7 @@ def test_dispatch_backward(T, k, E, H, absent):
 
 
 @pytest.mark.parametrize("absent", [0.0, 0.4])
-@pytest.mark.parametrize("T,k,E,H", ROWS + [(65, 4, 16, 384)])
+@pytest.mark.parametrize("T,k,E,H", ROWS + [(65, 4, 16, 384), (3, 5, 9, 7168), (1, 1, 1, 2056), (7, 3, 4, 4224)])
 def test_combine_backward(T, k, E, H, absent):
     dest, R = order(T, k, E, T + H + 2, absent)
     g = torch.Generator().manual_seed(T + H + 2)
