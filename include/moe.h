@@ -228,11 +228,18 @@ moe_status_t moe_mx_pack_scales(const moe_experts_t* bank, void* s_gate_up_packe
  * out_dt (F32 or BF16).  y_perm: [T*k][H] of type y_dt (F32, BF16, or E4M3
  * codes whose value is code * y_scale[row][col/128], y_scale [T*k][H/128]:
  * the FP8 combine of "DeepSeek V3/R1 Inference Efficiency (2)", section 2);
- * y_sh: [T][H] of type y_sh_dt (F32 or BF16). */
+ * y_sh: [T][H] of type y_sh_dt (F32 or BF16).  H a positive multiple of 128.  dest: of
+ * moe_permute; an assignment whose value lies outside [0, T*k) adds nothing. */
 moe_status_t moe_combine(const void* y_perm, int32_t y_dt, const float* y_scale,
                          const void* y_sh, int32_t y_sh_dt,
                          const int32_t* dest, const float* topk_w, int32_t T, int32_t k,
                          int32_t H, void* out, int32_t out_dt, void* stream);
+/* The same where only R rows are here: y_perm [R][H], y_scale [R][H/128] (NULL with R = 0);
+ * an assignment whose dest lies outside [0, R) (another GPU's expert) adds nothing. */
+moe_status_t moe_combine_rows(const void* y_perm, int32_t y_dt, const float* y_scale, int32_t R,
+                              const void* y_sh, int32_t y_sh_dt,
+                              const int32_t* dest, const float* topk_w, int32_t T, int32_t k,
+                              int32_t H, void* out, int32_t out_dt, void* stream);
 
 /* ---- the whole layer (the MoE FFN of "How DeepSeek inference works" and of
  * "DeepSeek V3/R1 Inference Efficiency (2)", section 2.3.1: gate, prepare
@@ -374,6 +381,8 @@ size_t moe_linear_i8_workspace_size(int32_t T, int32_t K, int32_t N);
  * The routed half of the layer with its gradients, on rows sorted by expert:
  * moe_route, moe_permute, moe_dispatch, moe_experts_ffn, moe_combine forward;
  * moe_combine_backward, moe_experts_ffn_backward, moe_dispatch_backward back.
+ * Where only a part of the experts is here, dest holds values outside [0, R) for the
+ * assignments to the others, and moe_combine_rows takes moe_combine's place.
  * (The shared expert: moe_ffn, moe_ffn_backward.)
  *
  * Activation checkpoints in 8 bits.  What the backward pass needs of the forward
@@ -416,7 +425,7 @@ moe_status_t moe_dispatch_backward(const void* dxs, int32_t dxs_dt, int32_t R, c
 
 /* Gradients of moe_combine for the output gradient dout [T][H] (MOE_F32 or MOE_BF16):
  *     dy[dest[t * k + j]] = topk_w[t][j] * dout[t]        dw[t][j] = sum_h dout[t][h] * y[dest[t * k + j]][h]
- * (the gradient of y_sh is dout itself).  y: what moe_combine read, [R][H] MOE_F32, MOE_BF16 or
+ * (the gradient of y_sh is dout itself).  y: what moe_combine or moe_combine_rows read, [R][H] MOE_F32, MOE_BF16 or
  * MOE_E4M3 with y_scale; may be NULL without dw.  dy: [R][H] MOE_F32 or MOE_BF16, rows that
  * dest does not name stay as they are; dw: [T][k] fp32, 0 for assignments without a row
  * here.  Either may be NULL; neither may overlap another tensor.  Sums are fp32.  H a positive multiple of 8

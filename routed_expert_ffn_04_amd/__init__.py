@@ -34,7 +34,7 @@ SCORE = {"softmax": SOFTMAX, "sigmoid": SIGMOID}
 EXPORTS = [
     "moe_route", "moe_route_workspace_size", "moe_permute", "moe_permute_workspace_size",
     "moe_quant_e4m3_1x128", "moe_quant_mxfp8", "moe_grouped_ffn", "moe_grouped_ffn_workspace_size",
-    "moe_combine", "moe_layer", "moe_layer_workspace_size", "moe_layer_noalloc", "moe_mx_pack_scales",
+    "moe_combine", "moe_combine_rows", "moe_layer", "moe_layer_workspace_size", "moe_layer_noalloc", "moe_mx_pack_scales",
     "moe_ffn", "moe_ffn_workspace_size", "moe_ffn_backward", "moe_ffn_backward_workspace_size",
     "moe_norm", "moe_norm_backward", "moe_norm_backward_workspace_size",
     "moe_quant_i8", "moe_linear_i8", "moe_linear_i8_workspace_size",
@@ -82,6 +82,7 @@ def lib() -> ctypes.CDLL:
                                  _P, _P, _I32, ctypes.POINTER(ExpertsT), _P, _I32, _P, _P, _I32, _P, _SZ, _P], _I32),
             "moe_grouped_ffn_workspace_size": ([_I32, _I32, _I32, _I32, _I32, _I32], _SZ),
             "moe_combine": ([_P, _I32, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _P, _I32, _P], _I32),
+            "moe_combine_rows": ([_P, _I32, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _P, _I32, _P], _I32),
             "moe_layer": ([_P, _I32, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.POINTER(ExpertsT),
                            ctypes.POINTER(ExpertsT), _P, _I32, _I32, _P, _P, _P, _P, _SZ, _P], _I32),
             "moe_layer_workspace_size": ([_I32] * 10, _SZ),
@@ -321,17 +322,18 @@ def grouped_ffn(a, offsets, routed: Experts, *, a_scale=None, src=None, src_div:
 
 
 def combine(y_perm, y_sh, dest, topk_w, out_dtype=None, out=None, stream=None, y_scale=None):
-    """moe_combine.  y_perm fp32/bf16, or e4m3 codes (torch.uint8) with
-    y_scale [rows][H/128]."""
+    """moe_combine_rows.  y_perm [R][H] fp32/bf16, or e4m3 codes (torch.uint8) with
+    y_scale [R][H/128]; values of dest outside [0, R) (assignments to another GPU's
+    experts) add nothing."""
     import torch
     T, k = topk_w.shape
-    H = y_perm.shape[1]
+    R, H = y_perm.shape
     out_dtype = out_dtype or torch.float32
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype, device=y_perm.device)
-    _check(lib().moe_combine(_ptr(y_perm), _dt_of(y_perm), _ptr(y_scale), _ptr(y_sh),
-                             _dt_of(y_sh) if y_sh is not None else F32, _ptr(dest), _ptr(topk_w), T, k, H,
-                             _ptr(out), _dt_of(out), _stream(stream)))
+    _check(lib().moe_combine_rows(_ptr(y_perm), _dt_of(y_perm), _ptr(y_scale), min(R, _MOST), _ptr(y_sh),
+                                  _dt_of(y_sh) if y_sh is not None else F32, _ptr(dest), _ptr(topk_w), T, k, H,
+                                  _ptr(out), _dt_of(out), _stream(stream)))
     return out
 
 

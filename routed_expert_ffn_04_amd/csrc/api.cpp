@@ -252,24 +252,38 @@ moe_status_t moe_mx_pack_scales(const moe_experts_t* bank, void* s_gate_up_packe
 }
 
 // ------------------------------------------------------------------ combine
+static moe_status_t combine_rows(const char* name, const void* y_perm, int32_t y_dt, const float* y_scale, int64_t R,
+                                 const void* y_sh, int32_t y_sh_dt, const int32_t* dest, const float* topk_w, int32_t T,
+                                 int32_t k, int32_t H, void* out, int32_t out_dt, void* stream) {
+    if (T < 0 || k <= 0 || H <= 0 || R < 0) return fail(MOE_ERR_INVALID, "%s: T=%d k=%d H=%d R=%lld", name, T, k, H, (long long)R);
+    if (H % 128) return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d not a multiple of 128", name, H);
+    if (y_dt != MOE_F32 && y_dt != MOE_BF16 && y_dt != MOE_E4M3)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: y dtype %d", name, y_dt);
+    if (y_sh && y_sh_dt != MOE_F32 && y_sh_dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: y_sh dtype %d", name, y_sh_dt);
+    if (out_dt != MOE_F32 && out_dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: out dtype %d", name, out_dt);
+    if (T == 0) return MOE_OK;
+    if ((!y_perm && R > 0) || !dest || !topk_w || !out) return fail(MOE_ERR_INVALID, "%s: null pointer", name);
+    if (y_dt == MOE_E4M3 && !y_scale && R > 0) return fail(MOE_ERR_INVALID, "%s: E4M3 y without y_scale", name);
+    if (!aligned16(y_perm) || (y_sh && !aligned16(y_sh)) || !aligned16(out))
+        return fail(MOE_ERR_INVALID, "%s: misaligned y or out", name);
+    const int ym = y_dt == MOE_E4M3 ? 2 : y_dt == MOE_BF16 ? 1 : 0;
+    // dest is int32: no row past 2^31 - 1 is named
+    return hip_check(moe::launch_combine(y_perm, ym, y_scale, y_sh, y_sh_dt == MOE_BF16, dest, topk_w, T, k, H,
+                                         (int)(R < INT32_MAX ? R : INT32_MAX), out, out_dt == MOE_BF16, (hipStream_t)stream),
+                     name);
+}
+
 moe_status_t moe_combine(const void* y_perm, int32_t y_dt, const float* y_scale, const void* y_sh,
                          int32_t y_sh_dt, const int32_t* dest, const float* topk_w, int32_t T, int32_t k,
                          int32_t H, void* out, int32_t out_dt, void* stream) {
-    if (T < 0 || k <= 0 || H <= 0) return fail(MOE_ERR_INVALID, "combine: T=%d k=%d H=%d", T, k, H);
-    if (H % 128) return fail(MOE_ERR_UNSUPPORTED, "combine: H=%d not a multiple of 128", H);
-    if (y_dt != MOE_F32 && y_dt != MOE_BF16 && y_dt != MOE_E4M3)
-        return fail(MOE_ERR_UNSUPPORTED, "combine: y dtype %d", y_dt);
-    if (y_sh && y_sh_dt != MOE_F32 && y_sh_dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "combine: y_sh dtype %d", y_sh_dt);
-    if (out_dt != MOE_F32 && out_dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "combine: out dtype %d", out_dt);
-    if (T == 0) return MOE_OK;
-    if (!y_perm || !dest || !topk_w || !out) return fail(MOE_ERR_INVALID, "combine: null pointer");
-    if (y_dt == MOE_E4M3 && !y_scale) return fail(MOE_ERR_INVALID, "combine: E4M3 y without y_scale");
-    if (!aligned16(y_perm) || (y_sh && !aligned16(y_sh)) || !aligned16(out))
-        return fail(MOE_ERR_INVALID, "combine: misaligned y or out");
-    const int ym = y_dt == MOE_E4M3 ? 2 : y_dt == MOE_BF16 ? 1 : 0;
-    return hip_check(moe::launch_combine(y_perm, ym, y_scale, y_sh, y_sh_dt == MOE_BF16, dest, topk_w, T, k, H, out,
-                                         out_dt == MOE_BF16, (hipStream_t)stream),
-                     "moe_combine");
+    return combine_rows("combine", y_perm, y_dt, y_scale, T < 0 || k < 0 ? 0 : (int64_t)T * k, y_sh, y_sh_dt, dest, topk_w,
+                        T, k, H, out, out_dt, stream);
+}
+
+moe_status_t moe_combine_rows(const void* y_perm, int32_t y_dt, const float* y_scale, int32_t R, const void* y_sh,
+                              int32_t y_sh_dt, const int32_t* dest, const float* topk_w, int32_t T, int32_t k,
+                              int32_t H, void* out, int32_t out_dt, void* stream) {
+    return combine_rows("combine_rows", y_perm, y_dt, y_scale, R, y_sh, y_sh_dt, dest, topk_w, T, k, H, out, out_dt, stream);
 }
 
 // ------------------------------------------------------------------ layer
@@ -380,7 +394,7 @@ moe_status_t moe_layer(const void* x, int32_t x_dt, int32_t T, int32_t H, const 
     if (e == hipSuccess)
         e = moe::launch_combine(w8 + L.yperm, y_dt == MOE_E4M3 ? 2 : y_dt == MOE_BF16 ? 1 : 0,
                                 (const float*)(w8 + L.yscale), has_sh ? w8 + L.ysh : nullptr, ybf, dest, tw, T, k, H,
-                                out, out_dt == MOE_BF16, s);
+                                R, out, out_dt == MOE_BF16, s);
     return hip_check(e, "moe_layer");
 }
 

@@ -4,6 +4,9 @@
 // one workgroup per token and 1024-column slab, 8 columns per thread.  The
 // expert outputs may arrive as e4m3 with per-1x128 scales (the FP8 combine the
 // same page names as the lever from 3300 to 5000 tokens/s per GPU).
+// Only rows in [0, R) are read: an assignment whose dest lies outside has none here
+// and adds nothing.  The row numbers are the same in a whole workgroup, so the check is
+// scalar work.
 #include "common.h"
 #include "internal.h"
 
@@ -77,7 +80,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_kernel(const void* __res
                                                                const float* __restrict__ y_scale,
                                                                const void* __restrict__ y_sh,
                                                                const int32_t* __restrict__ dest,
-                                                               const float* __restrict__ w, int T, int k, int H,
+                                                               const float* __restrict__ w, int T, int k, int H, int R,
                                                                void* __restrict__ out) {
     const int t = blockIdx.y;
     const int c = (blockIdx.x * kCombThreads + threadIdx.x) * kCombCols;
@@ -101,13 +104,17 @@ __global__ __launch_bounds__(kCombThreads) void combine_kernel(const void* __res
     for (int j0 = 0; j0 < k; j0 += kCombRows) {
         const int n = min(kCombRows, k - j0);
         YRaw<YM> raw[kCombRows];
+        bool here[kCombRows];
 #pragma unroll
-        for (int jj = 0; jj < kCombRows; ++jj)
-            if (jj < n) raw[jj] = load_y<YM>(y_perm, y_scale, (size_t)dt[j0 + jj], H, c);
+        for (int jj = 0; jj < kCombRows; ++jj) {
+            const int r = jj < n ? dt[j0 + jj] : -1;
+            here[jj] = (unsigned)r < (unsigned)R;
+            if (here[jj]) raw[jj] = load_y<YM>(y_perm, y_scale, (size_t)r, H, c);
+        }
         // out = y_sh + sum_j w_j * y_j, one fused multiply-add per slot, in slot order
 #pragma unroll
         for (int jj = 0; jj < kCombRows; ++jj) {
-            if (jj < n) {
+            if (here[jj]) {
                 const float wj = wt[j0 + jj];
                 float v[kCombCols];
                 decode_y<YM>(raw[jj], v);
@@ -131,13 +138,13 @@ __global__ __launch_bounds__(kCombThreads) void combine_kernel(const void* __res
 }
 
 hipError_t launch_combine(const void* y_perm, int y_mode, const float* y_scale, const void* y_sh, int y_sh_bf16,
-                          const int32_t* dest, const float* w, int T, int k, int H, void* out, int out_bf16,
+                          const int32_t* dest, const float* w, int T, int k, int H, int R, void* out, int out_bf16,
                           hipStream_t s) {
     if (T == 0) return hipSuccess;
     dim3 grid((H / kCombCols + kCombThreads - 1) / kCombThreads, T);
 #define MOE_COMB(YM, SB, OB)                                                                                         \
     hipLaunchKernelGGL((combine_kernel<YM, SB, OB>), grid, dim3(kCombThreads), 0, s, y_perm, y_scale, y_sh, dest, w, \
-                       T, k, H, out)
+                       T, k, H, R, out)
 #define MOE_COMB_O(YM, SB) \
     do { if (out_bf16) MOE_COMB(YM, SB, true); else MOE_COMB(YM, SB, false); } while (0)
 #define MOE_COMB_S(YM) \

@@ -29,9 +29,9 @@ hipError_t launch_quant_mxfp8(const void* x, int x_bf16, int rows, int cols, uin
                               uint8_t* e8, hipStream_t s);
 
 // combine.hip
-// y_mode: 0 fp32, 1 bf16, 2 e4m3 codes + y_scale [rows][H/128]
+// y_mode: 0 fp32, 1 bf16, 2 e4m3 codes + y_scale [rows][H/128]; R: rows of y_perm
 hipError_t launch_combine(const void* y_perm, int y_mode, const float* y_scale, const void* y_sh, int y_sh_bf16,
-                          const int32_t* dest, const float* w, int T, int k, int H, void* out, int out_bf16,
+                          const int32_t* dest, const float* w, int T, int k, int H, int R, void* out, int out_bf16,
                           hipStream_t s);
 
 // gffn.hip ------------------------------------------------------------------
