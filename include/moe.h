@@ -449,8 +449,8 @@ moe_status_t moe_experts_ffn(const void* xs, int32_t x_dt, const int32_t* offset
 size_t moe_experts_ffn_workspace_size(int32_t R, int32_t n, int32_t H, int32_t I);
 
 /* Gradients of moe_experts_ffn (those of moe_ffn_backward, each expert over its own
- * rows).  dy, dx: [R][H] MOE_BF16; xs: [R][H], x_dt MOE_BF16, or MOE_I8 with exponents
- * x_e8; gu, gu_dt, gu_e8: as moe_experts_ffn wrote them, or NULL (computed again from xs).
+ * rows).  dy, dx: [R][H] MOE_BF16; xs: [R][H], x_dt MOE_BF16, or MOE_I8 (codes 8-byte
+ * aligned, everything else 16) with exponents x_e8; gu, gu_dt, gu_e8: as moe_experts_ffn wrote them, or NULL (computed again from xs).
  * dw_gate, dw_up: [n][I][H], dw_down: [n][H][I], MOE_BF16, written, with zeros for an expert
  * without rows.  Each output may be NULL. */
 moe_status_t moe_experts_ffn_backward(const void* dy, const void* xs, int32_t x_dt, const uint8_t* x_e8,
@@ -461,8 +461,8 @@ size_t moe_experts_ffn_backward_workspace_size(int32_t R, int32_t n, int32_t H, 
                                                int32_t x_dt);
 
 /* moe_ffn and moe_ffn_backward with checkpoints in 8 bits: gu as codes [T][2 I] with
- * exponents gu_e8 [T][2 ceil(I / 16)] (required); in the backward pass xs as MOE_BF16, or
- * MOE_I8 with exponents x_e8. */
+ * exponents gu_e8 [T][2 ceil(I / 16)] (required); in the backward pass x as MOE_BF16, or
+ * MOE_I8 (codes 8-byte aligned) with exponents x_e8. */
 moe_status_t moe_ffn_ckpt(const void* x, int32_t x_dt, int32_t T, const moe_experts_t* bank, void* y, int32_t y_dt,
                           int8_t* gu, uint8_t* gu_e8, void* ws, size_t ws_bytes, void* stream);
 size_t moe_ffn_ckpt_workspace_size(int32_t T, int32_t H, int32_t I);
