@@ -312,7 +312,8 @@ size_t moe_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
  * stored like the weights ([I][H], [I][H], [H][I]) and are written, not added
  * to.  Each output may be NULL (not computed).  gu: what moe_ffn wrote for the
  * same x and bank, or NULL to compute it again (the workspace then also holds
- * it: has_gu = 0 in the size query).  dg, du and h are rounded to bf16 before
+ * it: has_gu = 0 in the size query).  x is read for g and u and for dW_gate and
+ * dW_up, and may be NULL where neither is computed.  dg, du and h are rounded to bf16 before
  * the next product.  T = 0 writes zero weight gradients.  No output may overlap
  * an input or another output. */
 moe_status_t moe_ffn_backward(const void* dy, const void* x, int32_t dt, int32_t T, const moe_experts_t* bank,
@@ -452,7 +453,8 @@ size_t moe_experts_ffn_workspace_size(int32_t R, int32_t n, int32_t H, int32_t I
  * rows).  dy, dx: [R][H] MOE_BF16; xs: [R][H], x_dt MOE_BF16, or MOE_I8 (codes 8-byte
  * aligned, everything else 16) with exponents x_e8; gu, gu_dt, gu_e8: as moe_experts_ffn wrote them, or NULL (computed again from xs).
  * dw_gate, dw_up: [n][I][H], dw_down: [n][H][I], MOE_BF16, written, with zeros for an expert
- * without rows.  Each output may be NULL. */
+ * without rows.  Each output may be NULL, and so may xs where it is not read (gu given, dw_gate
+ * and dw_up NULL). */
 moe_status_t moe_experts_ffn_backward(const void* dy, const void* xs, int32_t x_dt, const uint8_t* x_e8,
                                       const int32_t* offsets, int32_t R, const moe_experts_t* bank, const void* gu,
                                       int32_t gu_dt, const uint8_t* gu_e8, void* dx, void* dw_gate, void* dw_up,

@@ -629,19 +629,20 @@ def _grads(need, dy, bank):
 
 
 def _kept_x(device: int, name, x, rows, H):
-    """(pointer, dtype code, pointer of the exponents) of a bf16 matrix or its 8-bit checkpoint."""
+    """(pointer, dtype code, pointer of the exponents) of a bf16 matrix or its 8-bit checkpoint; the boundary
+    refuses None where it would be read."""
     if isinstance(x, tuple):
         _pair(device, name, x, rows, H)
         return x[0].data_ptr(), I8, x[1].data_ptr()
     _tensor(device, name, x, (rows, H), (torch.bfloat16,))
-    return x.data_ptr(), BF16, None
+    return _ptr(x), BF16, None
 
 
 def ffn_backward(dy, x, bank: Experts, gu=None, *, need=_GRADS, ws=None, stream=None):
     """Gradients of ffn (moe_ffn_backward): (dx [T][H], dw_gate, dw_up [1][I][H],
     dw_down [1][H][I]), None for those not in `need`.  gu: what ffn returned
     (None: computed again).  x may be its 8-bit checkpoint, the pair that
-    quant_i8x16 returned."""
+    quant_i8x16 returned, and None with gu and neither dw_gate nor dw_up in `need`."""
     T, H, dev = _matrix("dy", dy)
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -865,8 +866,9 @@ def experts_ffn(xs, offsets, bank: Experts, *, want_gu: bool = False, gu_dtype=N
 def experts_ffn_backward(dy, xs, offsets, bank: Experts, gu=None, *, need=_GRADS, ws=None, stream=None):
     """Gradients of experts_ffn (moe_experts_ffn_backward): (dx [R][H], dw_gate,
     dw_up [n][I][H], dw_down [n][H][I]), None for those not in `need`; zeros for an
-    expert without rows.  gu: what experts_ffn returned (None: computed again).  xs
-    may be its 8-bit checkpoint, the pair that quant_i8x16 returned."""
+    expert without rows; rows of dx of no expert are not written.  gu: what experts_ffn
+    returned (None: computed again).  xs may be its 8-bit checkpoint, the pair that
+    quant_i8x16 returned, and None with gu and neither dw_gate nor dw_up in `need`."""
     R, H, dev = _matrix("dy", dy)
     there = _elsewhere(dev, stream)
     if there is not None:

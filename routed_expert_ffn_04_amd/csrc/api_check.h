@@ -52,6 +52,9 @@ inline moe_status_t check_dense(const moe_experts_t* b, const char* name) {
     return check_ffn_bank(b, name);
 }
 
+// Whether the backward pass reads x: for g and u where they were not saved, and for the gradients of their weights.
+inline bool reads_x(const void* gu, const void* dw_gate, const void* dw_up) { return !gu || dw_gate || dw_up; }
+
 inline bool dense_sizes(int T, int H, int I) {
     return T >= 0 && T <= kMaxRows && H > 0 && I > 0 && H % 8 == 0 && I % 8 == 0 && H <= kMaxFfn && I <= kMaxFfn;
 }

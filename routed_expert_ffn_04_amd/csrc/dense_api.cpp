@@ -81,7 +81,7 @@ moe_status_t moe_ffn_backward(const void* dy, const void* x, int32_t dt, int32_t
         return fail(MOE_ERR_INVALID, "%s", "ffn_backward: tensors must be 16-byte aligned");
     if (!dx && !dw_gate && !dw_up && !dw_down) return MOE_OK;
     if (T > 0) {
-        if (!dy || !x) return fail(MOE_ERR_INVALID, "%s", "ffn_backward: null dy or x");
+        if (!dy || (!x && reads_x(gu, dw_gate, dw_up))) return fail(MOE_ERR_INVALID, "%s", "ffn_backward: null dy or x");
         const size_t need = moe::ffn_backward_ws_bytes(T, bank->H, bank->I, gu != nullptr);
         if (need == moe::kUnfit) return fail(MOE_ERR_UNSUPPORTED, "ffn_backward: T=%d H=%d I=%d", T, bank->H, bank->I);
         if (!ws || !aligned(ws, 256) || ws_bytes < need)

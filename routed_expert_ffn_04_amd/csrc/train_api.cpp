@@ -191,7 +191,8 @@ moe_status_t moe_experts_ffn_backward(const void* dy, const void* xs, int32_t x_
         return fail(MOE_ERR_INVALID, "%s: misaligned tensor", name);
     if (!dx && !dw_gate && !dw_up && !dw_down) return MOE_OK;
     if (R > 0) {
-        if (!dy || !xs || !offsets) return fail(MOE_ERR_INVALID, "%s: null dy, xs or offsets", name);
+        if (!dy || !offsets || (!xs && reads_x(gu, dw_gate, dw_up)))
+            return fail(MOE_ERR_INVALID, "%s: null dy, xs or offsets", name);
         const size_t need = moe::experts_backward_ws_bytes(R, bank->n, bank->H, bank->I, gu != nullptr, is_i8(x_dt));
         if (need == moe::kUnfit) return fail(MOE_ERR_UNSUPPORTED, "%s: R=%d H=%d I=%d", name, R, bank->H, bank->I);
         if (!ws || !aligned(ws, 256) || ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace", name);
@@ -252,7 +253,7 @@ moe_status_t moe_ffn_ckpt_backward(const void* dy, const void* x, int32_t x_dt, 
         return fail(MOE_ERR_INVALID, "%s: tensors must be 16-byte aligned", name);
     if (!dx && !dw_gate && !dw_up && !dw_down) return MOE_OK;
     if (T > 0) {
-        if (!dy || !x) return fail(MOE_ERR_INVALID, "%s: null dy or x", name);
+        if (!dy || (!x && reads_x(gu, dw_gate, dw_up))) return fail(MOE_ERR_INVALID, "%s: null dy or x", name);
         const size_t need = moe::ffn_backward_ws_bytes(T, bank->H, bank->I, gu != nullptr, is_i8(x_dt));
         if (need == moe::kUnfit) return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d H=%d I=%d", name, T, bank->H, bank->I);
         if (!ws || !aligned(ws, 256) || ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace", name);

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import routed_expert_ffn_04_amd as moe
-from test_gpu_train import I8, Experts
+from test_gpu_dense import F32
+from test_gpu_train import I8, NAMES, Experts
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +29,25 @@ def test_rows_of_a_checkpoint_on_8_bytes(dense):
     assert torch.equal(moe.dequant_i8x16(*kept), moe.dequant_i8x16(*copy))
     dest = torch.arange(c.R, dtype=torch.int32, device="cuda").flip(0)
     assert torch.equal(moe.dispatch(kept, dest, 1), moe.dispatch(copy, dest, 1))
+
+
+@pytest.mark.parametrize("dense", [False, True])
+def test_backward_without_x(dense):
+    """Frozen gate and up weights: the other gradients without x, with either kind of saved g and u."""
+    c = Experts([71] if dense else [30, 0, 41], 264, 136)
+    for dtype in (F32, I8):
+        if dense:
+            _, gu = moe.ffn(c.x, c.bank, want_gu=True, gu_dtype=dtype)
+            back = lambda x, need: moe.ffn_backward(c.dy, x, c.bank, gu, need=need)
+        else:
+            _, gu = moe.experts_ffn(c.x, c.offsets, c.bank, want_gu=True, gu_dtype=dtype)
+            back = lambda x, need: moe.experts_ffn_backward(c.dy, x, c.offsets, c.bank, gu, need=need)
+        for need in (("dx",), ("dw_down",), ("dx", "dw_down")):
+            got = back(None, need)
+            assert [t is not None for t in got] == [name in need for name in NAMES]
+            c.check_backward(got, gu if dtype is I8 else None)
+            assert all(torch.equal(a, b) for a, b in zip(got, back(c.x, need)) if a is not None)
+        with pytest.raises(moe.MoeError):
+            back(None, ("dw_up",))
+    with pytest.raises(moe.MoeError):
+        moe.ffn_backward(c.dy, None, c.bank) if dense else moe.experts_ffn_backward(c.dy, None, c.offsets, c.bank)

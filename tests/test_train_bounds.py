@@ -27,3 +27,16 @@ def test_codes_of_x_are_aligned_like_their_pieces():
         assert call(x=P + 8, x_dt=I8, xe=P + 1) == WORKSPACE
         assert call(x=P + 4, x_dt=I8, xe=P) == INVALID
         assert call(x=P + 8) == INVALID
+
+
+def test_x_is_asked_for_where_it_is_read():
+    """With g and u saved, x is read for the gradients of the gate and up weights alone."""
+    def dense(x=None, x_dt=BF, xe=None, gu=P, dx=P, dwg=None, dwu=None, dwd=P):
+        bank = moe.ExpertsT(1, 72, 32, BF, P, P, P, None, None, None)
+        return moe.lib().moe_ffn_backward(P, x, x_dt, 5, ctypes.byref(bank), gu, dx, dwg, dwu, dwd, P, 16, None)
+    for call in (experts_back, ffn_back, dense):
+        assert call(x=None, dwg=None, dwu=None) == WORKSPACE
+        assert call(x=None, dx=None, dwg=None, dwu=None) == WORKSPACE
+        assert call(x=None, dwg=P, dwu=None) == INVALID
+        assert call(x=None, dwg=None, dwu=P) == INVALID
+        assert call(x=None, dwg=None, dwu=None, gu=None) == INVALID     # g and u are computed again
