@@ -398,7 +398,8 @@ size_t moe_linear_i8_workspace_size(int32_t T, int32_t K, int32_t N);
  * NaN has E = 255, codes 0 and the value NaN. */
 
 /* x: [rows][cols] MOE_F32 or MOE_BF16, cols a positive multiple of 8; q: codes [rows][cols];
- * e8: [rows][ceil(cols / 16)].  x, out 16-byte, q 8-byte aligned. */
+ * e8: [rows][ceil(cols / 16)].  x, out 16-byte, q 8-byte aligned; rows and cols at most 2^30,
+ * rows * cols at most 2^40. */
 moe_status_t moe_quant_i8x16(const void* x, int32_t x_dt, int32_t rows, int32_t cols, int8_t* q, uint8_t* e8,
                              void* stream);
 /* The values, as MOE_F32 or MOE_BF16 (both exact). */

@@ -31,6 +31,7 @@ inline unsigned size_of(int dt) { return dt == MOE_F32 ? 4 : 2; }
 constexpr int kMaxFfn = 1 << 21;    // a tile's 256 rows of 2 I bf16 stay below 2^31 bytes
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxRows = 1 << 30;   // rows and tiles are counted in 32 bits
+constexpr int64_t kMaxValues = (int64_t)1 << 40;   // of a matrix by itself: more than a GPU's memory holds
 
 // A bank of the FFN that is trained: bf16, H and I multiples of 8.
 inline moe_status_t check_ffn_bank(const moe_experts_t* b, const char* name) {

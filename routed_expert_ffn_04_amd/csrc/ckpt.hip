@@ -51,34 +51,40 @@ __global__ __launch_bounds__(256) void dequant_kernel(const int8_t* __restrict__
     store_row<F32, 8>(out, (size_t)a.row * cols + a.c, v);
 }
 
-bool grid_of(long rows, int cols, dim3& grid) {
-    const long blocks = (rows * (2L * i8x16_blocks(cols)) + 255) / 256;
-    grid = dim3((unsigned)blocks);
-    return blocks > 0 && blocks <= 0xffffffffL / 256;
+// A grid holds fewer than 2^32 threads: rows with more lanes go out in several launches.
+template <class Launch>
+hipError_t launch_pieces(long rows, int cols, Launch&& launch) {
+    const long per = 2L * i8x16_blocks(cols), most = 0xffffff00L / per;
+    for (long r = 0; r < rows; r += most) {
+        const long n = rows - r < most ? rows - r : most;
+        launch(r, n, dim3((unsigned)((n * per + 255) / 256)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
 
-bool i8x16_fits(long rows, int cols) {
-    dim3 grid;
-    return grid_of(rows, cols, grid);
-}
-
 hipError_t launch_quant_i8x16(const void* x, int x_f32, long rows, int cols, int8_t* q, uint8_t* e8, hipStream_t s) {
-    dim3 grid;
-    if (!grid_of(rows, cols, grid)) return hipErrorInvalidValue;
-    if (x_f32) quant_kernel<true><<<grid, dim3(256), 0, s>>>(x, rows, cols, q, e8);
-    else quant_kernel<false><<<grid, dim3(256), 0, s>>>(x, rows, cols, q, e8);
-    return hipGetLastError();
+    return launch_pieces(rows, cols, [&](long r, long n, dim3 grid) {
+        const uint8_t* from = (const uint8_t*)x + (size_t)r * cols * (x_f32 ? 4 : 2);
+        int8_t* codes = q + (size_t)r * cols;
+        uint8_t* e = e8 + (size_t)r * i8x16_blocks(cols);
+        if (x_f32) quant_kernel<true><<<grid, dim3(256), 0, s>>>(from, n, cols, codes, e);
+        else quant_kernel<false><<<grid, dim3(256), 0, s>>>(from, n, cols, codes, e);
+    });
 }
 
 hipError_t launch_dequant_i8x16(const int8_t* q, const uint8_t* e8, long rows, int cols, void* out, int out_f32,
                                 hipStream_t s) {
-    dim3 grid;
-    if (!grid_of(rows, cols, grid)) return hipErrorInvalidValue;
-    if (out_f32) dequant_kernel<true><<<grid, dim3(256), 0, s>>>(q, e8, rows, cols, out);
-    else dequant_kernel<false><<<grid, dim3(256), 0, s>>>(q, e8, rows, cols, out);
-    return hipGetLastError();
+    return launch_pieces(rows, cols, [&](long r, long n, dim3 grid) {
+        const int8_t* codes = q + (size_t)r * cols;
+        const uint8_t* e = e8 + (size_t)r * i8x16_blocks(cols);
+        uint8_t* to = (uint8_t*)out + (size_t)r * cols * (out_f32 ? 4 : 2);
+        if (out_f32) dequant_kernel<true><<<grid, dim3(256), 0, s>>>(codes, e, n, cols, to);
+        else dequant_kernel<false><<<grid, dim3(256), 0, s>>>(codes, e, n, cols, to);
+    });
 }
 
 }  // namespace moe

@@ -65,7 +65,6 @@ size_t linear_i8_ws_bytes(int T, int K, int N);
 hipError_t launch_linear_i8(const LinearI8Problem& p, void* ws, hipStream_t s);
 
 // ckpt.hip
-bool i8x16_fits(long rows, int cols);
 hipError_t launch_quant_i8x16(const void* x, int x_f32, long rows, int cols, int8_t* q, uint8_t* e8, hipStream_t s);
 hipError_t launch_dequant_i8x16(const int8_t* q, const uint8_t* e8, long rows, int cols, void* out, int out_f32,
                                 hipStream_t s);

@@ -58,7 +58,7 @@ static moe_status_t check_i8x16(const char* name, int32_t rows, int32_t cols, in
     if (rows < 0 || cols <= 0) return fail(MOE_ERR_INVALID, "%s: rows=%d cols=%d", name, rows, cols);
     if (cols % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: cols=%d not a multiple of 8", name, cols);
     if (!is_float(dt)) return fail(MOE_ERR_UNSUPPORTED, "%s: dtype %d", name, dt);
-    if (rows > kMaxRows || cols > kMaxRows || (rows > 0 && !moe::i8x16_fits(rows, cols)))
+    if (rows > kMaxRows || cols > kMaxRows || (int64_t)rows * cols > kMaxValues)
         return fail(MOE_ERR_UNSUPPORTED, "%s: rows=%d cols=%d is too large", name, rows, cols);
     return MOE_OK;
 }

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import routed_expert_ffn_04_amd as moe
-from test_gpu_dense import F32
+from test_gpu_dense import BF, F32
 from test_gpu_train import I8, NAMES, Experts
 
 pytestmark = pytest.mark.gpu
@@ -51,3 +51,30 @@ def test_backward_without_x(dense):
             back(None, ("dw_up",))
     with pytest.raises(moe.MoeError):
         moe.ffn_backward(c.dy, None, c.bank) if dense else moe.experts_ffn_backward(c.dy, None, c.offsets, c.bank)
+
+
+def test_checkpoint_of_more_lanes_than_a_grid_holds():
+    """2^30 rows of 24 columns are 2^32 lanes, which go out in two launches: the rows around the seam, the first and the
+    last (the others hold whatever the memory held)."""
+    rows, cols, n = 1 << 30, 24, 50
+    seam = (2 ** 32 - 256) // 4
+    assert seam + n <= rows                                              # (the second launch has the last 64 rows)
+    x = torch.empty((rows, cols), dtype=BF, device="cuda")
+    q, e = torch.empty((rows, cols), dtype=I8, device="cuda"), torch.empty((rows, 2), dtype=torch.uint8, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    some = {}
+    for a in (0, seam - n, seam, rows - n):
+        some[a] = torch.randn((n, cols), generator=g).to("cuda", BF)
+        if a == rows - n:                                                # overlaps the rows behind the seam
+            some[seam] = some[seam][:a - seam]
+        x[a:a + n] = some[a]
+    moe.quant_i8x16(x, out=(q, e))
+    for a, v in some.items():
+        rq, re = moe.quant_i8x16(v)
+        assert torch.equal(q[a:a + len(v)], rq) and torch.equal(e[a:a + len(v)], re)
+        x[a:a + len(v)] = 0
+    moe.dequant_i8x16(q, e, out=x)
+    for a, v in some.items():
+        assert torch.equal(x[a:a + len(v)], moe.dequant_i8x16(*moe.quant_i8x16(v)))
+    del x, q, e
+    torch.cuda.empty_cache()

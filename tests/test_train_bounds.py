@@ -40,3 +40,22 @@ def test_x_is_asked_for_where_it_is_read():
         assert call(x=None, dwg=P, dwu=None) == INVALID
         assert call(x=None, dwg=None, dwu=P) == INVALID
         assert call(x=None, dwg=None, dwu=None, gu=None) == INVALID     # g and u are computed again
+
+
+def test_checkpoints_of_more_lanes_than_a_grid_holds():
+    """Up to 2^40 values are taken (the first pointer is missing here), also where a grid of one lane for eight is too small."""
+    L = moe.lib()
+    for rows, cols in ((5_000_000, 7168), (1 << 30, 24), (1 << 20, 1 << 20), (1 << 10, 1 << 30)):
+        for dt in (BF, moe.F32):
+            assert L.moe_quant_i8x16(None, dt, rows, cols, P, P, None) == INVALID
+            assert L.moe_dequant_i8x16(P, P, rows, cols, None, dt, None) == INVALID
+    for rows, cols in (((1 << 20) + 1, 1 << 20), ((1 << 30) + 1, 8), (1, (1 << 30) + 8)):
+        assert L.moe_quant_i8x16(None, BF, rows, cols, P, P, None) == UNSUPPORTED
+        assert L.moe_dequant_i8x16(P, P, rows, cols, None, BF, None) == UNSUPPORTED
+    # the backward passes restore x with the same kernel: none has a workspace for more
+    for n in (1, 8, 1024):
+        for bits in range(1, 31):
+            R, H = 1 << bits, 1 << min(42 - bits, 21)
+            if R * H > 1 << 40:
+                assert L.moe_experts_ffn_backward_workspace_size(R, n, H, 8, 1, I8) == 0
+                assert L.moe_ffn_ckpt_backward_workspace_size(R, H, 8, 1, I8) == 0
