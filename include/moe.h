@@ -411,8 +411,8 @@ moe_status_t moe_dequant_i8x16(const int8_t* q, const uint8_t* e8, int32_t rows,
  * (another GPU's experts), which are skipped; no row may be named twice.  Rows
  * that are not named stay as they are.  x: [T][H] MOE_F32, MOE_BF16, or MOE_I8: codes of
  * moe_quant_i8x16 with the exponents x_e8 [T][ceil(H / 16)] (NULL otherwise).  xs: [R][H] of x's type,
- * MOE_BF16 for MOE_I8.  H a positive multiple of 8; rows 16-byte aligned (codes 8); T, H, R and T * k at most 2^30
- * (here and in the two calls below).  xs may not overlap another tensor. */
+ * MOE_BF16 for MOE_I8.  H a positive multiple of 8; rows 16-byte aligned (codes 8); T, H, R and T * k at most 2^30,
+ * T * H at most 2^40 (here and in the two calls below).  xs may not overlap another tensor. */
 moe_status_t moe_dispatch(const void* x, int32_t x_dt, const uint8_t* x_e8, int32_t T, int32_t H, const int32_t* dest,
                           int32_t k, int32_t R, void* xs, void* stream);
 

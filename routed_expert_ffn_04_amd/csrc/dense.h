@@ -80,7 +80,6 @@ struct DispatchProblem {
     const void* add; int add_f32;               // or null
     void* dx; int dx_f32;
 };
-bool dispatch_fits(int T, int H, int k);
 hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t s);
 hipError_t launch_dispatch_backward(const DispatchProblem& p, hipStream_t s);
 

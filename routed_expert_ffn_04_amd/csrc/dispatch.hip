@@ -15,6 +15,8 @@
 // of other lengths keep the usual one, which joins the pieces of a line (2056 columns:
 // 45 us, against 63).  Row numbers that are the same in a whole wave are read
 // through the scalar cache: the gradient took 532 us with vector loads of them.
+#include <algorithm>
+
 #include "dense.h"
 #include "gffn_common.h"
 #include "i8x16.h"
@@ -132,12 +134,12 @@ constexpr int kGradWaves = 4, kAhead = 8;
 template <int Y, bool D_F32, bool DY_F32, bool NT, int S>
 __global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
     const void* __restrict__ dout, const void* __restrict__ y, const float* __restrict__ y_scale,
-    const int32_t* __restrict__ dest, const float* __restrict__ w, long n, int k, int H, int R, void* __restrict__ dy,
-    float* __restrict__ dw) {
+    const int32_t* __restrict__ dest, const float* __restrict__ w, long first, long n, int k, int H, int R,
+    void* __restrict__ dy, float* __restrict__ dw) {
     constexpr int C = D_F32 || DY_F32 || Y == kYF32 ? 4 : 8;   // 16 bytes a lane of the wider ones
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const long f = (long)(NT ? in_die_order(blockIdx.x, gridDim.x) : blockIdx.x) * (kGradWaves / S) + wave / S;
+    const long f = first + (long)(NT ? in_die_order(blockIdx.x, gridDim.x) : blockIdx.x) * (kGradWaves / S) + wave / S;
     if (S == 1 && f >= n) return;
     const long t = f / k;
     const int r = f < n ? dest[f] : -1;
@@ -217,21 +219,23 @@ __global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
     }
 }
 
-// Launch shape of the kernels over the tokens' pieces.
+// Launch shape of the kernels over the tokens' pieces.  A grid holds fewer than 2^32 threads: tokens
+// (of combine's gradient: assignments) that need more go out in several launches.
+constexpr long kMostBlocks = 0xffffffffL / 256;
 struct Shape {
     int slabs, per;
     bool rows;      // LONG
-    long blocks;
+    long most;      // tokens of a launch
+    long blocks(long T) const { return rows ? T * slabs : (T + per - 1) / per; }
 };
-Shape shape_of(int T, int pieces, int u) {
+Shape shape_of(int pieces, int u) {
     Shape s;
     s.rows = pieces > 128;   // up to 128 pieces two tokens and more fit a workgroup
     s.per = s.rows ? 1 : 256 / pieces;
     s.slabs = (pieces + u * 256 - 1) / (u * 256);
-    s.blocks = s.rows ? (long)T * s.slabs : ((long)T + s.per - 1) / s.per;
+    s.most = s.rows ? kMostBlocks / s.slabs : kMostBlocks * s.per;
     return s;
 }
-bool fits(long blocks, int threads) { return blocks <= 0xffffffffL / threads; }
 
 // Whether the rows of a matrix are whole lines.
 bool whole_lines(const void* p, size_t row_bytes) { return ((uintptr_t)p | row_bytes) % 128 == 0; }
@@ -240,18 +244,19 @@ constexpr int kU = 2;   // 512 pieces a workgroup: 415 us against 424 with 256 a
 
 }  // namespace
 
-bool dispatch_fits(int T, int H, int k) {
-    return fits(shape_of(T, H / 4, 1).blocks, 256) && fits(((long)T * k + kGradWaves - 1) / kGradWaves, kGradWaves * 64);
-}
-
 hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t s) {
     const int pieces = p.x_f32 ? p.H / 4 : p.H / 8;
-    const Shape g = shape_of(p.T, pieces, kU);
-    if (!fits(g.blocks, 256)) return hipErrorInvalidValue;
+    const Shape g = shape_of(pieces, kU);
     const auto run = [&](auto* kernel) {
-        kernel<<<dim3((unsigned)g.blocks), dim3(256), 0, s>>>((const uint8_t*)p.x, p.xe, p.T, pieces, g.slabs, g.per, p.dest,
-                                                             p.k, p.R, (i32x4*)p.xs);
-        return hipGetLastError();
+        for (long t = 0; t < p.T; t += g.most) {
+            const long n = std::min(g.most, p.T - t);
+            kernel<<<dim3((unsigned)g.blocks(n)), dim3(256), 0, s>>>(
+                (const uint8_t*)p.x + (size_t)t * pieces * (p.xe ? 8 : 16), p.xe ? p.xe + (size_t)t * i8x16_blocks(p.H) : nullptr,
+                (int)n, pieces, g.slabs, g.per, p.dest + (size_t)t * p.k, p.k, p.R, (i32x4*)p.xs);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
     };
     if (!g.rows) return p.xe ? run(dispatch_kernel<true, false, 1, false>) : run(dispatch_kernel<false, false, 1, false>);
     if (whole_lines(p.xs, (size_t)pieces * 16))
@@ -264,11 +269,18 @@ namespace {
 template <bool F32, bool ADD_F32, bool OUT_F32>
 hipError_t gather(const DispatchProblem& p, hipStream_t s) {
     const int pieces = p.H / (F32 ? 4 : 8);
-    const Shape g = shape_of(p.T, pieces, 1);
-    if (!fits(g.blocks, 256)) return hipErrorInvalidValue;
+    const Shape g = shape_of(pieces, 1);
     const auto run = [&](auto* kernel) {
-        kernel<<<dim3((unsigned)g.blocks), dim3(256), 0, s>>>(p.dxs, p.add, p.T, pieces, g.slabs, g.per, p.dest, p.k, p.R, p.dx);
-        return hipGetLastError();
+        for (long t = 0; t < p.T; t += g.most) {
+            const long n = std::min(g.most, p.T - t);
+            const size_t at = (size_t)t * p.H;
+            kernel<<<dim3((unsigned)g.blocks(n)), dim3(256), 0, s>>>(
+                p.dxs, p.add ? (const uint8_t*)p.add + at * (ADD_F32 ? 4 : 2) : nullptr, (int)n, pieces, g.slabs, g.per,
+                p.dest + (size_t)t * p.k, p.k, p.R, (uint8_t*)p.dx + at * (OUT_F32 ? 4 : 2));
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
     };
     if (!g.rows) return run(gather_kernel<F32, ADD_F32, OUT_F32, false, false>);
     if (whole_lines(p.dxs, (size_t)pieces * 16)) return run(gather_kernel<F32, ADD_F32, OUT_F32, true, true>);
@@ -293,12 +305,16 @@ hipError_t combine_grad(const CombineGradProblem& p, hipStream_t s) {
     const long n = (long)p.T * p.k;
     constexpr int C = D_F32 || DY_F32 || Y == kYF32 ? 4 : 8;   // as in the kernel
     const int split = n <= 4L * device_cu_count() && p.H > kAhead * kWave * C ? 2 : 1;
-    const long blocks = (n * split + kGradWaves - 1) / kGradWaves;
-    if (!fits(blocks, kGradWaves * 64)) return hipErrorInvalidValue;
+    static_assert(kGradWaves * 64 == 256, "kMostBlocks counts such workgroups");
     const auto run = [&](auto* kernel) {
-        kernel<<<dim3((unsigned)blocks), dim3(kGradWaves * 64), 0, s>>>(p.dout, p.y, p.y_scale, p.dest, p.w, n, p.k, p.H, p.R,
-                                                                       p.dy, p.dw);
-        return hipGetLastError();
+        for (long f = 0; f < n; f += kMostBlocks * kGradWaves / split) {
+            const long blocks = std::min(((n - f) * split + kGradWaves - 1) / kGradWaves, kMostBlocks);
+            kernel<<<dim3((unsigned)blocks), dim3(kGradWaves * 64), 0, s>>>(p.dout, p.y, p.y_scale, p.dest, p.w, f, n, p.k, p.H,
+                                                                           p.R, p.dy, p.dw);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
     };
     const bool nt = (!p.dy || whole_lines(p.dy, (size_t)p.H * (DY_F32 ? 4 : 2))) &&
                     (Y == kYNone || Y == kYE4m3 || whole_lines(p.y, (size_t)p.H * (Y == kYF32 ? 4 : 2)));

@@ -18,7 +18,7 @@ bool is_i8(int dt) { return dt == MOE_I8; }
 moe_status_t check_rows(const char* name, int32_t T, int32_t k, int32_t H, int32_t R) {
     if (T < 0 || k <= 0 || H <= 0 || R < 0) return fail(MOE_ERR_INVALID, "%s: T=%d k=%d H=%d R=%d", name, T, k, H, R);
     if (H % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d not a multiple of 8", name, H);
-    if (T > kMaxRows || R > kMaxRows || H > kMaxRows || (int64_t)T * k > kMaxRows || !moe::dispatch_fits(T, H, k))
+    if (T > kMaxRows || R > kMaxRows || H > kMaxRows || (int64_t)T * k > kMaxRows || (int64_t)T * H > kMaxValues)
         return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d k=%d H=%d R=%d is too large", name, T, k, H, R);
     return MOE_OK;
 }

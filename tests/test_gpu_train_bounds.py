@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import routed_expert_ffn_04_amd as moe
-from test_gpu_dense import BF, F32
+from test_gpu_dense import BF, F32, outbuf, rand
 from test_gpu_train import I8, NAMES, Experts
 
 pytestmark = pytest.mark.gpu
@@ -77,4 +77,66 @@ def test_checkpoint_of_more_lanes_than_a_grid_holds():
     for a, v in some.items():
         assert torch.equal(x[a:a + len(v)], moe.dequant_i8x16(*moe.quant_i8x16(v)))
     del x, q, e
+    torch.cuda.empty_cache()
+
+
+def test_rows_of_more_workgroups_than_a_grid_holds():
+    """2^24 workgroups of 256 threads are one more than a grid holds: tokens of one workgroup each, in two launches.  The
+    tokens that have a row here lie around the seam and at both ends."""
+    H, R, seam = 1032, 8, (2 ** 32 - 1) // 256
+    T = seam + 9
+    at = [0, 1, seam - 1, seam, seam + 1, T - 2, T - 1]
+    dest = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    x = torch.empty((T, H), dtype=BF, device="cuda")
+    g = torch.Generator().manual_seed(2)
+    for i, t in enumerate(at):
+        dest[t] = i
+        x[t] = torch.randn(H, generator=g).to("cuda", BF)
+    xs, guard = outbuf((R, H), BF)
+    moe.dispatch(x, dest, 1, out=xs)
+    guard()
+    assert bool((xs[len(at):] == 77).all())
+    for i, t in enumerate(at):
+        assert torch.equal(xs[i], x[t])
+    rows = rand(g, (R, H), 1.0, BF)
+    moe.dispatch_backward(rows, dest, 1, out=x)
+    for i, t in enumerate(at):
+        assert torch.equal(x[t], rows[i])
+    for t in (2, seam - 2, seam + 2, T - 3):
+        assert bool((x[t] == 0).all())
+    moe.dispatch_backward(rows, dest, 1, add=x, out=x)
+    for i, t in enumerate(at):
+        assert torch.equal(x[t], (2 * rows[i].float()).to(BF))
+    # 8-bit checkpoints of the same many tokens: codes and exponents move on together
+    del x
+    q, e = torch.empty((T, H), dtype=I8, device="cuda"), torch.empty((T, 65), dtype=torch.uint8, device="cuda")
+    kept, exps = moe.quant_i8x16(rows)
+    for i, t in enumerate(at):
+        q[t], e[t] = kept[i], exps[i]
+    moe.dispatch((q, e), dest, 1, out=xs)
+    assert torch.equal(xs[:len(at)], moe.dequant_i8x16(kept, exps)[:len(at)])
+    guard()
+    del q, e
+    torch.cuda.empty_cache()
+
+
+def test_assignments_of_more_waves_than_a_grid_holds():
+    """2^26 assignments and more, four a workgroup, in two launches."""
+    H, R, k, seam = 8, 8, 2, (2 ** 32 - 1) // 256 * 4
+    T = seam // k + 5
+    at = [0, 1, seam - 1, seam, seam + 1, T * k - 2, T * k - 1]
+    dest = torch.full((T * k,), -1, dtype=torch.int32, device="cuda")
+    dout = torch.ones((T, H), dtype=BF, device="cuda")
+    w = torch.full((T, k), 0.5, device="cuda")
+    for i, f in enumerate(at):
+        dest[f] = i
+        dout[f // k] = f % 11 + 1
+    y = torch.arange(R, device="cuda", dtype=torch.float32).add(1).unsqueeze(1).expand(R, H).to(BF).contiguous()
+    buf, guard = outbuf((R, H), BF)
+    dy, dw = moe.combine_backward(dout, y, dest, w, dy=buf)
+    guard()
+    for i, f in enumerate(at):
+        assert torch.equal(dy[i], 0.5 * dout[f // k]) and float(dw.view(-1)[f]) == 8 * float(dout[f // k, 0]) * (i + 1)
+    assert bool((dy[len(at):] == 77).all()) and int((dw != 0).sum()) == len(at)
+    del dw, dout, w, dest
     torch.cuda.empty_cache()

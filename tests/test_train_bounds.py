@@ -59,3 +59,19 @@ def test_checkpoints_of_more_lanes_than_a_grid_holds():
             if R * H > 1 << 40:
                 assert L.moe_experts_ffn_backward_workspace_size(R, n, H, 8, 1, I8) == 0
                 assert L.moe_ffn_ckpt_backward_workspace_size(R, H, 8, 1, I8) == 0
+
+
+def test_rows_of_more_workgroups_than_a_grid_holds():
+    """T, H and T * k up to 2^30 and T * H up to 2^40 are taken (the first pointer is missing here), and not more."""
+    L = moe.lib()
+
+    def calls(T, k, H, dt):
+        return (L.moe_dispatch(None, dt, None, T, H, P, k, 8, P, None),
+                L.moe_dispatch_backward(None, dt, 8, P, T, k, H, None, 0, P, dt, None),
+                L.moe_combine_backward(None, dt, P, dt, None, 8, P, P, T, k, H, P, dt, P, None))
+    for dt in (BF, moe.F32):
+        for T, k, H in ((1 << 24, 8, 8), (2_500_000, 1, 7168), (20_000_000, 2, 7168), (1 << 30, 1, 8), (1, 1 << 30, 8),
+                        (1 << 10, 1, 1 << 30), (1 << 20, 1 << 10, 1 << 20)):
+            assert calls(T, k, H, dt) == (INVALID,) * 3
+        for T, k, H in (((1 << 30) + 1, 1, 8), (1 << 29, 3, 8), (1, 1, (1 << 30) + 8), ((1 << 20) + 1, 1, 1 << 20)):
+            assert calls(T, k, H, dt) == (UNSUPPORTED,) * 3
