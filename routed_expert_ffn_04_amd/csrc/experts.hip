@@ -40,23 +40,12 @@ struct Grouped {
     int cus;               // kRows, 256-row tiles: CUs of a die
 };
 
-// Position in the order of `total` tiles, of which every die takes one contiguous
-// run, of workgroup `block`; -1 past them.
-__device__ __forceinline__ int in_die_order(int block, int total) {
-    const int x = block % kXcds, j = block / kXcds;
-    const int base = total / kXcds, extra = total % kXcds;
-    return j < base + (x < extra ? 1 : 0) ? x * base + min(x, extra) + j : -1;
-}
-
 // Workgroup `block`'s among all experts' row tiles: the expert, the tile within it and
 // the expert's rows; false past the last one.  Every wave does this by itself.
-//
-// cuts (256-row tiles): where a die's tiles leave up to half of its CUs without work in
-// their last round, the tiles of that round are cut into halves of 128 rows, which
-// take 0.6 of a tile's time each (half_tile).
+// cuts: with the halves of the last round (cut_of, half_tile).
 struct Place {
     int e, t, first, m;
-    int half;   // 0: the whole tile, 1: its upper, 2: its lower half
+    int half;   // as in Cut
 };
 __device__ __forceinline__ bool find_rows(const Grouped& P, int edge, int block, bool cuts, Place& at) {
     const int lane = threadIdx.x % kWave;
@@ -77,12 +66,9 @@ __device__ __forceinline__ bool find_rows(const Grouped& P, int edge, int block,
     for (int e0 = 0; e0 < P.n; e0 += kWave) total += __builtin_amdgcn_readlane(scan(tiles(e0 + lane)), kWave - 1);
     at.half = 0;
     if (cuts) {
-        const int x = block % kXcds, j = block / kXcds;
-        const int mine = total / kXcds + (x < total % kXcds ? 1 : 0), last = mine % P.cus, whole = mine - last;
-        if (2 * last <= P.cus && last <= kMostCuts && j >= whole) {
-            at.half = 1 + (j - whole) % 2;
-            block = (whole + (j - whole) / 2) * kXcds + x;
-        }
+        const Cut c = cut_of(block, total, P.cus);
+        block = c.block;
+        at.half = c.half;
     }
     int t = in_die_order(block, total);
     if (t < 0) return false;

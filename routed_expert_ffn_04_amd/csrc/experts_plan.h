@@ -19,10 +19,32 @@ inline long row_tiles(int R, int n, int edge) { return (long)R / edge + std::min
 inline int even_rows(int R, int n) { return (R + std::min(R, n) - 1) / std::min(R, n); }
 inline long even_tiles(int R, int n, int edge) { return (long)std::min(R, n) * ((even_rows(R, n) + edge - 1) / edge); }
 
+// Position in the order of `total` tiles, of which every die takes one contiguous
+// run, of workgroup `block`; -1 past them.
+constexpr int in_die_order(int block, int total) {
+    const int x = block % kDies, j = block / kDies;
+    const int base = total / kDies, extra = total % kDies;
+    return j < base + (x < extra ? 1 : 0) ? x * base + (x < extra ? x : extra) + j : -1;
+}
+
+// 256-row tiles: where a die's tiles leave half or more of its `cus` CUs without work in
+// their last round, the tiles of that round are cut into halves of 128 rows, which
+// take 0.6 of a tile's time each.  The workgroup whose tile workgroup `block` takes, and which part of it.
+constexpr int kMostCuts = 16;   // of a die
+struct Cut {
+    int block;
+    int half;   // 0: the whole tile, 1: its upper, 2: its lower half
+};
+constexpr Cut cut_of(int block, int total, int cus) {
+    const int x = block % kDies, j = block / kDies;
+    const int mine = total / kDies + (x < total % kDies ? 1 : 0), last = mine % cus, whole = mine - last;
+    if (2 * last > cus || last > kMostCuts || j < whole) return {block, 0};
+    return {(whole + (j - whole) / 2) * kDies + x, 1 + (j - whole) % 2};
+}
+
 // Workgroups of a product over the experts' rows: a multiple of the dies, which share
 // the tiles that there are evenly, and of 256-row tiles so many more for the second
-// halves of those that are cut (find_rows).
-constexpr int kMostCuts = 16;   // of a die
+// halves of those that are cut.
 inline long rows_grid(int R, int n, int edge, long nt) {
     return (row_tiles(R, n, edge) * nt + kDies - 1) / kDies * kDies + (edge == 256 ? kDies * kMostCuts : 0);
 }

@@ -240,16 +240,7 @@ __device__ __forceinline__ void store8(const Args& G, uint8_t* row, int n, const
 
 // Workgroup b of `total` -> tile.  Workgroups go to the eight dies round robin,
 // each die with an L2 of its own: every die takes one contiguous run of tiles,
-// ordered in bands of 8 m-tiles with n outermost, so the 32 tiles that a die
-// works on together form a block of about 8 x 4 and share their operands in L2.
-// Tile t of the bands:
-__device__ __forceinline__ void band_of(int t, int mt, int nt, int& tm, int& tn) {
-    const int band = t / (8 * nt);
-    const int rows = min(8, mt - band * 8);
-    t -= band * 8 * nt;
-    tn = t / rows;
-    tm = band * 8 + t % rows;
-}
+// ordered in bands (band_of).
 __device__ __forceinline__ void tile_of(int b, int mt, int nt, int total, int& tm, int& tn, int& split) {
     const int x = b % kXcds, j = b / kXcds;
     const int base = total / kXcds, extra = total % kXcds;

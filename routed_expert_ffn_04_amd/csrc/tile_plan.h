@@ -22,6 +22,16 @@ constexpr int kFewThreads = 512;
 // 33 rows.
 constexpr int kFewRows = 16;
 
+// Tile t of mt x nt in bands of 8 m-tiles with n outermost: the 32 tiles that a die
+// works on together form a block of about 8 x 4 and share their operands in L2.
+constexpr void band_of(int t, int mt, int nt, int& tm, int& tn) {
+    const int band = t / (8 * nt);
+    const int rows = mt - band * 8 < 8 ? mt - band * 8 : 8;
+    t -= band * 8 * nt;
+    tn = t / rows;
+    tm = band * 8 + t % rows;
+}
+
 struct Plan {
     int few;             // the kernel for a few rows
     int edge;            // 256 x 256, 128 x 128 or 64 x 64 tiles; 0 and not few: no kernel's grid holds the product
