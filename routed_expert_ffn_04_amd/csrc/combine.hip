@@ -6,7 +6,7 @@
 // same page names as the lever from 3300 to 5000 tokens/s per GPU).
 // Only rows in [0, R) are read: an assignment whose dest lies outside has none here
 // and adds nothing.  The row numbers are the same in a whole workgroup, so the check is
-// scalar work.
+// scalar work: 16384 tokens of 8 bf16 rows of 7168 450 us against 447 without, e4m3 rows 274 either way.
 #include "common.h"
 #include "internal.h"
 

@@ -4,15 +4,16 @@
 //   dispatch            xs[dest[t k + j]] = x[t]
 //   its gradient        dx[t] = add[t] + sum_j dxs[dest[t k + j]]               (fp32, in this order)
 //   combine's gradient  dy[dest[t k + j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[dest[t k + j]]>
-// Memory-bound, no arithmetic to speak of.  Each runs over the tokens, so a token's row
-// is read once from HBM and every sorted row once (read or written): a kernel
-// that ran over the sorted rows instead would read the tokens' rows k times.
+// Memory-bound, no arithmetic to speak of.  Dispatch and its gradient run over the tokens, so
+// a token's row is read or written once, and every sorted row once.  Combine's gradient runs
+// over a token's assignments one after the other, a wave for each: it loads the token's row k
+// times, of which the caches answer all but the first.
 //
 // Sorted rows are met once, and there are many more of them than the caches hold, so
 // they go past the caches' usual order (NT) where a row is whole lines: dispatch of 16384
 // tokens to 8 of 7168 columns in bf16 437 -> 355 us for the same tokens again, which the caches
-// hold (5.9 TB/s written and read; 415 for others every time, 5.1), its gradient 420 -> 376.  Rows
-// of other lengths keep the usual one, which joins the pieces of a line (2056 columns:
+// hold; for others every time 415 to 419 by itself (5.1 TB/s written and read) and 442 in turn with its
+// gradient; the gradient 420 -> 376 (5.6).  Rows of other lengths keep the usual one, which joins the pieces of a line (2056 columns:
 // 45 us, against 63).  Row numbers that are the same in a whole wave are read
 // through the scalar cache: the gradient took 532 us with vector loads of them.
 #include <algorithm>

@@ -10,9 +10,10 @@
 // expert and tile by a prefix sum over the offsets, which its first wave-wide loads
 // bring: no list is made beforehand, and nothing about the rows has to reach the host.
 //
-// 16384 rows, 32 experts of 7168 x 2048, shares that differ, g and u in 8 bits: gate/up 989 us,
-// down 534, dh 526, dx 943 (0.9 to 1.0 PFLOP/s; rows that fill no tile and weights from HBM while
-// it multiplies), weight gradients 1633 (gemm_stream.h); a large product reaches 1.4.  Few rows,
+// 16384 rows, 32 experts of 7168 x 2048, shares that differ, g and u in 8 bits: gate/up 1001 us,
+// down 544, dh 535, dx 957 (0.9 to 1.0 PFLOP/s: experts' last tiles are 13 to 15 % more of a tile's time
+// than their rows need, and weights come from HBM meanwhile), weight gradients 1690
+// (gemm_stream.h); a large product reaches 1.4.  Few rows,
 // 64 experts of 2048 x 1408: the weights' bytes, 5.2 TB/s over the whole step.
 #include <algorithm>
 
