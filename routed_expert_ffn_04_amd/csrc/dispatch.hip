@@ -12,10 +12,11 @@
 // Sorted rows are met once, and there are many more of them than the caches hold, so
 // they go past the caches' usual order (NT) where a row is whole lines: dispatch of 16384
 // tokens to 8 of 7168 columns in bf16 437 -> 355 us for the same tokens again, which the caches
-// hold; for others every time 415 to 419 by itself (5.1 TB/s written and read) and 442 in turn with its
-// gradient; the gradient 420 -> 376 (5.6).  Rows of other lengths keep the usual one, which joins the pieces of a line (2056 columns:
-// 45 us, against 63).  Row numbers that are the same in a whole wave are read
-// through the scalar cache: the gradient took 532 us with vector loads of them.
+// hold; for others every time 415 to 419 by itself (5.1 TB/s written and read) and 442 in
+// turn with its gradient; the gradient 420 -> 376 (5.6).  Rows of other lengths keep the usual
+// one, which joins the pieces of a line (2056 columns: 45 us, against 63).  Row numbers that
+// are the same in a whole wave are read through the scalar cache: the gradient took 532 us with
+// vector loads of them.
 #include <algorithm>
 
 #include "dense.h"
